@@ -6,6 +6,7 @@ the library is missing this module raises on import -- there is no fallback.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -17,13 +18,18 @@ LIB_PATH = os.environ.get("GDP_LIBRARY") or os.path.join(_HERE, "libgdp.so")
 GDP_F32, GDP_BF16, GDP_I32, GDP_I64, GDP_F16 = 0, 1, 2, 3, 4
 GDP_OK, GDP_EINVAL, GDP_EUNSUPPORTED, GDP_EALIAS, GDP_EWORKSPACE, GDP_EHIP = 0, -1, -2, -3, -4, -5
 GDP_DBG_CU, GDP_DBG_SLOT, GDP_DBG_DUP = 1, 2, 4
+GDP_SCAN_CHECKPOINT_ROWS = 64
+ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "sigmoid": 2}  # gdp_activation
 STATUS_NAMES = {GDP_EINVAL: "GDP_EINVAL", GDP_EUNSUPPORTED: "GDP_EUNSUPPORTED", GDP_EALIAS: "GDP_EALIAS",
                 GDP_EWORKSPACE: "GDP_EWORKSPACE", GDP_EHIP: "GDP_EHIP"}
 
 EXPORTED = ("gdp_descriptor_capacity", "gdp_build_descriptors", "gdp_workspace_bytes",
             "gdp_chunk_prefill", "gdp_recurrent_decode", "gdp_fi_workspace_bytes",
             "gdp_chunk_gated_delta_product", "gdp_backward_workspace_bytes", "gdp_chunk_prefill_backward",
-            "gdp_debug_status", "gdp_last_error", "gdp_version", "gdp_chunk_prefill_noalloc")
+            "gdp_debug_status", "gdp_last_error", "gdp_version", "gdp_chunk_prefill_noalloc",
+            "gdp_gated_scan_workspace_bytes", "gdp_gated_scan", "gdp_gated_scan_decode",
+            "gdp_gated_scan_backward_workspace_bytes", "gdp_gated_scan_backward", "gdp_group_norm",
+            "gdp_group_norm_backward_workspace_bytes", "gdp_group_norm_backward")
 
 
 class gdp_tensor(ctypes.Structure):
@@ -85,6 +91,22 @@ def _load(path=LIB_PATH):
                                                ctypes.c_void_p]
     lib.gdp_debug_status.restype = ctypes.c_int
     lib.gdp_debug_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int32, ctypes.c_void_p]
+    # the recurrence's and the norm's tensors cross as packed gdp_tensor records (_pack)
+    P, i32, i64, size = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    for name in ("gdp_gated_scan_workspace_bytes", "gdp_gated_scan_backward_workspace_bytes",
+                 "gdp_group_norm_backward_workspace_bytes"):
+        getattr(lib, name).restype = size
+        getattr(lib, name).argtypes = [i64, i64, i64]
+    lib.gdp_gated_scan.restype = ctypes.c_int
+    lib.gdp_gated_scan.argtypes = [P, P, P, i32, P, i32, P, P, i32, P, P, P, P, size, P]
+    lib.gdp_gated_scan_decode.restype = ctypes.c_int
+    lib.gdp_gated_scan_decode.argtypes = [P, P, i32, P, P, P, P]
+    lib.gdp_gated_scan_backward.restype = ctypes.c_int
+    lib.gdp_gated_scan_backward.argtypes = [P, P, P, i32, P, P, P, P, P, P, P, P, size, P]
+    lib.gdp_group_norm.restype = ctypes.c_int
+    lib.gdp_group_norm.argtypes = [P, P, P, P, i32, i32, ctypes.c_float, P, P]
+    lib.gdp_group_norm_backward.restype = ctypes.c_int
+    lib.gdp_group_norm_backward.argtypes = [P, P, P, P, i32, i32, ctypes.c_float, P, P, P, P, P, P, size, P]
     lib.gdp_last_error.restype = ctypes.c_char_p
     lib.gdp_last_error.argtypes = []
     lib.gdp_version.restype = ctypes.c_char_p
@@ -126,6 +148,39 @@ def _check(rc):
 
 def _stream(device):
     return torch.cuda.current_stream(device).cuda_stream
+
+
+_RECORD = struct.Struct("@Pii8q")  # the layout of gdp_tensor
+
+
+def _pack(t, device):
+    """The gdp_tensor record of a torch tensor as bytes (None -> absent): a third of the time of
+    as_gdp_tensor, which counts in a call of a few microseconds.  Refuses a tensor elsewhere than on
+    `device`."""
+    if t is None:
+        return None
+    if t.device != device:
+        raise ValueError(f"expected a tensor on {device}, got one on {t.device}")
+    code = _DT.get(t.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    n = t.dim()
+    if n > 4:
+        raise ValueError("at most 4 dims")
+    pad = (0,) * (4 - n)
+    # an empty tensor is still "present": a non-null dummy address
+    return _RECORD.pack(t.data_ptr() or 16, code, n, *t.shape, *pad, *t.stride(), *pad)
+
+
+def _on(device):
+    """Whether a call on `device` can launch as it is; raises for tensors that are not on a GPU."""
+    if device.type != "cuda":
+        raise ValueError(f"expected tensors on a GPU, got {device}")
+    return device.index == torch.cuda.current_device()
+
+
+def _workspace(nbytes, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 # ---------------------------------------------------------------- C ABI names
@@ -302,6 +357,81 @@ def gdp_chunk_prefill_backward(q, k, v, g_log, beta, num_householder, cu_seqlens
                                           *[ctypes.byref(a) for a in dts], ws_ptr, ws_bytes, st))
 
 
+def gdp_gated_scan_workspace_bytes(T, N, D):
+    return int(LIB.gdp_gated_scan_workspace_bytes(T, N, D))
+
+
+def gdp_gated_scan_backward_workspace_bytes(T, N, D):
+    return int(LIB.gdp_gated_scan_backward_workspace_bytes(T, N, D))
+
+
+def gdp_group_norm_backward_workspace_bytes(T, G, V):
+    return int(LIB.gdp_group_norm_backward_workspace_bytes(T, G, V))
+
+
+def _call(device, entry, *args, workspace=(), stream=None):
+    """Calls a C entry point with its workspace and the stream to launch on (by default the current one
+    of `device`, which is made the current device for the call)."""
+    if workspace is None:
+        workspace = (None, 0)
+    elif len(workspace):
+        workspace = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if _on(device):
+        _check(entry(*args, *workspace, _stream(device) if stream is None else stream))
+    else:
+        with torch.cuda.device(device):
+            _check(entry(*args, *workspace, _stream(device) if stream is None else stream))
+
+
+def gdp_gated_scan(x, g_log, cu_seqlens, complement_input, initial_state, output_final_state, state_cache,
+                   state_indices, return_checkpoints, o, final_state, checkpoints, workspace, stream=None):
+    """Direct call of the C entry point (caller-allocated outputs and workspace)."""
+    dev = x.device
+    _call(dev, LIB.gdp_gated_scan, _pack(x, dev), _pack(g_log, dev), _pack(cu_seqlens, dev),
+          int(bool(complement_input)), _pack(initial_state, dev), int(bool(output_final_state)),
+          _pack(state_cache, dev), _pack(state_indices, dev), int(bool(return_checkpoints)), _pack(o, dev),
+          _pack(final_state, dev), _pack(checkpoints, dev), workspace=workspace, stream=stream)
+
+
+def gdp_gated_scan_decode(x, g_log, complement_input, state_cache, state_indices, o, stream=None):
+    """Direct call of the C entry point; o is caller-allocated, state_cache is updated in place."""
+    dev = x.device
+    _call(dev, LIB.gdp_gated_scan_decode, _pack(x, dev), _pack(g_log, dev), int(bool(complement_input)),
+          _pack(state_cache, dev), _pack(state_indices, dev), _pack(o, dev), stream=stream)
+
+
+def gdp_gated_scan_backward(x, g_log, cu_seqlens, complement_input, initial_state, checkpoints, d_o, d_final_state,
+                            dx, dg_log, d_initial_state, workspace, stream=None):
+    """Direct call of the C entry point (caller-allocated gradients and workspace)."""
+    dev = x.device
+    _call(dev, LIB.gdp_gated_scan_backward, _pack(x, dev), _pack(g_log, dev), _pack(cu_seqlens, dev),
+          int(bool(complement_input)), _pack(initial_state, dev), _pack(checkpoints, dev), _pack(d_o, dev),
+          _pack(d_final_state, dev), _pack(dx, dev), _pack(dg_log, dev), _pack(d_initial_state, dev),
+          workspace=workspace, stream=stream)
+
+
+def gdp_group_norm(x, weight, bias, gate, activation, subtract_mean, eps, y, stream=None):
+    """Direct call of the C entry point; `activation` is a key of ACTIVATIONS, y is caller-allocated."""
+    dev = x.device
+    _call(dev, LIB.gdp_group_norm, _pack(x, dev), _pack(weight, dev), _pack(bias, dev), _pack(gate, dev),
+          _activation(activation), int(bool(subtract_mean)), float(eps), _pack(y, dev), stream=stream)
+
+
+def gdp_group_norm_backward(x, weight, bias, gate, activation, subtract_mean, eps, d_y, dx, dweight, dbias, dgate,
+                            workspace, stream=None):
+    """Direct call of the C entry point (caller-allocated gradients and workspace)."""
+    dev = x.device
+    _call(dev, LIB.gdp_group_norm_backward, _pack(x, dev), _pack(weight, dev), _pack(bias, dev), _pack(gate, dev),
+          _activation(activation), int(bool(subtract_mean)), float(eps), _pack(d_y, dev), _pack(dx, dev),
+          _pack(dweight, dev), _pack(dbias, dev), _pack(dgate, dev), workspace=workspace, stream=stream)
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(k for k in ACTIVATIONS if k)} or None, got {name!r}")
+    return ACTIVATIONS[name]
+
+
 # ---------------------------------------------------------------- convenience wrapper
 
 def chunk_prefill(q, k, v, g_log, beta, num_householder, cu_seqlens, scale=None, initial_state=None,
@@ -397,3 +527,70 @@ def chunk_prefill_backward(q, k, v, g_log, beta, num_householder, cu_seqlens, d_
     gdp_chunk_prefill_backward(q, k, v, g_log, beta, n, cu_seqlens, scale, initial_state, use_qk_l2norm, d_o,
                                d_final_state, dq, dk, dv, dg, db, ds0, ws)
     return {"dq": dq, "dk": dk, "dv": dv, "dg_log": dg, "dbeta": db, "d_initial_state": ds0}
+
+
+def gated_scan(x, g_log, cu_seqlens, initial_state=None, output_final_state=False, complement_input=False,
+               state_cache=None, state_indices=None, return_checkpoints=False, out=None):
+    """Allocating front end of the gated linear recurrence h_t = exp(g_log_t) h_{t-1} + u_t over packed
+    sequences (x, g_log [T, D]; u = x, or (1 - exp(g_log)) x with complement_input).  Returns
+    (o, final_state or None) or, with return_checkpoints, (o, final_state or None, checkpoints), which
+    gated_scan_backward takes.  Rows that no sequence covers are left as they are in `out`."""
+    T, D = x.shape
+    N = cu_seqlens.shape[0] - 1
+    dev = x.device
+    o = out if out is not None else torch.empty((T, D), dtype=x.dtype, device=dev)
+    fs = torch.empty((N, D), dtype=torch.float32, device=dev) if output_final_state else None
+    cp = None
+    if return_checkpoints:
+        cp = torch.empty((-(-T // GDP_SCAN_CHECKPOINT_ROWS), D), dtype=torch.float32, device=dev)
+    gdp_gated_scan(x, g_log, cu_seqlens, complement_input, initial_state, output_final_state, state_cache,
+                   state_indices, return_checkpoints, o, fs, cp,
+                   _workspace(gdp_gated_scan_workspace_bytes(T, N, D), dev))
+    return (o, fs, cp) if return_checkpoints else (o, fs)
+
+
+def gated_scan_decode(x, g_log, state_cache, state_indices, complement_input=False, out=None):
+    """Allocating front end of the recurrence's single-token step: returns o [N, D] in x's dtype; the
+    state cache [S, D] is updated in place."""
+    o = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    gdp_gated_scan_decode(x, g_log, complement_input, state_cache, state_indices, o)
+    return o
+
+
+def gated_scan_backward(x, g_log, cu_seqlens, d_o, d_final_state=None, initial_state=None, complement_input=False,
+                        checkpoints=None, grads_like_inputs=False):
+    """Allocating front end of the recurrence's gradients: returns a dict of dx, dg_log (float32, or the
+    dtypes of x and g_log with grads_like_inputs) and d_initial_state (float32; None without an initial
+    state).  Without the forward call's `checkpoints` the states are formed again first."""
+    T, D = x.shape
+    N = cu_seqlens.shape[0] - 1
+    dev = x.device
+    dx = torch.empty((T, D), dtype=x.dtype if grads_like_inputs else torch.float32, device=dev)
+    dg = torch.empty((T, D), dtype=g_log.dtype if grads_like_inputs else torch.float32, device=dev)
+    ds0 = torch.empty((N, D), dtype=torch.float32, device=dev) if initial_state is not None else None
+    gdp_gated_scan_backward(x, g_log, cu_seqlens, complement_input, initial_state, checkpoints, d_o, d_final_state,
+                            dx, dg, ds0, _workspace(gdp_gated_scan_backward_workspace_bytes(T, N, D), dev))
+    return {"dx": dx, "dg_log": dg, "d_initial_state": ds0}
+
+
+def group_norm(x, weight=None, bias=None, gate=None, activation=None, subtract_mean=True, eps=1e-5, out=None):
+    """Allocating front end of the group norm over the last dimension of x [T, G, V] (the heads' outputs,
+    channels last): act(n) without a gate, n * act(gate) with one; weight and bias [V] or [G, V];
+    activation None, "silu" or "sigmoid"; subtract_mean=False is the root mean square norm."""
+    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    gdp_group_norm(x, weight, bias, gate, activation, subtract_mean, eps, y)
+    return y
+
+
+def group_norm_backward(x, d_y, weight=None, bias=None, gate=None, activation=None, subtract_mean=True, eps=1e-5):
+    """Allocating front end of the group norm's gradients: returns a dict of dx and dgate (x's dtype) and
+    dweight and dbias (float32), None where the forward call had none.  dx is what the recurrences'
+    backward calls take as d_o."""
+    T, G, V = x.shape
+    dev = x.device
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dz = torch.empty(x.shape, dtype=x.dtype, device=dev) if gate is not None else None
+    dw, db = (None if p is None else torch.empty(p.shape, dtype=torch.float32, device=dev) for p in (weight, bias))
+    gdp_group_norm_backward(x, weight, bias, gate, activation, subtract_mean, eps, d_y, dx, dw, db, dz,
+                            _workspace(gdp_group_norm_backward_workspace_bytes(T, G, V), dev))
+    return {"dx": dx, "dweight": dw, "dbias": db, "dgate": dz}

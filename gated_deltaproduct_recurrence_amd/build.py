@@ -13,6 +13,8 @@ SOURCES = [os.path.join(CSRC, "gdp_kernels.hip"), os.path.join(CSRC, "gdp_decode
            os.path.join(CSRC, "gdp_backward.hip"), os.path.join(CSRC, "gdp_bwd_chunk.hip"),
            os.path.join(CSRC, "gdp_validate.hip"),
            os.path.join(CSRC, "gdp_noalloc.hip"),
+           os.path.join(CSRC, "gdp_scan.hip"), os.path.join(CSRC, "gdp_norm.hip"),
+           os.path.join(CSRC, "gdp_layer_api.cpp"),
            os.path.join(CSRC, "gdp_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

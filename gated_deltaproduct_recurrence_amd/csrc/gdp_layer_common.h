@@ -1,0 +1,44 @@
+// gdp_layer_common.h -- device helpers shared by the recurrence (gdp_scan.hip)
+// and the norm (gdp_norm.hip).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gdp {
+
+typedef __bf16 bf16;
+
+__device__ __forceinline__ int64_t index_at(const void *p, int is64, int64_t i) {
+  return is64 ? ((const int64_t *)p)[i] : (int64_t)((const int32_t *)p)[i];
+}
+
+// cu_seqlens[i] clamped to [0, T]
+__device__ __forceinline__ int64_t bound_at(const void *cu, int is64, int64_t i, int64_t T) {
+  const int64_t v = index_at(cu, is64, i);
+  return v < 0 ? 0 : (v > T ? T : v);
+}
+
+constexpr float LOG2E_L = 1.4426950408889634f;
+
+// exp(g) by the hardware's base-2 exponential (1 ulp; its result below 2^-126 is
+// 0, that of -inf is 0).  The product's rounding adds |g| 2^-24 relative, which
+// is below an ulp of the result's effect on a state while |g| < 1 and concerns
+// decays below 0.4 otherwise.
+__device__ __forceinline__ float decay(float g) { return __builtin_amdgcn_exp2f(g * LOG2E_L); }
+
+// 1 - exp(g): the Taylor polynomial of degree 8 for |g| < 1/2 (its first omitted
+// term is g^9 / 9!, below 2^-26 of the result there), else the difference, whose
+// rounding is 2^-25 of a value above 0.39.  `a` is decay(g).
+__device__ __forceinline__ float one_minus_decay(float g, float a) {
+  float p = 1.f / 40320.f;
+  p = fmaf(p, g, 1.f / 5040.f);
+  p = fmaf(p, g, 1.f / 720.f);
+  p = fmaf(p, g, 1.f / 120.f);
+  p = fmaf(p, g, 1.f / 24.f);
+  p = fmaf(p, g, 1.f / 6.f);
+  p = fmaf(p, g, 0.5f);
+  p = fmaf(p, g * g, g);
+  return fabsf(g) < 0.5f ? -p : 1.f - a;
+}
+
+}  // namespace gdp

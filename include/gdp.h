@@ -334,12 +334,146 @@ int gdp_chunk_gated_delta_product(const gdp_tensor *q, const gdp_tensor *k, cons
                                   const gdp_tensor *output, const gdp_tensor *output_state, void *workspace,
                                   size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Layers around the matrix-state recurrence: a per-channel (vector-state) gated
+ * linear recurrence, and the group norm that follows either recurrence's
+ * outputs.  The conventions above hold here too.
+ * ------------------------------------------------------------------------ */
+
+/* Rows of the token stream per recurrence checkpoint. */
+#define GDP_SCAN_CHECKPOINT_ROWS 64
+
+/* Host-only.  Workspace bytes gdp_gated_scan needs for T rows, N sequences and D
+ * channels: a ticket counter and, per 64 rows and channel, one 8-byte word through
+ * which the workgroups of a long sequence hand their states on.  The call writes
+ * it before use and leaves nothing in it that a later call reads.  Returns 0 for
+ * invalid sizes. */
+size_t gdp_gated_scan_workspace_bytes(int64_t T, int64_t N, int64_t D);
+
+/* Device.  The gated linear recurrence over packed sequences.  For every sequence
+ * and channel d, from h = initial_state (or 0), per token t:
+ *     h_t = a_t h_{t-1} + u_t,   a_t = exp(g_log[t, d]),   o[t, d] = h_t,
+ *     u_t = x[t, d], or (1 - a_t) x[t, d] with complement_input.
+ *   x            [T, D]    f32, bf16 or f16; rows may be strided
+ *   g_log        [T, D]    f32 or x's dtype; log decays, g_log <= 0 (a positive
+ *                          entry is served while the products of decays over 64
+ *                          rows stay finite in float32); -inf restarts the channel
+ *   cu_seqlens   [N+1]     int32 or int64, contiguous
+ *   initial_state [N, D]   f32 contiguous, or data == NULL for zeros
+ *   output_final_state     write final_state when nonzero
+ *   state_cache  [S, D]    f32 contiguous, or NULL; when given, the final state of
+ *                          sequence i is written at slot state_indices[i]; an index
+ *                          outside [0, S) writes nothing
+ *   state_indices [N]      int32 or int64; required with state_cache
+ *   return_checkpoints     write checkpoints when nonzero
+ *   o            [T, D]    x's dtype, rows may be strided; the rows no sequence
+ *                          covers are left as they are
+ *   final_state  [N, D]    f32 contiguous; required iff output_final_state; of an
+ *                          empty sequence its initial state
+ *   checkpoints  [ceil(T / 64), D]  f32 contiguous: row c is the state entering
+ *                          token row 64 c where that row continues a sequence, and
+ *                          unspecified elsewhere; what gdp_gated_scan_backward reads
+ *   workspace    at least gdp_gated_scan_workspace_bytes(...), 256-byte aligned
+ * States are held in float32.  A non-finite x stays within its sequence and
+ * channel.  No output may overlap an input or another output (GDP_EALIAS).
+ * Calls that share a workspace must be ordered.  Two runs on the same inputs give
+ * the same bits.  One or two launches on `stream`, no allocation: capturable. */
+int gdp_gated_scan(const gdp_tensor *x, const gdp_tensor *g_log, const gdp_tensor *cu_seqlens,
+                   int32_t complement_input, const gdp_tensor *initial_state, int32_t output_final_state,
+                   const gdp_tensor *state_cache, const gdp_tensor *state_indices, int32_t return_checkpoints,
+                   const gdp_tensor *o, const gdp_tensor *final_state, const gdp_tensor *checkpoints,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* Device.  One token of the recurrence per entry, on the state cache in place:
+ * for slot = state_indices[i] in [0, S),
+ *     state_cache[slot] = a_i state_cache[slot] + u_i,   o[i] = state_cache[slot];
+ * the other entries (padding, -1) get a zero output row and touch no state.
+ *   x, g_log, o [N, D] as for gdp_gated_scan, state_cache [S, D] f32 contiguous,
+ *   state_indices [N] int32 or int64.  Two entries naming one slot race (caller
+ *   error).  One launch on `stream`; capturable. */
+int gdp_gated_scan_decode(const gdp_tensor *x, const gdp_tensor *g_log, int32_t complement_input,
+                          const gdp_tensor *state_cache, const gdp_tensor *state_indices, const gdp_tensor *o,
+                          void *stream);
+
+/* Host-only.  Workspace bytes gdp_gated_scan_backward needs (the forward scan's
+ * words and, for calls without checkpoints, room for them).  0 for invalid sizes. */
+size_t gdp_gated_scan_backward_workspace_bytes(int64_t T, int64_t N, int64_t D);
+
+/* Device.  Gradients of gdp_gated_scan.  With L = <o, d_o> + <final_state,
+ * d_final_state> and e_t the gradient of the state after token t (walking back from
+ * d_final_state, or 0):
+ *     e_t = d_o_t + a_{t+1} e_{t+1},   dx_t = e_t  or  (1 - a_t) e_t,
+ *     dg_log_t = e_t a_t (h_{t-1}  or  h_{t-1} - x_t),   d_initial_state = a_0 e_0.
+ *   x, g_log, cu_seqlens, complement_input, initial_state  the forward call's
+ *   checkpoints  those of the forward call, or data == NULL: the states are then
+ *                formed again first (x and g_log are read a second time)
+ *   d_o          [T, D]  x's dtype, rows may be strided
+ *   d_final_state [N, D] f32 contiguous, or data == NULL for zeros
+ *   dx           [T, D]  float32 or x's dtype, rows may be strided
+ *   dg_log       [T, D]  float32 or g_log's dtype, rows may be strided; the rows of dx
+ *                        and dg_log that no sequence covers are written as zeros
+ *   d_initial_state [N, D] f32 contiguous, or data == NULL; of an empty sequence its
+ *                        d_final_state
+ *   workspace    at least gdp_gated_scan_backward_workspace_bytes(...), 256-byte aligned
+ * No gradient may overlap an input or another gradient (GDP_EALIAS).  No allocation,
+ * everything on `stream`: capturable. */
+int gdp_gated_scan_backward(const gdp_tensor *x, const gdp_tensor *g_log, const gdp_tensor *cu_seqlens,
+                            int32_t complement_input, const gdp_tensor *initial_state,
+                            const gdp_tensor *checkpoints, const gdp_tensor *d_o,
+                            const gdp_tensor *d_final_state, const gdp_tensor *dx, const gdp_tensor *dg_log,
+                            const gdp_tensor *d_initial_state, void *workspace, size_t workspace_bytes,
+                            void *stream);
+
+/* Activations of gdp_group_norm. */
+enum gdp_activation { GDP_ACT_NONE = 0, GDP_ACT_SILU = 1, GDP_ACT_SIGMOID = 2 };
+
+/* Device.  Group norm with an activation over the channels of each token, channels
+ * last: the G groups of V channels are the heads of a recurrence's output [T, Hv, V].
+ * For every token t and group:
+ *     n = (x - mean) rstd weight + bias,   rstd = 1 / sqrt(mean((x - mean)^2) + eps),
+ *     y = act(n) without a gate,   y = n act(gate) with one;
+ * mean is the mean over the group's V channels, or 0 with subtract_mean == 0 (root
+ * mean square norm).
+ *   x            [T, G, V]  f32, bf16 or f16; tokens and groups may be strided
+ *   weight       [V] (one for all groups) or [G, V], f32 or x's dtype, contiguous, or
+ *                data == NULL for ones
+ *   bias         as weight, or data == NULL for zeros; with a weight its shape and dtype
+ *   gate         [T, G, V]  x's dtype, may be strided, or data == NULL
+ *   activation   a gdp_activation
+ *   eps          > 0
+ *   y            [T, G, V]  x's dtype, may be strided
+ * Statistics and products are float32; y is rounded once.  y may not overlap an input
+ * (GDP_EALIAS).  V <= 16384 (GDP_EUNSUPPORTED otherwise).  One launch on `stream`;
+ * capturable. */
+int gdp_group_norm(const gdp_tensor *x, const gdp_tensor *weight, const gdp_tensor *bias, const gdp_tensor *gate,
+                   int32_t activation, int32_t subtract_mean, float eps, const gdp_tensor *y, void *stream);
+
+/* Host-only.  Workspace bytes gdp_group_norm_backward needs: partial sums of the
+ * weight and bias gradients.  0 for invalid sizes. */
+size_t gdp_group_norm_backward_workspace_bytes(int64_t T, int64_t G, int64_t V);
+
+/* Device.  Gradients of gdp_group_norm (the same x, weight, bias, gate, activation,
+ * subtract_mean and eps) for d_y [T, G, V] of x's dtype:
+ *   dx, dgate    [T, G, V]  x's dtype, may be strided; dgate required iff a gate is given
+ *   dweight, dbias          f32, contiguous, the shape of weight and bias; required iff
+ *                           weight, respectively bias, is given: summed over the tokens
+ *                           (and the groups that share them) in a fixed order
+ *   workspace    at least gdp_group_norm_backward_workspace_bytes(...), 256-byte aligned
+ * The statistics are formed again from x.  No gradient may overlap an input or another
+ * gradient (GDP_EALIAS).  Everything on `stream`, no allocation: capturable. */
+int gdp_group_norm_backward(const gdp_tensor *x, const gdp_tensor *weight, const gdp_tensor *bias,
+                            const gdp_tensor *gate, int32_t activation, int32_t subtract_mean, float eps,
+                            const gdp_tensor *d_y, const gdp_tensor *dx, const gdp_tensor *dweight,
+                            const gdp_tensor *dbias, const gdp_tensor *dgate, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 /* Debug validation of the data-dependent arguments.  These are not checked by
  * default, because checking them needs a read of device data.  A bad value stays
  * in bounds (every kernel clamps sequence ranges to [0, T] and skips slots
  * outside the cache), but the results are then undefined.  With the environment
- * variable GDP_DEBUG_VALIDATE=1, gdp_chunk_prefill (and the entries built on it)
- * and gdp_recurrent_decode first launch a check on their stream.  The check ORs
+ * variable GDP_DEBUG_VALIDATE=1, gdp_chunk_prefill (and the entries built on it),
+ * gdp_recurrent_decode, gdp_gated_scan and gdp_gated_scan_decode first launch a
+ * check on their stream.  The check ORs
  * these bits into a word kept per device:
  *   GDP_DBG_CU    cu_seqlens decreases somewhere, or an entry lies outside [0, T]
  *                 (Megatron Core page, chunk_gated_delta_product_varlen: the
