@@ -1,7 +1,35 @@
 // gdp_scan.hip -- gfx950 kernels of the gated linear recurrence
 //     h_t = a_t h_{t-1} + u_t,  a_t = exp(g_t),  u_t = x_t or (1 - a_t) x_t
-// per channel over packed sequences, of its single-token step, and of its
-// gradients.  One lane per (sequence, channel) walks the sequence's rows.
+// per channel over packed sequences, of its gradients, and of its single-token
+// step.
+//
+// The recurrence is a composition of affine maps h -> A h + B, so a block of rows
+// can be reduced to one pair (A, B) per channel before the state that enters it is
+// known.  The token stream (all sequences end to end) is cut into tiles of 64 rows;
+// a workgroup of 8 waves takes one tile of one channel block, wave w rows 8 w ..
+// 8 w + 7, a lane VEC neighbouring channels.  Every input is loaded once into
+// registers and every output written once:
+//   1. the rows' decays and terms, and their maps composed: per wave, then (through
+//      LDS) per tile;
+//   2. the tile's pair is published in an 8-byte word per channel, and the state
+//      entering the tile is formed from the words of the tiles before it (below);
+//   3. the rows again from the entering state, out of registers, to the outputs.
+// A sequence that starts inside a tile cuts the chain there: its first row takes
+// initial_state in place of the state before it, and the map's A is 0.
+//
+// Handing on the states.  A word holds (A, B) of one tile; a tile that knows its
+// entering state h, or needs none, holds (0, A h + B) instead: A = 0 says that
+// nothing before the tile matters.  A workgroup reads the words of the WIN tiles
+// before its own until for every channel it has found one with A = 0 and all those
+// between, and composes them from that one forward.  That is the sequential fold,
+// whichever tile the fold starts from, so the result does not depend on timing.
+// The words are written and read with relaxed agent-scope atomics (8 bytes, so a
+// pair is whole), which go past the XCDs' own caches; all-ones bits (two NaNs that
+// no published pair has) mean not yet written, and a fill kernel sets them before.
+// Tiles are handed out by an atomic counter, rows ascending, so a workgroup waits
+// only for tiles whose workgroups are running, and those publish their pairs before
+// they wait themselves: the first of the waiting tiles finds its predecessor's word
+// at A = 0, so every wait ends.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -12,69 +40,442 @@
 namespace gdp {
 namespace {
 
-template <typename XT, typename GT>
-__global__ void __launch_bounds__(64) gdp_scan_kernel(ScanArgs a) {
-  const int64_t i = blockIdx.x, ch = (int64_t)blockIdx.y * 64 + threadIdx.x;
-  if (ch >= a.D) return;
-  const int64_t lo = bound_at(a.cu, a.cu_is64, i, a.T), hi = bound_at(a.cu, a.cu_is64, i + 1, a.T);
-  float h = a.s0 ? a.s0[i * a.D + ch] : 0.f;
-  for (int64_t t = lo; t < hi; ++t) {
-    if (a.checkpoints && t % SCAN_ROWS == 0) a.checkpoints[t / SCAN_ROWS * a.D + ch] = h;
-    const float g = (float)((const GT *)a.g)[t * a.g_st + ch], x = (float)((const XT *)a.x)[t * a.x_st + ch];
-    const float d = decay(g);
-    h = fmaf(d, h, a.complement ? one_minus_decay(g, d) * x : x);
-    if (a.o) ((XT *)a.o)[t * a.o_st + ch] = (XT)h;
+constexpr int WAVES = 8, R = SCAN_ROWS / WAVES, THREADS = 64 * WAVES;
+constexpr uint64_t NOT_WRITTEN = ~0ull;
+
+template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Pack { T v[VEC]; };
+
+template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> load_pack(const T *p) {
+  return *(const Pack<T, VEC> *)p;
+}
+template <typename T, int VEC> __device__ __forceinline__ void store_pack(T *p, const float (&x)[VEC]) {
+  Pack<T, VEC> s;
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) s.v[c] = (T)x[c];
+  *(Pack<T, VEC> *)p = s;
+}
+
+// the map (A, B) applied to h; A = 0 drops h, also one that is not finite
+__device__ __forceinline__ float apply(float A, float h, float B) { return A == 0.f ? B : fmaf(A, h, B); }
+
+__device__ __forceinline__ uint64_t make_word(float A, float B) {
+  const uint32_t a = A != A ? 0x7fc00000u : __float_as_uint(A);  // a NaN that is not NOT_WRITTEN's
+  return ((uint64_t)a << 32) | __float_as_uint(B);
+}
+
+template <int VEC> struct Shared {
+  static constexpr int NCH = 64 * VEC, PARTS = THREADS / NCH;
+  static constexpr int Q = VEC == 4 ? 8 : 4;  // words a thread reads per round
+  static constexpr int WIN = PARTS * Q;       // tiles before this one that a round looks at
+  float A[WAVES][NCH], B[WAVES][NCH];
+  uint64_t win[WIN][NCH];
+  int start_id[SCAN_ROWS], end_id[SCAN_ROWS];  // sequence that starts / ends at a row of the tile, or -1
+  int ticket;
+};
+
+// Marks the tile's rows [r0, r0 + 64) where sequences start and end (nonempty
+// ones), in LDS and as two masks.  Boundaries are read 512 at a time; with more
+// sequences, the one that holds r0 is found first in 512-way steps.  Bad contents
+// give wrong marks, with ids in [0, N).
+struct Marks { uint64_t start, end; };
+template <typename S> __device__ __forceinline__ Marks mark_rows(S &sh, const ScanArgs &a, int64_t r0, int tid) {
+  int64_t lo = 0, hi = a.N;
+  while (hi - lo > THREADS) {  // the last sequence that starts at or before r0
+    const int64_t step = (hi - lo + THREADS - 1) / THREADS, i = lo + tid * step;
+    const int c = __syncthreads_count(i < hi && bound_at(a.cu, a.cu_is64, i, a.T) <= r0);
+    if (c == 0) {
+      hi = lo + 1;
+    } else {
+      lo += (c - 1) * step;
+      hi = hi < lo + step ? hi : lo + step;
+    }
   }
-  if (a.final_state) a.final_state[i * a.D + ch] = h;
-  if (a.cache) {
-    const int64_t slot = index_at(a.slots, a.slots_is64, i);
-    if (slot >= 0 && slot < a.num_slots) a.cache[slot * a.D + ch] = h;
+  for (int64_t base = lo; base < a.N; base += THREADS) {
+    const int64_t i = base + tid;
+    bool past = true;
+    if (i < a.N) {
+      const int64_t s = bound_at(a.cu, a.cu_is64, i, a.T) - r0, e = bound_at(a.cu, a.cu_is64, i + 1, a.T) - r0 - 1;
+      if (e >= s) {
+        if (s >= 0 && s < SCAN_ROWS) sh.start_id[s] = (int)i;
+        if (e >= 0 && e < SCAN_ROWS) sh.end_id[e] = (int)i;
+      }
+      past = s >= SCAN_ROWS;
+    }
+    if (__syncthreads_or(past)) break;
+  }
+  return Marks{__ballot(sh.start_id[tid & 63] >= 0), __ballot(sh.end_id[tid & 63] >= 0)};
+}
+
+// The state entering this tile (per channel, in threads tid < NCH) from the words
+// of the `count` tiles before it; `word(i)` is the address of the i-th before it.
+template <int VEC, typename F>
+__device__ __forceinline__ float entering(Shared<VEC> &sh, int64_t count, bool live, int tid, F word) {
+  using S = Shared<VEC>;
+  const int part = tid / S::NCH, c = tid % S::NCH;
+  float h = 0.f;
+  for (;;) {
+    uint64_t w[S::Q];
+#pragma unroll
+    for (int q = 0; q < S::Q; ++q) {
+      const int i = part * S::Q + q;
+      w[q] = live && i < count ? __hip_atomic_load(word(i), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+    }
+#pragma unroll
+    for (int q = 0; q < S::Q; ++q) sh.win[part * S::Q + q][c] = w[q];
+    __syncthreads();
+    bool found = true;
+    if (tid < S::NCH) {
+      int n = 0;
+      found = false;
+      for (; n < S::WIN; ++n) {
+        const uint64_t v = sh.win[n][c];
+        if (v == NOT_WRITTEN) break;
+        if (__uint_as_float((uint32_t)(v >> 32)) == 0.f) {
+          found = true;
+          break;
+        }
+      }
+      if (found) {
+        h = __uint_as_float((uint32_t)sh.win[n][c]);
+        while (--n >= 0) {
+          const uint64_t v = sh.win[n][c];
+          h = fmaf(__uint_as_float((uint32_t)(v >> 32)), h, __uint_as_float((uint32_t)v));
+        }
+      }
+    }
+    if (__syncthreads_and(found)) return h;
+    __builtin_amdgcn_s_sleep(1);
   }
 }
 
-// The rows before the first sequence and behind the last one (i = N) get zeros.
-template <typename XT, typename GT>
-__global__ void __launch_bounds__(64) gdp_scan_backward_kernel(ScanArgs a) {
-  const int64_t i = blockIdx.x, ch = (int64_t)blockIdx.y * 64 + threadIdx.x;
-  if (ch >= a.D) return;
-  auto put = [&](int64_t t, float dx, float dg) {
-    if (a.dx_f32) ((float *)a.dx)[t * a.dx_st + ch] = dx; else ((XT *)a.dx)[t * a.dx_st + ch] = (XT)dx;
-    if (a.dg_f32) ((float *)a.dg)[t * a.dg_st + ch] = dg; else ((GT *)a.dg)[t * a.dg_st + ch] = (GT)dg;
-  };
-  if (i == a.N) {
-    const int64_t first = bound_at(a.cu, a.cu_is64, 0, a.T), last = bound_at(a.cu, a.cu_is64, a.N, a.T);
-    for (int64_t t = 0; t < first; ++t) put(t, 0.f, 0.f);
-    for (int64_t t = last; t < a.T; ++t) put(t, 0.f, 0.f);
+// The workgroup's job: its ticket (the counter starts at -1), or the block's own
+// index when nothing is handed on.  Clears the row marks.
+template <typename S> __device__ __forceinline__ int take_ticket(S &sh, const ScanArgs &a, bool hand_on, int tid) {
+  if (tid < SCAN_ROWS) sh.start_id[tid] = sh.end_id[tid] = -1;
+  if (!hand_on) {
+    __syncthreads();
+    return (int)blockIdx.x;
+  }
+  if (tid == 0) sh.ticket = atomicAdd((int *)a.ws, 1) + 1;
+  __syncthreads();
+  return sh.ticket;
+}
+
+// The jobs behind the tiles: 64 sequences each, whose empty ones hand src (or
+// zeros) to dst (and to the state cache).
+__device__ __forceinline__ void empty_sequences(const ScanArgs &a, int64_t job, const float *src, float *dst, int tid) {
+  for (int64_t i = job * 64; i < (job + 1) * 64 && i < a.N; ++i) {
+    if (bound_at(a.cu, a.cu_is64, i + 1, a.T) > bound_at(a.cu, a.cu_is64, i, a.T)) continue;
+    int64_t slot = -1;
+    if (a.cache) {
+      slot = index_at(a.slots, a.slots_is64, i);
+      if (slot >= a.num_slots) slot = -1;
+    }
+    for (int64_t ch = tid; ch < a.D; ch += THREADS) {
+      const float h = src ? src[i * a.D + ch] : 0.f;
+      if (dst) dst[i * a.D + ch] = h;
+      if (slot >= 0) a.cache[slot * a.D + ch] = h;
+    }
+  }
+}
+
+template <typename XT, typename GT, int VEC, bool COMPL>
+__global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int tiles, int blocks) {
+  using S = Shared<VEC>;
+  __shared__ S sh;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const bool hand_on = tiles > 1;
+  const int ticket = take_ticket(sh, a, hand_on, tid);
+  const int tile = __builtin_amdgcn_readfirstlane(ticket / blocks);
+  if (tile >= tiles) {
+    empty_sequences(a, ticket - tiles * blocks, a.s0, a.final_state, tid);
     return;
   }
-  const int64_t lo = bound_at(a.cu, a.cu_is64, i, a.T), hi = bound_at(a.cu, a.cu_is64, i + 1, a.T);
-  float e = a.dfinal ? a.dfinal[i * a.D + ch] : 0.f;
-  float before[SCAN_ROWS];
-  for (int64_t end = hi; end > lo;) {
-    int64_t begin = (end - 1) / SCAN_ROWS * SCAN_ROWS;
-    float h;
-    if (begin <= lo) {
-      begin = lo;
-      h = a.s0 ? a.s0[i * a.D + ch] : 0.f;
-    } else {
-      h = a.checkpoints[begin / SCAN_ROWS * a.D + ch];
-    }
-    for (int64_t t = begin; t < end; ++t) {
-      const float g = (float)((const GT *)a.g)[t * a.g_st + ch], x = (float)((const XT *)a.x)[t * a.x_st + ch];
-      const float d = decay(g);
-      before[t - begin] = h;
-      h = fmaf(d, h, a.complement ? one_minus_decay(g, d) * x : x);
-    }
-    for (int64_t t = end - 1; t >= begin; --t) {
-      const float g = (float)((const GT *)a.g)[t * a.g_st + ch], x = (float)((const XT *)a.x)[t * a.x_st + ch];
-      const float d = decay(g), p = before[t - begin];
-      e += (float)((const XT *)a.dout)[t * a.do_st + ch];
-      put(t, a.complement ? one_minus_decay(g, d) * e : e, e * d * (a.complement ? p - x : p));
-      e *= d;
-    }
-    end = begin;
+  const int64_t first = (int64_t)(ticket % blocks) * S::NCH;  // the block's first channel
+  const int64_t r0 = (int64_t)tile * SCAN_ROWS;
+  const bool mine = first + lane * VEC < a.D;
+  const int64_t ch = mine ? first + lane * VEC : 0;
+  const int64_t t0 = r0 + w * R;
+
+  Pack<GT, VEC> graw[R];
+  Pack<XT, VEC> xraw[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {  // rows behind the last one read that row again
+    const int64_t t = t0 + r < a.T ? t0 + r : a.T - 1;
+    graw[r] = load_pack<GT, VEC>((const GT *)a.g + t * a.g_st + ch);
+    xraw[r] = load_pack<XT, VEC>((const XT *)a.x + t * a.x_st + ch);
   }
-  if (a.ds0) a.ds0[i * a.D + ch] = e;
+  const int64_t c0 = bound_at(a.cu, a.cu_is64, 0, a.T), cN = bound_at(a.cu, a.cu_is64, a.N, a.T);
+  const Marks marks = mark_rows(sh, a, r0, tid);
+  const uint32_t starts = (uint32_t)(marks.start >> (w * R)) & 0xff, ends = (uint32_t)(marks.end >> (w * R)) & 0xff;
+
+  float d[R][VEC], u[R][VEC], sum[VEC] = {}, h[VEC] = {};
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      const float g = (float)graw[r].v[c], x = (float)xraw[r].v[c];
+      d[r][c] = decay(g);
+      u[r][c] = COMPL ? one_minus_decay(g, d[r][c]) * x : x;
+      sum[c] += g;
+    }
+    if (starts >> r & 1) {  // the sequence's first row: its initial state's share joins the term
+      if (a.s0) {
+        const Pack<float, VEC> s0 = load_pack<float, VEC>(a.s0 + (int64_t)sh.start_id[w * R + r] * a.D + ch);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) u[r][c] = fmaf(d[r][c], s0.v[c], u[r][c]);
+      }
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) h[c] = u[r][c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) h[c] = fmaf(d[r][c], h[c], u[r][c]);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) {
+    sh.A[w][lane * VEC + c] = starts ? 0.f : decay(sum[c]);
+    sh.B[w][lane * VEC + c] = h[c];
+  }
+  __syncthreads();
+
+  const bool needs = tile > 0 && !(marks.start & 1) && r0 >= c0 && r0 < cN;
+  const int col = tid % S::NCH;
+  const bool live = first + col < a.D;
+  float carry = 0.f;
+  if (hand_on) {
+    float A = 1.f, B = 0.f;
+    if (tid < S::NCH) {
+#pragma unroll
+      for (int v = 0; v < WAVES; ++v) {
+        B = apply(sh.A[v][col], B, sh.B[v][col]);
+        A *= sh.A[v][col];
+      }
+      if (!needs) A = 0.f;
+    }
+    uint64_t *words = (uint64_t *)((char *)a.ws + 256) + first + col;
+    const bool publish = tid < S::NCH && live && tile + 1 < tiles;
+    if (publish)
+      __hip_atomic_store(words + (int64_t)tile * a.D, make_word(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (needs) {
+      carry = entering(sh, tile, live, tid, [&](int i) { return words + (int64_t)(tile - 1 - i) * a.D; });
+      if (publish && A != 0.f)
+        __hip_atomic_store(words + (int64_t)tile * a.D, make_word(0.f, fmaf(A, carry, B)), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  if (tid < S::NCH) {  // the state entering each wave's rows, in place of its A
+    if (a.checkpoints && live && r0 >= c0 && r0 < cN) a.checkpoints[(int64_t)tile * a.D + first + col] = carry;
+#pragma unroll
+    for (int v = 0; v < WAVES; ++v) {
+      const float next = apply(sh.A[v][col], carry, sh.B[v][col]);
+      sh.A[v][col] = carry;
+      carry = next;
+    }
+  }
+  __syncthreads();
+
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) h[c] = sh.A[w][lane * VEC + c];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) h[c] = starts >> r & 1 ? u[r][c] : fmaf(d[r][c], h[c], u[r][c]);
+    const int64_t t = t0 + r;
+    if (a.o && mine && t >= c0 && t < cN) store_pack<XT, VEC>((XT *)a.o + t * a.o_st + ch, h);
+    if (ends >> r & 1) {
+      const int64_t i = sh.end_id[w * R + r];
+      if (a.final_state && mine) store_pack<float, VEC>(a.final_state + i * a.D + ch, h);
+      if (a.cache) {
+        const int64_t slot = index_at(a.slots, a.slots_is64, i);
+        if (slot >= 0 && slot < a.num_slots && mine) store_pack<float, VEC>(a.cache + slot * a.D + ch, h);
+      }
+    }
+  }
+}
+
+// Gradients, tiles handed out from the last rows to the first.  The gradient e of
+// a row's state follows the recurrence in reverse, e <- a (d_o + e) from the row
+// behind, cut at the sequences' last rows (where d_final_state enters), and is
+// handed on between tiles the same way.  The states are formed again from the
+// checkpoint at the tile's first row.
+template <typename XT, typename GT, int VEC, bool COMPL>
+__global__ void __launch_bounds__(THREADS, 2)
+    gdp_scan_backward_kernel(ScanArgs a, int tiles, int blocks) {
+  using S = Shared<VEC>;
+  __shared__ S sh;
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const bool hand_on = tiles > 1;
+  const int ticket = take_ticket(sh, a, hand_on, tid);
+  const int tile = __builtin_amdgcn_readfirstlane(tiles - 1 - ticket / blocks);
+  if (tile < 0) {
+    empty_sequences(a, ticket - tiles * blocks, a.dfinal, a.ds0, tid);
+    return;
+  }
+  const int64_t first = (int64_t)(ticket % blocks) * S::NCH;
+  const int64_t r0 = (int64_t)tile * SCAN_ROWS;
+  const bool mine = first + lane * VEC < a.D;
+  const int64_t ch = mine ? first + lane * VEC : 0;
+  const int64_t t0 = r0 + w * R;
+
+  Pack<GT, VEC> graw[R];
+  Pack<XT, VEC> xraw[R], draw[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t t = t0 + r < a.T ? t0 + r : a.T - 1;
+    graw[r] = load_pack<GT, VEC>((const GT *)a.g + t * a.g_st + ch);
+    xraw[r] = load_pack<XT, VEC>((const XT *)a.x + t * a.x_st + ch);
+    draw[r] = load_pack<XT, VEC>((const XT *)a.dout + t * a.do_st + ch);
+  }
+  const int col = tid % S::NCH;
+  const bool live = first + col < a.D;
+  float state = 0.f;
+  if (tid < S::NCH && live) state = a.checkpoints[(int64_t)tile * a.D + first + col];
+  const int64_t c0 = bound_at(a.cu, a.cu_is64, 0, a.T), cN = bound_at(a.cu, a.cu_is64, a.N, a.T);
+  const Marks marks = mark_rows(sh, a, r0, tid);
+  const uint32_t starts = (uint32_t)(marks.start >> (w * R)) & 0xff, ends = (uint32_t)(marks.end >> (w * R)) & 0xff;
+
+  // the states before the wave's rows: the forward maps of the waves, composed
+  float d[R][VEC], m[COMPL ? R : 1][VEC], h[VEC] = {}, sum[VEC] = {};
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    float s0[VEC] = {};
+    if ((starts >> r & 1) && a.s0) {
+      const Pack<float, VEC> p = load_pack<float, VEC>(a.s0 + (int64_t)sh.start_id[w * R + r] * a.D + ch);
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) s0[c] = p.v[c];
+    }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      const float g = (float)graw[r].v[c], x = (float)xraw[r].v[c];
+      d[r][c] = decay(g);
+      if (COMPL) m[r][c] = one_minus_decay(g, d[r][c]);
+      sum[c] += g;
+      h[c] = fmaf(d[r][c], starts >> r & 1 ? s0[c] : h[c], COMPL ? m[r][c] * x : x);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) {
+    sum[c] = decay(sum[c]);  // the product of the wave's decays, forward and in reverse
+    sh.A[w][lane * VEC + c] = starts ? 0.f : sum[c];
+    sh.B[w][lane * VEC + c] = h[c];
+  }
+  __syncthreads();
+  if (tid < S::NCH) {
+#pragma unroll
+    for (int v = 0; v < WAVES; ++v) {
+      const float next = apply(sh.A[v][col], state, sh.B[v][col]);
+      sh.A[v][col] = state;
+      state = next;
+    }
+  }
+  __syncthreads();
+  // p = a (h before [- x]), by which e gives dg; then the wave's map of e
+  float p[R][VEC];
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) h[c] = sh.A[w][lane * VEC + c];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (starts >> r & 1) {
+      if (a.s0) {
+        const Pack<float, VEC> s0 = load_pack<float, VEC>(a.s0 + (int64_t)sh.start_id[w * R + r] * a.D + ch);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) h[c] = s0.v[c];
+      } else {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) h[c] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      const float x = (float)xraw[r].v[c];
+      p[r][c] = d[r][c] * (COMPL ? h[c] - x : h[c]);
+      h[c] = fmaf(d[r][c], h[c], COMPL ? m[r][c] * x : x);
+    }
+  }
+  float e[VEC] = {};
+  auto last_row = [&](int r, float (&e)[VEC]) {  // a sequence's last row: e comes from d_final_state
+    if (a.dfinal) {
+      const Pack<float, VEC> f = load_pack<float, VEC>(a.dfinal + (int64_t)sh.end_id[w * R + r] * a.D + ch);
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) e[c] = f.v[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) e[c] = 0.f;
+    }
+  };
+#pragma unroll
+  for (int r = R - 1; r >= 0; --r) {
+    if (ends >> r & 1) last_row(r, e);
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) e[c] = d[r][c] * ((float)draw[r].v[c] + e[c]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) {
+    sh.A[w][lane * VEC + c] = ends ? 0.f : sum[c];
+    sh.B[w][lane * VEC + c] = e[c];
+  }
+  __syncthreads();
+
+  const int64_t rl = r0 + SCAN_ROWS - 1;  // the tile's last row
+  const bool needs = tile + 1 < tiles && !(marks.end >> 63) && rl >= c0 && rl < cN;
+  float carry = 0.f;
+  if (hand_on) {
+    float A = 1.f, B = 0.f;
+    if (tid < S::NCH) {
+#pragma unroll
+      for (int v = WAVES - 1; v >= 0; --v) {
+        B = apply(sh.A[v][col], B, sh.B[v][col]);
+        A *= sh.A[v][col];
+      }
+      if (!needs) A = 0.f;
+    }
+    uint64_t *words = (uint64_t *)((char *)a.ws + 256) + first + col;
+    const bool publish = tid < S::NCH && live && tile > 0;
+    if (publish)
+      __hip_atomic_store(words + (int64_t)tile * a.D, make_word(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (needs) {
+      carry = entering(sh, tiles - 1 - tile, live, tid, [&](int i) { return words + (int64_t)(tile + 1 + i) * a.D; });
+      if (publish && A != 0.f)
+        __hip_atomic_store(words + (int64_t)tile * a.D, make_word(0.f, fmaf(A, carry, B)), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  if (tid < S::NCH) {
+#pragma unroll
+    for (int v = WAVES - 1; v >= 0; --v) {
+      const float next = apply(sh.A[v][col], carry, sh.B[v][col]);
+      sh.A[v][col] = carry;
+      carry = next;
+    }
+  }
+  __syncthreads();
+
+#pragma unroll
+  for (int c = 0; c < VEC; ++c) e[c] = sh.A[w][lane * VEC + c];
+#pragma unroll
+  for (int r = R - 1; r >= 0; --r) {
+    const int64_t t = t0 + r;
+    const bool covered = t >= c0 && t < cN;
+    if (ends >> r & 1) last_row(r, e);
+    float dx[VEC], dg[VEC];
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      e[c] += (float)draw[r].v[c];
+      dx[c] = covered ? (COMPL ? m[r][c] * e[c] : e[c]) : 0.f;
+      dg[c] = covered ? e[c] * p[r][c] : 0.f;
+      e[c] *= d[r][c];
+    }
+    if (mine && t < a.T) {
+      if (a.dx_f32) store_pack<float, VEC>((float *)a.dx + t * a.dx_st + ch, dx);
+      else store_pack<XT, VEC>((XT *)a.dx + t * a.dx_st + ch, dx);
+      if (a.dg_f32) store_pack<float, VEC>((float *)a.dg + t * a.dg_st + ch, dg);
+      else store_pack<GT, VEC>((GT *)a.dg + t * a.dg_st + ch, dg);
+    }
+    if ((starts >> r & 1) && a.ds0 && mine)
+      store_pack<float, VEC>(a.ds0 + (int64_t)sh.start_id[w * R + r] * a.D + ch, e);
+  }
 }
 
 template <typename XT, typename GT>
@@ -101,24 +502,78 @@ template <typename F> hipError_t by_types(int xt, int gt, F f) {
   return gt == EL_F32 ? f((_Float16)0, (float)0) : f((_Float16)0, (_Float16)0);
 }
 
+// the counter and the words: everything to all-ones bits
+__global__ void __launch_bounds__(256) gdp_scan_fill_kernel(uint4 *p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+    p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+}
+
+bool aligned(const void *p, int64_t stride, int es) { return !p || (((uintptr_t)p & (4 * es - 1)) == 0 && stride % 4 == 0); }
+
+struct Grid { int tiles, blocks; unsigned jobs; };
+
+template <int VEC> Grid grid_of(const ScanArgs &a, bool empties) {
+  Grid g;
+  g.tiles = (int)((a.T + SCAN_ROWS - 1) / SCAN_ROWS);
+  g.blocks = (int)((a.D + 64 * VEC - 1) / (64 * VEC));
+  g.jobs = (unsigned)((int64_t)g.tiles * g.blocks + (empties ? (a.N + 63) / 64 : 0));
+  return g;
+}
+
+hipError_t fill_words(const ScanArgs &a, const Grid &g, hipStream_t stream) {
+  if (g.tiles <= 1) return hipSuccess;
+  const int64_t n = (int64_t)scan_state_bytes(a.T, a.D) / 16, want = (n + 255) / 256;
+  hipLaunchKernelGGL(gdp_scan_fill_kernel, dim3((unsigned)(want < 2048 ? want : 2048)), dim3(256), 0, stream,
+                     (uint4 *)a.ws, n);
+  return hipGetLastError();
+}
+
 }  // namespace
 
-size_t scan_state_bytes(int64_t, int64_t) { return 0; }
-bool scan_served(int64_t, int64_t N, int64_t D) { return N < INT32_MAX && (D + 63) / 64 <= 65535; }
+size_t scan_state_bytes(int64_t T, int64_t D) {
+  const int64_t tiles = (T + SCAN_ROWS - 1) / SCAN_ROWS;
+  return tiles <= 1 ? 0 : (256 + (size_t)tiles * D * 8 + 255) & ~(size_t)255;
+}
+
+bool scan_served(int64_t T, int64_t N, int64_t D) {
+  const int64_t tiles = T / SCAN_ROWS + 1, blocks = D / 64 + 1;
+  return N < INT32_MAX && D / 256 < 65535 && tiles < INT32_MAX && blocks < INT32_MAX / tiles - N / 64 - 1;
+}
 
 hipError_t launch_scan(const ScanArgs &a, int xt, int gt, hipStream_t stream) {
-  if (a.N == 0) return hipSuccess;
   return by_types(xt, gt, [&](auto x, auto g) {
-    hipLaunchKernelGGL((gdp_scan_kernel<decltype(x), decltype(g)>), dim3((unsigned)a.N, (unsigned)((a.D + 63) / 64)),
-                       dim3(64), 0, stream, a);
+    using XT = decltype(x);
+    using GT = decltype(g);
+    const bool vec = a.D % 4 == 0 && aligned(a.x, a.x_st, sizeof(XT)) && aligned(a.g, a.g_st, sizeof(GT)) &&
+                     aligned(a.o, a.o_st, sizeof(XT)) && aligned(a.s0, 0, 4) && aligned(a.final_state, 0, 4) &&
+                     aligned(a.cache, 0, 4);
+    const bool empties = a.N > 0 && (a.final_state || a.cache);
+    const Grid k = vec ? grid_of<4>(a, empties) : grid_of<1>(a, empties);
+    if (k.jobs == 0) return hipSuccess;
+    if (hipError_t e = fill_words(a, k, stream)) return e;
+    auto *kernel = vec ? (a.complement ? gdp_scan_kernel<XT, GT, 4, true> : gdp_scan_kernel<XT, GT, 4, false>)
+                       : (a.complement ? gdp_scan_kernel<XT, GT, 1, true> : gdp_scan_kernel<XT, GT, 1, false>);
+    hipLaunchKernelGGL(kernel, dim3(k.jobs), dim3(THREADS), 0, stream, a, k.tiles, k.blocks);
     return hipGetLastError();
   });
 }
 
 hipError_t launch_scan_backward(const ScanArgs &a, int xt, int gt, hipStream_t stream) {
   return by_types(xt, gt, [&](auto x, auto g) {
-    hipLaunchKernelGGL((gdp_scan_backward_kernel<decltype(x), decltype(g)>),
-                       dim3((unsigned)(a.N + 1), (unsigned)((a.D + 63) / 64)), dim3(64), 0, stream, a);
+    using XT = decltype(x);
+    using GT = decltype(g);
+    const bool vec = a.D % 4 == 0 && aligned(a.x, a.x_st, sizeof(XT)) && aligned(a.g, a.g_st, sizeof(GT)) &&
+                     aligned(a.dout, a.do_st, sizeof(XT)) && aligned(a.dx, a.dx_st, a.dx_f32 ? 4 : sizeof(XT)) &&
+                     aligned(a.dg, a.dg_st, a.dg_f32 ? 4 : sizeof(GT)) && aligned(a.s0, 0, 4) &&
+                     aligned(a.dfinal, 0, 4) && aligned(a.ds0, 0, 4);
+    const bool empties = a.N > 0 && a.ds0;
+    const Grid k = vec ? grid_of<4>(a, empties) : grid_of<1>(a, empties);
+    if (k.jobs == 0) return hipSuccess;
+    if (hipError_t e = fill_words(a, k, stream)) return e;
+    auto *kernel =
+        vec ? (a.complement ? gdp_scan_backward_kernel<XT, GT, 4, true> : gdp_scan_backward_kernel<XT, GT, 4, false>)
+            : (a.complement ? gdp_scan_backward_kernel<XT, GT, 1, true> : gdp_scan_backward_kernel<XT, GT, 1, false>);
+    hipLaunchKernelGGL(kernel, dim3(k.jobs), dim3(THREADS), 0, stream, a, k.tiles, k.blocks);
     return hipGetLastError();
   });
 }
