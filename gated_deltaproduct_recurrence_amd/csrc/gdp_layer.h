@@ -67,6 +67,7 @@ struct NormArgs {
   float *dw, *db;                       // [V] or [G, V] or null
   float *ws;                            // norm_backward_bytes(T, G, V)
 };
+constexpr int64_t NORM_MAX_SIZE = 16384, NORM_MAX_GROUPS = 65535;
 size_t norm_backward_bytes(int64_t T, int64_t G, int64_t V);
 hipError_t launch_norm(const NormArgs &a, int x_type, hipStream_t stream);
 hipError_t launch_norm_backward(const NormArgs &a, int x_type, hipStream_t stream);

@@ -309,7 +309,7 @@ int gdp_gated_scan_backward(const gdp_tensor *x, const gdp_tensor *g_log, const 
 }
 
 size_t gdp_group_norm_backward_workspace_bytes(int64_t T, int64_t G, int64_t V) {
-  if (T < 0 || G < 1 || V < 1 || V > 16384 || G > INT32_MAX / V) return 0;
+  if (T < 0 || G < 1 || V < 1 || V > NORM_MAX_SIZE || G > NORM_MAX_GROUPS) return 0;
   return align256(norm_backward_bytes(T, G, V));
 }
 
@@ -322,8 +322,9 @@ int norm_args(const gdp_tensor *x, const gdp_tensor *weight, const gdp_tensor *b
   const int64_t T = x->shape[0], G = x->shape[1], V = x->shape[2];
   if (G < 1 || V < 1) return fail(GDP_EINVAL, "the group count and group size must be positive");
   if (!is_float(x->dtype)) return fail(GDP_EUNSUPPORTED, "x must be float32, bfloat16 or float16");
-  if (V > 16384) return fail(GDP_EUNSUPPORTED, "groups of more than 16384 channels are not served (V = %lld)", (long long)V);
-  if (G > INT32_MAX / V) return fail(GDP_EUNSUPPORTED, "too many channels (G=%lld, V=%lld)", (long long)G, (long long)V);
+  if (V > NORM_MAX_SIZE || G > NORM_MAX_GROUPS)
+    return fail(GDP_EUNSUPPORTED, "more than 65535 groups, or 16384 channels in a group, are not served (G=%lld, V=%lld)",
+                (long long)G, (long long)V);
   if (activation != GDP_ACT_NONE && activation != GDP_ACT_SILU && activation != GDP_ACT_SIGMOID)
     return fail(GDP_EINVAL, "unknown activation %d", activation);
   if (!(eps > 0.f) || std::isinf(eps)) return fail(GDP_EINVAL, "eps must be positive and finite");

@@ -1,6 +1,21 @@
 // gdp_norm.hip -- gfx950 kernels of the group norm with an activation over the
-// channels of each (token, group), and of its gradients.  One wave per (token,
-// group); the weight gradients are summed by one workgroup per channel.
+// channels of each (token, group), and of its gradients.
+//
+//     n = (x - mean) rstd w + b,   y = act(n)  or  n act(z)
+//     q = dn w:   dx = rstd (q - mean(q) - xhat mean(q xhat)),   xhat = (x - mean) rstd
+//     dw = sum dn xhat,  db = sum dn,   dn = d_y act'(n)  or  d_y act(z),
+//     dz = d_y n act'(z)
+//
+// Both directions are streams: each input is read once, each output written once.
+// A team of LPG lanes (a power of two) holds one (token, group) in registers, E
+// pieces of VEC neighbouring channels per lane, so that the two passes of the
+// statistics (mean, then the squares of x - mean: no cancellation under a large
+// mean) and the gradient's sums take no second read.  A workgroup holds S teams;
+// the teams of the whole grid step through the tokens together, by a number of
+// (token, group) pairs that is a multiple of G: a team keeps its group, hence its
+// weights and, in the backward pass, its partial sums of dw and db, in registers.
+// The raw values of a team's next token are loaded before the current one is
+// computed.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -12,154 +27,441 @@
 namespace gdp {
 namespace {
 
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m, 64);
+constexpr int MAX_VALUES = 16;  // values a lane holds of one group
+
+// Sum over the lanes of an aligned team of LPG <= 64 lanes, in every lane: DPP
+// moves within 16 lanes, then the row swaps.
+template <int CTRL> __device__ __forceinline__ float dpp_add(float x) {
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float team_sum(float x, int lpg) {
+  if (lpg > 1) x = dpp_add<0xb1>(x);   // quad_perm 1,0,3,2
+  if (lpg > 2) x = dpp_add<0x4e>(x);   // quad_perm 2,3,0,1
+  if (lpg > 4) x = dpp_add<0x141>(x);  // row_half_mirror
+  if (lpg > 8) x = dpp_add<0x140>(x);  // row_mirror
+  if (lpg > 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if (lpg > 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
   return x;
 }
 
-template <typename T> __device__ __forceinline__ float param(const void *p, int type, int64_t i) {
-  return type == EL_F32 ? ((const float *)p)[i] : (float)((const T *)p)[i];
-}
-
-// f = act(v) and its derivative
-__device__ __forceinline__ void activate(int act, float v, float &f, float &df) {
-  if (act == GDP_ACT_NONE) { f = v; df = 1.f; return; }
-  const float s = 1.f / (1.f + expf(-v));
-  if (act == GDP_ACT_SIGMOID) { f = s; df = s * (1.f - s); return; }
-  f = v * s;
-  df = s * (1.f + v * (1.f - s));
-}
-
-template <typename T> struct Row {
-  const T *x;
-  float mean, rstd;
-  __device__ Row(const NormArgs &a, int64_t t, int g, int lane) {
-    x = (const T *)a.x + t * a.x_st + g * a.x_sh;
-    mean = 0.f;
-    if (a.center) {
-      float s = 0.f;
-      for (int v = lane; v < a.V; v += 64) s += (float)x[v];
-      mean = wave_sum(s) / a.V;
+// ... of a team of whole waves (LPG > 64): the waves' sums through LDS.  `turn`
+// alternates the slots, so one barrier per sum is enough.
+template <int WIDE> struct Team {
+  int lpg, lane, first_wave;  // lanes per team, lane within it, its first wave in the workgroup
+  float (*slots)[16];         // [2][16]
+  int turn = 0;
+  __device__ float sum(float x) {
+    x = team_sum(x, WIDE ? 64 : lpg);
+    if constexpr (WIDE) {
+      if ((lane & 63) == 0) slots[turn][first_wave + (lane >> 6)] = x;
+      __syncthreads();
+      x = 0.f;
+      for (int v = 0; v < lpg >> 6; ++v) x += slots[turn][first_wave + v];
+      turn ^= 1;
     }
-    float ss = 0.f;
-    for (int v = lane; v < a.V; v += 64) {
-      const float d = (float)x[v] - mean;
-      ss = fmaf(d, d, ss);
-    }
-    rstd = 1.f / sqrtf(wave_sum(ss) / a.V + a.eps);
+    return x;
   }
 };
 
-template <typename T> __global__ void __launch_bounds__(64) gdp_norm_kernel(NormArgs a) {
-  const int64_t t = blockIdx.x / a.G;
-  const int g = (int)(blockIdx.x % a.G), lane = threadIdx.x;
-  const Row<T> r(a, t, g, lane);
-  for (int v = lane; v < a.V; v += 64) {
-    float n = ((float)r.x[v] - r.mean) * r.rstd;
-    if (a.w) n *= param<T>(a.w, a.w_type, g * a.w_sh + v);
-    if (a.b) n += param<T>(a.b, a.w_type, g * a.w_sh + v);
-    float f, df;
-    activate(a.act, a.z ? (float)((const T *)a.z)[t * a.z_st + g * a.z_sh + v] : n, f, df);
-    ((T *)a.y)[t * a.y_st + g * a.y_sh + v] = (T)(a.z ? n * f : f);
+template <typename T, int N> struct alignas(sizeof(T) * N) Pack { T v[N]; };
+
+// s = sigmoid(v): the hardware's exponential and reciprocal, each good to one step
+__device__ __forceinline__ float sigmoid(float v) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -LOG2E_L));
+}
+
+// E pieces of one (token, group)
+template <typename T, int VEC, int E> struct Values {
+  Pack<T, VEC> p[E];
+  __device__ __forceinline__ void load(const T *row, int lane, int lpg, int V) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int v = (e * lpg + lane) * VEC;
+      if (v < V) p[e] = *(const Pack<T, VEC> *)(row + v);
+      else p[e] = {};
+    }
+  }
+};
+
+template <typename T, int VEC, int E>
+__device__ __forceinline__ void store_values(T *row, const float (&y)[E][VEC], int lane, int lpg, int V) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int v = (e * lpg + lane) * VEC;
+    Pack<T, VEC> s;
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) s.v[c] = (T)y[e][c];
+    if (v < V) *(Pack<T, VEC> *)(row + v) = s;
   }
 }
 
-template <typename T> __global__ void __launch_bounds__(64) gdp_norm_backward_kernel(NormArgs a) {
-  const int64_t t = blockIdx.x / a.G;
-  const int g = (int)(blockIdx.x % a.G), lane = threadIdx.x;
-  const Row<T> r(a, t, g, lane);
-  const T *z = a.z ? (const T *)a.z + t * a.z_st + g * a.z_sh : nullptr;
-  const T *dy = (const T *)a.dy + t * a.dy_st + g * a.dy_sh;
-  float s1 = 0.f, s2 = 0.f;
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int v = lane; v < a.V; v += 64) {
-      const float xhat = ((float)r.x[v] - r.mean) * r.rstd;
-      const float w = a.w ? param<T>(a.w, a.w_type, g * a.w_sh + v) : 1.f;
-      float n = xhat * w;
-      if (a.b) n += param<T>(a.b, a.w_type, g * a.w_sh + v);
-      float f, df;
-      activate(a.act, z ? (float)z[v] : n, f, df);
-      const float d = (float)dy[v], dn = d * (z ? f : df);
-      if (pass == 0) {
-        s1 += dn * w;
-        s2 = fmaf(dn * w, xhat, s2);
-      } else {
-        ((T *)a.dx)[t * a.dx_st + g * a.dx_sh + v] = (T)((dn * w - s1 - xhat * s2) * r.rstd);
-        if (z) ((T *)a.dz)[t * a.dz_st + g * a.dz_sh + v] = (T)(d * n * df);
-      }
+// a group's weights or biases (or `other` without any)
+template <typename T, int VEC, int E>
+__device__ __forceinline__ void load_params(float (&w)[E][VEC], const void *p, int type, int64_t at, float other,
+                                            int lane, int lpg, int V) {
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      const int v = (e * lpg + lane) * VEC + c;
+      w[e][c] = !p || v >= V ? other : (type == EL_F32 ? ((const float *)p)[at + v] : (float)((const T *)p)[at + v]);
     }
-    if (pass == 0) {
-      s1 = a.center ? wave_sum(s1) / a.V : 0.f;
-      s2 = wave_sum(s2) / a.V;
-      if (a.ws && lane == 0) {
-        a.ws[2 * (t * a.G + g)] = r.mean;
-        a.ws[2 * (t * a.G + g) + 1] = r.rstd;
+}
+
+// xhat of a group in place of its values; returns rstd.  Lanes past V hold zeros.
+template <typename T, int VEC, int E, int WIDE>
+__device__ __forceinline__ float normalise(float (&xhat)[E][VEC], const Values<T, VEC, E> &x, const NormArgs &a,
+                                           Team<WIDE> &team, float inv_v) {
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) xhat[e][c] = (float)x.p[e].v[c];
+  if (a.center) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) s += xhat[e][c];
+    const float mean = team.sum(s) * inv_v;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) xhat[e][c] = (e * team.lpg + team.lane) * VEC < a.V ? xhat[e][c] - mean : 0.f;
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) ss = fmaf(xhat[e][c], xhat[e][c], ss);
+  const float rstd = __builtin_amdgcn_rsqf(fmaf(team.sum(ss), inv_v, a.eps));
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) xhat[e][c] *= rstd;
+  return rstd;
+}
+
+// The team's place: its group and first token.
+struct Place { int q, g; int64_t t, t_block, step; };
+__device__ __forceinline__ Place place_of(const NormArgs &a, int teams, int team) {
+  Place p;
+  p.q = (int)blockIdx.x * teams + team;
+  p.g = p.q % a.G;
+  p.t = p.q / a.G;
+  p.t_block = (int)blockIdx.x * teams / a.G;  // the block's earliest token: a loop bound its waves share
+  p.step = (int64_t)gridDim.x * teams / a.G;
+  return p;
+}
+
+template <typename T, int VEC, int E, int WIDE>
+__global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_norm_kernel(NormArgs a, int lpg) {
+  __shared__ float slots[WIDE ? 2 : 1][16];
+  const int tid = threadIdx.x;
+  Team<WIDE> team{lpg, tid & (lpg - 1), (tid & ~(lpg - 1)) >> 6, slots};
+  const Place at = place_of(a, (int)blockDim.x / lpg, tid / lpg);
+  const float inv_v = 1.f / (float)a.V;
+  const T *x = (const T *)a.x + at.g * a.x_sh, *z = (const T *)a.z + at.g * a.z_sh;
+  T *y = (T *)a.y + at.g * a.y_sh;
+  float w[E][VEC], b[E][VEC];
+  load_params<T, VEC, E>(w, a.w, a.w_type, at.g * a.w_sh, 1.f, team.lane, lpg, a.V);
+  load_params<T, VEC, E>(b, a.b, a.w_type, at.g * a.w_sh, 0.f, team.lane, lpg, a.V);
+  Values<T, VEC, E> xv{}, zv{}, xn{}, zn{};
+  auto fetch = [&](int64_t t) {
+    if (t < a.T) {
+      xn.load(x + t * a.x_st, team.lane, lpg, a.V);
+      if (a.z) zn.load(z + t * a.z_st, team.lane, lpg, a.V);
+    }
+  };
+  int64_t t = at.t;
+  fetch(t);
+  for (int64_t tb = at.t_block; tb < a.T; tb += at.step, t += at.step) {
+    xv = xn;
+    zv = zn;
+    fetch(t + at.step);
+    float n[E][VEC];
+    normalise<T, VEC, E, WIDE>(n, xv, a, team, inv_v);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) n[e][c] = fmaf(n[e][c], w[e][c], b[e][c]);
+    if (a.z) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+          const float v = (float)zv.p[e].v[c];
+          n[e][c] *= a.act == GDP_ACT_NONE ? v : (a.act == GDP_ACT_SILU ? v * sigmoid(v) : sigmoid(v));
+        }
+    } else if (a.act != GDP_ACT_NONE) {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+          const float s = sigmoid(n[e][c]);
+          n[e][c] = a.act == GDP_ACT_SILU ? n[e][c] * s : s;
+        }
+    }
+    if (t < a.T) store_values<T, VEC, E>(y + t * a.y_st, n, team.lane, lpg, a.V);
+  }
+}
+
+// The gradients; partial sums of dw and db to the workspace: one row [2][V] per
+// workgroup when the groups share their weights (the teams' sums added in LDS),
+// else one per team.
+template <typename T, int VEC, int E, int WIDE>
+__global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_norm_backward_kernel(NormArgs a, int lpg) {
+  __shared__ float slots[WIDE ? 2 : 1][16];
+  __shared__ float part[WIDE ? 1 : 256 * MAX_VALUES];
+  const int tid = threadIdx.x, teams = (int)blockDim.x / lpg;
+  Team<WIDE> team{lpg, tid & (lpg - 1), (tid & ~(lpg - 1)) >> 6, slots};
+  const Place at = place_of(a, teams, tid / lpg);
+  const float inv_v = 1.f / (float)a.V;
+  const T *x = (const T *)a.x + at.g * a.x_sh, *z = (const T *)a.z + at.g * a.z_sh,
+          *dy = (const T *)a.dy + at.g * a.dy_sh;
+  T *dx = (T *)a.dx + at.g * a.dx_sh, *dz = (T *)a.dz + at.g * a.dz_sh;
+  float w[E][VEC], b[E][VEC], dw[E][VEC] = {}, db[E][VEC] = {};
+  load_params<T, VEC, E>(w, a.w, a.w_type, at.g * a.w_sh, 1.f, team.lane, lpg, a.V);
+  load_params<T, VEC, E>(b, a.b, a.w_type, at.g * a.w_sh, 0.f, team.lane, lpg, a.V);
+  Values<T, VEC, E> xv{}, zv{}, dv{}, xn{}, zn{}, dn_{};
+  auto fetch = [&](int64_t t) {
+    if (t < a.T) {
+      xn.load(x + t * a.x_st, team.lane, lpg, a.V);
+      dn_.load(dy + t * a.dy_st, team.lane, lpg, a.V);
+      if (a.z) zn.load(z + t * a.z_st, team.lane, lpg, a.V);
+    }
+  };
+  int64_t t = at.t;
+  fetch(t);
+  for (int64_t tb = at.t_block; tb < a.T; tb += at.step, t += at.step) {
+    xv = xn;
+    zv = zn;
+    dv = dn_;
+    fetch(t + at.step);
+    float xhat[E][VEC], dn[E][VEC], g[E][VEC];  // g: dz
+    const float rstd = normalise<T, VEC, E, WIDE>(xhat, xv, a, team, inv_v);
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) {
+        const float n = fmaf(xhat[e][c], w[e][c], b[e][c]), d = (float)dv.p[e].v[c];
+        const float v = a.z ? (float)zv.p[e].v[c] : n;
+        float f = v, df = 1.f;
+        if (a.act != GDP_ACT_NONE) {
+          const float s = sigmoid(v);
+          if (a.act == GDP_ACT_SILU) {
+            f = v * s;
+            df = fmaf(f, 1.f - s, s);  // s (1 + v (1 - s))
+          } else {
+            f = s;
+            df = s * (1.f - s);
+          }
+        }
+        dn[e][c] = d * (a.z ? f : df);
+        g[e][c] = d * n * df;
+        s1 = fmaf(dn[e][c], w[e][c], s1);
+        s2 = fmaf(dn[e][c] * w[e][c], xhat[e][c], s2);
       }
+    s1 = a.center ? team.sum(s1) * inv_v : 0.f;
+    s2 = team.sum(s2) * inv_v;
+    if (t < a.T) {
+      if (a.z) store_values<T, VEC, E>(dz + t * a.dz_st, g, team.lane, lpg, a.V);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+          dw[e][c] = fmaf(dn[e][c], xhat[e][c], dw[e][c]);
+          db[e][c] += dn[e][c];
+          g[e][c] = (dn[e][c] * w[e][c] - s1 - xhat[e][c] * s2) * rstd;
+        }
+      store_values<T, VEC, E>(dx + t * a.dx_st, g, team.lane, lpg, a.V);
+    }
+  }
+  if (!a.dw && !a.db) return;
+  const bool fold = !WIDE && a.w_sh == 0 && teams > 1;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (!(k == 0 ? a.dw : a.db)) continue;
+    float *row = a.ws + ((int64_t)(fold ? (int)blockIdx.x : at.q) * 2 + k) * a.V;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) {
+        const int v = (e * lpg + team.lane) * VEC + c;
+        const float s = k == 0 ? dw[e][c] : db[e][c];
+        if (v < a.V) {
+          if (fold) part[(tid / lpg) * a.V + v] = s;
+          else row[v] = s;
+        }
+      }
+    if (fold) {
+      __syncthreads();
+      for (int v = tid; v < a.V; v += 256) {
+        float s = 0.f;
+        for (int i = 0; i < teams; ++i) s += part[i * a.V + v];
+        row[v] = s;
+      }
+      __syncthreads();
     }
   }
 }
 
-// dw, db of channel blockIdx.x of group blockIdx.y (or of all groups)
-template <typename T> __global__ void __launch_bounds__(256) gdp_norm_weight_kernel(NormArgs a) {
-  const int v = blockIdx.x, tid = threadIdx.x;
-  const bool shared = a.w_sh == 0;
-  const int64_t rows = shared ? a.T * a.G : a.T;
-  float dw = 0.f, db = 0.f;
-  for (int64_t i = tid; i < rows; i += 256) {
-    const int64_t t = shared ? i / a.G : i;
-    const int g = shared ? (int)(i % a.G) : (int)blockIdx.y;
-    const float mean = a.ws[2 * (t * a.G + g)], rstd = a.ws[2 * (t * a.G + g) + 1];
-    const float xhat = ((float)((const T *)a.x)[t * a.x_st + g * a.x_sh + v] - mean) * rstd;
-    float n = xhat;
-    if (a.w) n *= param<T>(a.w, a.w_type, g * a.w_sh + v);
-    if (a.b) n += param<T>(a.b, a.w_type, g * a.w_sh + v);
-    float f, df;
-    activate(a.act, a.z ? (float)((const T *)a.z)[t * a.z_st + g * a.z_sh + v] : n, f, df);
-    const float dn = (float)((const T *)a.dy)[t * a.dy_st + g * a.dy_sh + v] * (a.z ? f : df);
-    dw = fmaf(dn, xhat, dw);
-    db += dn;
+// dw and db from the partial rows of a group (row r: r * stride + blockIdx.y), 64
+// channels per workgroup, the rows dealt over 16 waves.
+__global__ void __launch_bounds__(1024) gdp_norm_weight_kernel(NormArgs a, int rows, int stride) {
+  __shared__ float red[2][16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int v = (int)blockIdx.x * 64 + lane;
+  float s[2] = {0.f, 0.f};
+  if (v < a.V) {
+#pragma unroll 8
+    for (int r = wave; r < rows; r += 16) {
+      const float *row = a.ws + ((int64_t)r * stride + blockIdx.y) * 2 * a.V + v;
+      if (a.dw) s[0] += row[0];
+      if (a.db) s[1] += row[a.V];
+    }
   }
-  __shared__ float red[2][4];
-  dw = wave_sum(dw);
-  db = wave_sum(db);
-  if ((tid & 63) == 0) { red[0][tid >> 6] = dw; red[1][tid >> 6] = db; }
+  red[0][wave][lane] = s[0];
+  red[1][wave][lane] = s[1];
   __syncthreads();
-  if (tid == 0) {
-    const int64_t at = blockIdx.y * a.w_sh + v;
-    if (a.dw) a.dw[at] = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
-    if (a.db) a.db[at] = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  if (wave < 2 && v < a.V) {
+    float *out = wave == 0 ? a.dw : a.db;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += red[wave][i][lane];
+    if (out) out[(int64_t)blockIdx.y * a.V + v] = sum;
   }
 }
+
+// How the groups are laid over lanes.  E pieces of VEC channels per lane: one while
+// a wave holds the group, then up to MAX_VALUES values per lane, then more waves.
+struct Plan { int vec, pieces, lpg, threads, teams; };
+Plan plan_of(int64_t V, int vec) {
+  Plan p;
+  p.vec = vec;
+  const int64_t chunks = (V + vec - 1) / vec;
+  p.pieces = 1;
+  while ((chunks + p.pieces - 1) / p.pieces > 64 && p.pieces * vec < MAX_VALUES) p.pieces *= vec == 1 ? 4 : 2;
+  const int64_t lanes = (chunks + p.pieces - 1) / p.pieces;
+  p.lpg = 1;
+  while (p.lpg < lanes) p.lpg *= 2;
+  p.threads = p.lpg > 256 ? p.lpg : 256;
+  p.teams = p.threads / p.lpg;
+  return p;
+}
+
+int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+
+// Workgroups: one pair per team while that gives at most `most` / 2, then down to
+// `per_team` pairs per team, at most `most`; in multiples that keep a team's group.
+int64_t grid_of(const Plan &p, int64_t T, int G, int64_t per_team, int64_t most) {
+  const int64_t want = (T * G + p.teams - 1) / p.teams, unit = G / gcd(G, p.teams);
+  int64_t n = want;
+  if (want > most / 2) {
+    n = want / per_team;
+    n = n < most / 2 ? most / 2 : (n > most ? most : n);
+  }
+  return (n + unit - 1) / unit * unit;
+}
+constexpr int64_t FORWARD_GRID = 2048, BACKWARD_GRID = 1024;
 
 template <typename F> hipError_t by_type(int xt, F f) {
   if (xt == EL_F32) return f((float)0);
   return xt == EL_BF16 ? f((bf16)0) : f((_Float16)0);
 }
 
+// WIDE: 0 while a wave holds a group, 1 up to 512 lanes, 2 up to 1024 (whose lanes
+// have half the registers: the gradients of more than 512 lanes' groups spill)
+template <int VEC, int E, int WIDE> struct Shape { static constexpr int vec = VEC, pieces = E, wide = WIDE; };
+
+// calls f with the compile-time shape of a plan
+template <int VEC, int E, typename F> hipError_t by_width(const Plan &p, F f) {
+  if (p.lpg <= 64) return f(Shape<VEC, E, 0>());
+  return p.lpg <= 512 ? f(Shape<VEC, E, 1>()) : f(Shape<VEC, E, 2>());
+}
+template <typename T, typename F> hipError_t by_plan(const Plan &p, F f) {
+  if constexpr (sizeof(T) == 2) {
+    if (p.vec == 8) return p.pieces == 1 ? f(Shape<8, 1, 0>()) : by_width<8, 2>(p, f);
+  }
+  if (p.vec == 4) {
+    if (p.pieces == 1) return f(Shape<4, 1, 0>());
+    return p.pieces == 2 ? f(Shape<4, 2, 0>()) : by_width<4, 4>(p, f);
+  }
+  if (p.pieces == 1) return f(Shape<1, 1, 0>());
+  return p.pieces == 4 ? f(Shape<1, 4, 0>()) : by_width<1, 16>(p, f);
+}
+
+// whether pieces of `vec` elements of es bytes are aligned everywhere in a tensor
+bool fits(const void *p, int64_t st, int64_t sh, int vec, int es) {
+  return !p || (((uintptr_t)p & (vec * es - 1)) == 0 && st % vec == 0 && sh % vec == 0);
+}
+int vec_of(const NormArgs &a, int es, bool backward) {
+  for (int vec = es == 2 ? 8 : 4; vec > 1; vec = vec == 8 ? 4 : 1) {
+    bool ok = a.V % vec == 0 && fits(a.x, a.x_st, a.x_sh, vec, es) && fits(a.z, a.z_st, a.z_sh, vec, es);
+    if (backward)
+      ok = ok && fits(a.dy, a.dy_st, a.dy_sh, vec, es) && fits(a.dx, a.dx_st, a.dx_sh, vec, es) &&
+           fits(a.dz, a.dz_st, a.dz_sh, vec, es);
+    else
+      ok = ok && fits(a.y, a.y_st, a.y_sh, vec, es);
+    if (ok) return vec;
+  }
+  return 1;
+}
+
 }  // namespace
 
-size_t norm_backward_bytes(int64_t T, int64_t G, int64_t) { return (size_t)T * G * 8; }
+size_t norm_backward_bytes(int64_t T, int64_t G, int64_t V) {
+  int64_t most = 0;  // of the plans that the alignment of a call's tensors can choose
+  for (int vec : {8, 4, 1}) {
+    if (V % vec) continue;
+    const Plan p = plan_of(V, vec);
+    const int64_t rows = grid_of(p, T, (int)G, 8, BACKWARD_GRID) * p.teams;
+    most = rows > most ? rows : most;
+  }
+  return (size_t)most * V * 8;
+}
 
 hipError_t launch_norm(const NormArgs &a, int xt, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
-  if (a.T > INT32_MAX / a.G) return hipErrorInvalidValue;
   return by_type(xt, [&](auto x) {
-    hipLaunchKernelGGL((gdp_norm_kernel<decltype(x)>), dim3((unsigned)(a.T * a.G)), dim3(64), 0, stream, a);
-    return hipGetLastError();
+    using T = decltype(x);
+    const Plan p = plan_of(a.V, vec_of(a, sizeof(T), false));
+    const int64_t blocks = grid_of(p, a.T, a.G, 1, FORWARD_GRID);
+    return by_plan<T>(p, [&](auto s) {
+      using S = decltype(s);
+      hipLaunchKernelGGL((gdp_norm_kernel<T, S::vec, S::pieces, S::wide>), dim3((unsigned)blocks), dim3(p.threads), 0,
+                         stream, a, p.lpg);
+      return hipGetLastError();
+    });
   });
 }
 
 hipError_t launch_norm_backward(const NormArgs &a, int xt, hipStream_t stream) {
-  if (a.T > INT32_MAX / a.G) return hipErrorInvalidValue;
   return by_type(xt, [&](auto x) {
-    if (a.T > 0) {
-      hipLaunchKernelGGL((gdp_norm_backward_kernel<decltype(x)>), dim3((unsigned)(a.T * a.G)), dim3(64), 0, stream, a);
-      if (hipError_t e = hipGetLastError()) return e;
+    using T = decltype(x);
+    const Plan p = plan_of(a.V, vec_of(a, sizeof(T), true));
+    const int64_t blocks = a.T ? grid_of(p, a.T, a.G, 8, BACKWARD_GRID) : 0;
+    if (blocks) {
+      const hipError_t e = by_plan<T>(p, [&](auto s) {
+        using S = decltype(s);
+        hipLaunchKernelGGL((gdp_norm_backward_kernel<T, S::vec, S::pieces, S::wide>), dim3((unsigned)blocks),
+                           dim3(p.threads), 0, stream, a, p.lpg);
+        return hipGetLastError();
+      });
+      if (e != hipSuccess) return e;
     }
-    if (a.dw || a.db)
-      hipLaunchKernelGGL((gdp_norm_weight_kernel<decltype(x)>), dim3((unsigned)a.V, a.w_sh ? (unsigned)a.G : 1u),
-                         dim3(256), 0, stream, a);
+    if (!a.dw && !a.db) return hipSuccess;
+    const bool shared = a.w_sh == 0, fold = shared && p.lpg <= 64 && p.teams > 1;
+    const int64_t rows = fold ? blocks : blocks * p.teams;
+    const dim3 grid((unsigned)((a.V + 63) / 64), shared ? 1u : (unsigned)a.G);
+    hipLaunchKernelGGL(gdp_norm_weight_kernel, grid, dim3(1024), 0, stream, a, (int)(shared ? rows : rows / a.G),
+                       shared ? 1 : a.G);
     return hipGetLastError();
   });
 }

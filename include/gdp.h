@@ -443,8 +443,8 @@ enum gdp_activation { GDP_ACT_NONE = 0, GDP_ACT_SILU = 1, GDP_ACT_SIGMOID = 2 };
  *   eps          > 0
  *   y            [T, G, V]  x's dtype, may be strided
  * Statistics and products are float32; y is rounded once.  y may not overlap an input
- * (GDP_EALIAS).  V <= 16384 (GDP_EUNSUPPORTED otherwise).  One launch on `stream`;
- * capturable. */
+ * (GDP_EALIAS).  V <= 16384 and G <= 65535 (GDP_EUNSUPPORTED otherwise).  One launch on
+ * `stream`; capturable. */
 int gdp_group_norm(const gdp_tensor *x, const gdp_tensor *weight, const gdp_tensor *bias, const gdp_tensor *gate,
                    int32_t activation, int32_t subtract_mean, float eps, const gdp_tensor *y, void *stream);
 

@@ -201,6 +201,7 @@ def test_norm_refusals(b, call):
     r(new(x=(b.GDP_I64, [20, 4, 48])), b.GDP_EUNSUPPORTED, "x must be float32")
     r(new(x=(BF16, [20, 0, 48])), b.GDP_EINVAL, "positive")
     r(new(x=(BF16, [20, 4, 16385])), b.GDP_EUNSUPPORTED, "16384")
+    r(new(x=(BF16, [20, 65536, 48])), b.GDP_EUNSUPPORTED, "65535 groups")
     r(new(w=(F32, [47])), b.GDP_EINVAL, "weight: dim 0")
     r(new(w=(F32, [4, 4, 3])), b.GDP_EINVAL, "weight must be")
     r(new(w=(b.GDP_F16, [48])), b.GDP_EUNSUPPORTED, "weight must be")
