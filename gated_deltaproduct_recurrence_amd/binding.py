@@ -150,11 +150,12 @@ def _stream(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
-_RECORD = struct.Struct("@Pii8q")  # the layout of gdp_tensor
+# the layout of gdp_tensor, for each number of dims
+_RECORDS = [struct.Struct("@Pii" + f"{n}q{8 * (4 - n)}x" * 2) for n in range(5)]
 
 
 def _pack(t, device):
-    """The gdp_tensor record of a torch tensor as bytes (None -> absent): a third of the time of
+    """The gdp_tensor record of a torch tensor as bytes (None -> absent): a fifth of the time of
     as_gdp_tensor, which counts in a call of a few microseconds.  Refuses a tensor elsewhere than on
     `device`."""
     if t is None:
@@ -164,23 +165,31 @@ def _pack(t, device):
     code = _DT.get(t.dtype)
     if code is None:
         raise ValueError(f"unsupported dtype {t.dtype}")
-    n = t.dim()
+    shape = t.shape
+    n = len(shape)
     if n > 4:
         raise ValueError("at most 4 dims")
-    pad = (0,) * (4 - n)
     # an empty tensor is still "present": a non-null dummy address
-    return _RECORD.pack(t.data_ptr() or 16, code, n, *t.shape, *pad, *t.stride(), *pad)
+    return _RECORDS[n].pack(t.data_ptr() or 16, code, n, *shape, *t.stride())
 
 
-def _on(device):
-    """Whether a call on `device` can launch as it is; raises for tensors that are not on a GPU."""
-    if device.type != "cuda":
-        raise ValueError(f"expected tensors on a GPU, got {device}")
-    return device.index == torch.cuda.current_device()
+# the current stream's handle without the Python object around it (2 us less a call), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _workspace(nbytes, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+def _current_stream(device):
+    return _raw_stream(device.index) if _raw_stream is not None else _stream(device)
+
+
+def _empty(like, shape=None, dtype=None):
+    """A new contiguous tensor on `like`'s device, by default of its shape and dtype."""
+    if shape is None:
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    return like.new_empty(shape, dtype=dtype)
+
+
+def _workspace(like, nbytes):
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
 
 
 # ---------------------------------------------------------------- C ABI names
@@ -372,15 +381,17 @@ def gdp_group_norm_backward_workspace_bytes(T, G, V):
 def _call(device, entry, *args, workspace=(), stream=None):
     """Calls a C entry point with its workspace and the stream to launch on (by default the current one
     of `device`, which is made the current device for the call)."""
+    if device.type != "cuda":
+        raise ValueError(f"expected tensors on a GPU, got {device}")
     if workspace is None:
         workspace = (None, 0)
     elif len(workspace):
         workspace = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    if _on(device):
-        _check(entry(*args, *workspace, _stream(device) if stream is None else stream))
+    if device.index == torch.cuda.current_device():
+        _check(entry(*args, *workspace, _current_stream(device) if stream is None else stream))
     else:
         with torch.cuda.device(device):
-            _check(entry(*args, *workspace, _stream(device) if stream is None else stream))
+            _check(entry(*args, *workspace, _current_stream(device) if stream is None else stream))
 
 
 def gdp_gated_scan(x, g_log, cu_seqlens, complement_input, initial_state, output_final_state, state_cache,
@@ -537,22 +548,21 @@ def gated_scan(x, g_log, cu_seqlens, initial_state=None, output_final_state=Fals
     gated_scan_backward takes.  Rows that no sequence covers are left as they are in `out`."""
     T, D = x.shape
     N = cu_seqlens.shape[0] - 1
-    dev = x.device
-    o = out if out is not None else torch.empty((T, D), dtype=x.dtype, device=dev)
-    fs = torch.empty((N, D), dtype=torch.float32, device=dev) if output_final_state else None
+    o = out if out is not None else _empty(x)
+    fs = _empty(x, (N, D), torch.float32) if output_final_state else None
     cp = None
     if return_checkpoints:
-        cp = torch.empty((-(-T // GDP_SCAN_CHECKPOINT_ROWS), D), dtype=torch.float32, device=dev)
+        cp = _empty(x, (-(-T // GDP_SCAN_CHECKPOINT_ROWS), D), torch.float32)
     gdp_gated_scan(x, g_log, cu_seqlens, complement_input, initial_state, output_final_state, state_cache,
                    state_indices, return_checkpoints, o, fs, cp,
-                   _workspace(gdp_gated_scan_workspace_bytes(T, N, D), dev))
+                   _workspace(x, gdp_gated_scan_workspace_bytes(T, N, D)))
     return (o, fs, cp) if return_checkpoints else (o, fs)
 
 
 def gated_scan_decode(x, g_log, state_cache, state_indices, complement_input=False, out=None):
     """Allocating front end of the recurrence's single-token step: returns o [N, D] in x's dtype; the
     state cache [S, D] is updated in place."""
-    o = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    o = out if out is not None else _empty(x)
     gdp_gated_scan_decode(x, g_log, complement_input, state_cache, state_indices, o)
     return o
 
@@ -564,12 +574,11 @@ def gated_scan_backward(x, g_log, cu_seqlens, d_o, d_final_state=None, initial_s
     state).  Without the forward call's `checkpoints` the states are formed again first."""
     T, D = x.shape
     N = cu_seqlens.shape[0] - 1
-    dev = x.device
-    dx = torch.empty((T, D), dtype=x.dtype if grads_like_inputs else torch.float32, device=dev)
-    dg = torch.empty((T, D), dtype=g_log.dtype if grads_like_inputs else torch.float32, device=dev)
-    ds0 = torch.empty((N, D), dtype=torch.float32, device=dev) if initial_state is not None else None
+    dx = _empty(x, (T, D), x.dtype if grads_like_inputs else torch.float32)
+    dg = _empty(x, (T, D), g_log.dtype if grads_like_inputs else torch.float32)
+    ds0 = _empty(x, (N, D), torch.float32) if initial_state is not None else None
     gdp_gated_scan_backward(x, g_log, cu_seqlens, complement_input, initial_state, checkpoints, d_o, d_final_state,
-                            dx, dg, ds0, _workspace(gdp_gated_scan_backward_workspace_bytes(T, N, D), dev))
+                            dx, dg, ds0, _workspace(x, gdp_gated_scan_backward_workspace_bytes(T, N, D)))
     return {"dx": dx, "dg_log": dg, "d_initial_state": ds0}
 
 
@@ -577,7 +586,7 @@ def group_norm(x, weight=None, bias=None, gate=None, activation=None, subtract_m
     """Allocating front end of the group norm over the last dimension of x [T, G, V] (the heads' outputs,
     channels last): act(n) without a gate, n * act(gate) with one; weight and bias [V] or [G, V];
     activation None, "silu" or "sigmoid"; subtract_mean=False is the root mean square norm."""
-    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = out if out is not None else _empty(x)
     gdp_group_norm(x, weight, bias, gate, activation, subtract_mean, eps, y)
     return y
 
@@ -587,10 +596,9 @@ def group_norm_backward(x, d_y, weight=None, bias=None, gate=None, activation=No
     dweight and dbias (float32), None where the forward call had none.  dx is what the recurrences'
     backward calls take as d_o."""
     T, G, V = x.shape
-    dev = x.device
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dz = torch.empty(x.shape, dtype=x.dtype, device=dev) if gate is not None else None
-    dw, db = (None if p is None else torch.empty(p.shape, dtype=torch.float32, device=dev) for p in (weight, bias))
+    dx = _empty(x)
+    dz = _empty(x) if gate is not None else None
+    dw, db = (None if p is None else _empty(x, p.shape, torch.float32) for p in (weight, bias))
     gdp_group_norm_backward(x, weight, bias, gate, activation, subtract_mean, eps, d_y, dx, dw, db, dz,
-                            _workspace(gdp_group_norm_backward_workspace_bytes(T, G, V), dev))
+                            _workspace(x, gdp_group_norm_backward_workspace_bytes(T, G, V)))
     return {"dx": dx, "dweight": dw, "dbias": db, "dgate": dz}
