@@ -5,9 +5,9 @@
 //
 // The recurrence is a composition of affine maps h -> A h + B, so a block of rows
 // can be reduced to one pair (A, B) per channel before the state that enters it is
-// known.  The token stream (all sequences end to end) is cut into tiles of 64 rows;
-// a workgroup of 8 waves takes one tile of one channel block, wave w rows 8 w ..
-// 8 w + 7, a lane VEC neighbouring channels.  Every input is loaded once into
+// known.  The token stream (all sequences end to end) is cut into tiles of 8 R rows;
+// a workgroup of 8 waves takes one tile of one channel block, wave w rows R w ..
+// R w + R - 1, a lane VEC neighbouring channels.  Every input is loaded once into
 // registers and every output written once:
 //   1. the rows' decays and terms, and their maps composed: per wave, then (through
 //      LDS) per tile;
@@ -19,10 +19,11 @@
 //
 // Handing on the states.  A word holds (A, B) of one tile; a tile that knows its
 // entering state h, or needs none, holds (0, A h + B) instead: A = 0 says that
-// nothing before the tile matters.  A workgroup reads the words of the WIN tiles
-// before its own until for every channel it has found one with A = 0 and all those
-// between, and composes them from that one forward.  That is the sequential fold,
-// whichever tile the fold starts from, so the result does not depend on timing.
+// nothing before the tile matters.  A lane reads the words of the WINDOW tiles
+// before its own until it has found one with A = 0 and all those between, and
+// composes them from that one forward.  That is the sequential fold, whichever tile
+// the fold starts from, so the result does not depend on timing.  While none has
+// A = 0 only the farthest is read again: the known states reach it first.
 // The words are written and read with relaxed agent-scope atomics (8 bytes, so a
 // pair is whole), which go past the XCDs' own caches; all-ones bits (two NaNs that
 // no published pair has) mean not yet written, and a fill kernel sets them before.
@@ -40,19 +41,44 @@
 namespace gdp {
 namespace {
 
-constexpr int WAVES = 8, R = SCAN_ROWS / WAVES, THREADS = 64 * WAVES;
+constexpr int WAVES = 8, THREADS = 64 * WAVES;
+constexpr int WINDOW = 16;  // tiles before this one that a lane looks at
 constexpr uint64_t NOT_WRITTEN = ~0ull;
 
 template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Pack { T v[VEC]; };
 
-template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> load_pack(const T *p) {
-  return *(const Pack<T, VEC> *)p;
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// channel ch of a row: the row's address is the same for a whole wave (scalar
+// registers), the lane's part a 32-bit byte offset
+template <typename T> __device__ __forceinline__ T *at(T *row, uint32_t ch) {
+  return (T *)((char *)row + (uint32_t)(ch * sizeof(T)));
 }
-template <typename T, int VEC> __device__ __forceinline__ void store_pack(T *p, const float (&x)[VEC]) {
+template <typename T> __device__ __forceinline__ const T *at(const T *row, uint32_t ch) {
+  return (const T *)((const char *)row + (uint32_t)(ch * sizeof(T)));
+}
+template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> load_pack(const T *row, uint32_t ch) {
+  return *(const Pack<T, VEC> *)at(row, ch);
+}
+template <typename T, int VEC> __device__ __forceinline__ void store_pack(T *row, uint32_t ch, const float (&x)[VEC]) {
   Pack<T, VEC> s;
 #pragma unroll
   for (int c = 0; c < VEC; ++c) s.v[c] = (T)x[c];
-  *(Pack<T, VEC> *)p = s;
+  *(Pack<T, VEC> *)at(row, ch) = s;
+}
+
+// R rows from t0 on; rows behind the last one (T > 0) read that row again
+template <int R, typename T, int VEC>
+__device__ __forceinline__ void load_rows(Pack<T, VEC> (&v)[R], const T *base, int64_t stride, int64_t t0, int64_t T_,
+                                          uint32_t ch) {
+  if (t0 + R <= T_) {
+    const T *row = base + t0 * stride;
+#pragma unroll
+    for (int r = 0; r < R; ++r, row += stride) v[r] = load_pack<T, VEC>(row, ch);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = load_pack<T, VEC>(base + (t0 + r < T_ ? t0 + r : T_ - 1) * stride, ch);
+  }
 }
 
 // the map (A, B) applied to h; A = 0 drops h, also one that is not finite
@@ -63,22 +89,18 @@ __device__ __forceinline__ uint64_t make_word(float A, float B) {
   return ((uint64_t)a << 32) | __float_as_uint(B);
 }
 
-template <int VEC> struct Shared {
-  static constexpr int NCH = 64 * VEC, PARTS = THREADS / NCH;
-  static constexpr int Q = VEC == 4 ? 8 : 4;  // words a thread reads per round
-  static constexpr int WIN = PARTS * Q;       // tiles before this one that a round looks at
+template <int VEC, int R> struct Shared {
+  static constexpr int NCH = 64 * VEC, ROWS = WAVES * R;
   float A[WAVES][NCH], B[WAVES][NCH];
-  uint64_t win[WIN][NCH];
-  int start_id[SCAN_ROWS], end_id[SCAN_ROWS];  // sequence that starts / ends at a row of the tile, or -1
+  int start_id[ROWS], end_id[ROWS];  // sequence that starts / ends at a row of the tile, or -1
   int ticket;
 };
 
-// Marks the tile's rows [r0, r0 + 64) where sequences start and end (nonempty
-// ones), in LDS and as two masks.  Boundaries are read 512 at a time; with more
-// sequences, the one that holds r0 is found first in 512-way steps.  Bad contents
-// give wrong marks, with ids in [0, N).
-struct Marks { uint64_t start, end; };
-template <typename S> __device__ __forceinline__ Marks mark_rows(S &sh, const ScanArgs &a, int64_t r0, int tid) {
+// Marks the tile's rows where sequences start and end (nonempty ones), in LDS.
+// Boundaries are read 512 at a time; with more sequences, the one that holds the
+// first row r0 is found first in 512-way steps.  Bad contents give wrong marks,
+// with ids in [0, N).
+template <typename S> __device__ __forceinline__ void mark_rows(S &sh, const ScanArgs &a, int64_t r0, int tid) {
   int64_t lo = 0, hi = a.N;
   while (hi - lo > THREADS) {  // the last sequence that starts at or before r0
     const int64_t step = (hi - lo + THREADS - 1) / THREADS, i = lo + tid * step;
@@ -96,69 +118,73 @@ template <typename S> __device__ __forceinline__ Marks mark_rows(S &sh, const Sc
     if (i < a.N) {
       const int64_t s = bound_at(a.cu, a.cu_is64, i, a.T) - r0, e = bound_at(a.cu, a.cu_is64, i + 1, a.T) - r0 - 1;
       if (e >= s) {
-        if (s >= 0 && s < SCAN_ROWS) sh.start_id[s] = (int)i;
-        if (e >= 0 && e < SCAN_ROWS) sh.end_id[e] = (int)i;
+        if (s >= 0 && s < S::ROWS) sh.start_id[s] = (int)i;
+        if (e >= 0 && e < S::ROWS) sh.end_id[e] = (int)i;
       }
-      past = s >= SCAN_ROWS;
+      past = s >= S::ROWS;
     }
     if (__syncthreads_or(past)) break;
   }
-  return Marks{__ballot(sh.start_id[tid & 63] >= 0), __ballot(sh.end_id[tid & 63] >= 0)};
+}
+// a wave's rows that are marked, as a mask
+template <int R> __device__ __forceinline__ uint32_t marked(const int *ids, int w, int lane) {
+  return (uint32_t)__ballot(lane < R && ids[w * R + (lane & (R - 1))] >= 0);
 }
 
-// The state entering this tile (per channel, in threads tid < NCH) from the words
-// of the `count` tiles before it; `word(i)` is the address of the i-th before it.
-template <int VEC, typename F>
-__device__ __forceinline__ float entering(Shared<VEC> &sh, int64_t count, bool live, int tid, F word) {
-  using S = Shared<VEC>;
-  const int part = tid / S::NCH, c = tid % S::NCH;
-  float h = 0.f;
-  for (;;) {
-    uint64_t w[S::Q];
+// The state entering this tile, of one channel, from the words of the `count` tiles
+// before it: `word` is the nearest one's, the others lie `step` words apart.
+__device__ __forceinline__ float entering(const uint64_t *word, int64_t step, int count, bool live) {
+  uint64_t v[WINDOW];
+  auto read = [&](const uint64_t *w, int i) {  // tiles before the first count as a state of 0
+    return live && i < count ? __hip_atomic_load(w + i * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+  };
+  auto first_part = [](uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); };
+  // the nearest word with A = 0 among the first n, if all words before it are there
+  auto resolved = [&](int n) {
+    bool open = true, found = false;
 #pragma unroll
-    for (int q = 0; q < S::Q; ++q) {
-      const int i = part * S::Q + q;
-      w[q] = live && i < count ? __hip_atomic_load(word(i), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+    for (int i = 0; i < WINDOW; ++i) {
+      if (i >= n) break;
+      const bool there = v[i] != NOT_WRITTEN;
+      found = found || (open && there && first_part(v[i]) == 0.f);
+      open = open && there && !found;
     }
+    return found;
+  };
+  constexpr int NEAR = WINDOW / 2;
 #pragma unroll
-    for (int q = 0; q < S::Q; ++q) sh.win[part * S::Q + q][c] = w[q];
-    __syncthreads();
-    bool found = true;
-    if (tid < S::NCH) {
-      int n = 0;
-      found = false;
-      for (; n < S::WIN; ++n) {
-        const uint64_t v = sh.win[n][c];
-        if (v == NOT_WRITTEN) break;
-        if (__uint_as_float((uint32_t)(v >> 32)) == 0.f) {
-          found = true;
-          break;
-        }
-      }
-      if (found) {
-        h = __uint_as_float((uint32_t)sh.win[n][c]);
-        while (--n >= 0) {
-          const uint64_t v = sh.win[n][c];
-          h = fmaf(__uint_as_float((uint32_t)(v >> 32)), h, __uint_as_float((uint32_t)v));
-        }
-      }
+  for (int i = 0; i < NEAR; ++i) v[i] = read(word, i);
+#pragma unroll
+  for (int i = NEAR; i < WINDOW; ++i) v[i] = NOT_WRITTEN;
+  if (!__all(resolved(NEAR))) {
+#pragma unroll
+    for (int i = NEAR; i < WINDOW; ++i) v[i] = read(word, i);
+    while (!__all(resolved(WINDOW))) {
+      __builtin_amdgcn_s_sleep(1);
+      asm volatile("" : "+v"(word));  // or every word's address is kept in registers over the loop
+#pragma unroll
+      for (int i = 0; i < WINDOW; ++i)
+        if (i == WINDOW - 1 || v[i] == NOT_WRITTEN) v[i] = read(word, i);
     }
-    if (__syncthreads_and(found)) return h;
-    __builtin_amdgcn_s_sleep(1);
   }
+  float h = 0.f;
+#pragma unroll
+  for (int i = WINDOW - 1; i >= 0; --i)
+    if (v[i] != NOT_WRITTEN) h = apply(first_part(v[i]), h, __uint_as_float((uint32_t)v[i]));
+  return h;
 }
 
 // The workgroup's job: its ticket (the counter starts at -1), or the block's own
 // index when nothing is handed on.  Clears the row marks.
 template <typename S> __device__ __forceinline__ int take_ticket(S &sh, const ScanArgs &a, bool hand_on, int tid) {
-  if (tid < SCAN_ROWS) sh.start_id[tid] = sh.end_id[tid] = -1;
+  if (tid < S::ROWS) sh.start_id[tid] = sh.end_id[tid] = -1;
   if (!hand_on) {
     __syncthreads();
     return (int)blockIdx.x;
   }
   if (tid == 0) sh.ticket = atomicAdd((int *)a.ws, 1) + 1;
   __syncthreads();
-  return sh.ticket;
+  return __builtin_amdgcn_readfirstlane(sh.ticket);
 }
 
 // The jobs behind the tiles: 64 sequences each, whose empty ones hand src (or
@@ -179,57 +205,65 @@ __device__ __forceinline__ void empty_sequences(const ScanArgs &a, int64_t job, 
   }
 }
 
-template <typename XT, typename GT, int VEC, bool COMPL>
+template <typename XT, typename GT, int VEC, int R, bool COMPL>
 __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int tiles, int blocks) {
-  using S = Shared<VEC>;
+  using S = Shared<VEC, R>;
   __shared__ S sh;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool hand_on = tiles > 1;
   const int ticket = take_ticket(sh, a, hand_on, tid);
-  const int tile = __builtin_amdgcn_readfirstlane(ticket / blocks);
+  const int tile = ticket / blocks;
   if (tile >= tiles) {
     empty_sequences(a, ticket - tiles * blocks, a.s0, a.final_state, tid);
     return;
   }
-  const int64_t first = (int64_t)(ticket % blocks) * S::NCH;  // the block's first channel
-  const int64_t r0 = (int64_t)tile * SCAN_ROWS;
+  const int first = (ticket % blocks) * S::NCH;  // the block's first channel
+  const int64_t r0 = (int64_t)tile * S::ROWS;
   const bool mine = first + lane * VEC < a.D;
-  const int64_t ch = mine ? first + lane * VEC : 0;
+  const uint32_t ch = mine ? first + lane * VEC : 0;
   const int64_t t0 = r0 + w * R;
 
   Pack<GT, VEC> graw[R];
   Pack<XT, VEC> xraw[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {  // rows behind the last one read that row again
-    const int64_t t = t0 + r < a.T ? t0 + r : a.T - 1;
-    graw[r] = load_pack<GT, VEC>((const GT *)a.g + t * a.g_st + ch);
-    xraw[r] = load_pack<XT, VEC>((const XT *)a.x + t * a.x_st + ch);
-  }
+  load_rows<R>(graw, (const GT *)a.g, a.g_st, t0, a.T, ch);
+  load_rows<R>(xraw, (const XT *)a.x, a.x_st, t0, a.T, ch);
   const int64_t c0 = bound_at(a.cu, a.cu_is64, 0, a.T), cN = bound_at(a.cu, a.cu_is64, a.N, a.T);
-  const Marks marks = mark_rows(sh, a, r0, tid);
-  const uint32_t starts = (uint32_t)(marks.start >> (w * R)) & 0xff, ends = (uint32_t)(marks.end >> (w * R)) & 0xff;
+  mark_rows(sh, a, r0, tid);
+  const uint32_t starts = marked<R>(sh.start_id, w, lane), ends = marked<R>(sh.end_id, w, lane);
 
-  float d[R][VEC], u[R][VEC], sum[VEC] = {}, h[VEC] = {};
+  float d[R][VEC], u[COMPL ? R : 1][VEC], sum[VEC] = {}, h[VEC] = {};
+  auto restart = [&](int r) {  // a sequence's first row
+    if (a.s0) {
+      const Pack<float, VEC> s0 = load_pack<float, VEC>(a.s0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch);
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) h[c] = s0.v[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) h[c] = 0.f;
+    }
+  };
 #pragma unroll
   for (int r = 0; r < R; ++r) {
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
-      const float g = (float)graw[r].v[c], x = (float)xraw[r].v[c];
+      const float g = (float)graw[r].v[c];
       d[r][c] = decay(g);
-      u[r][c] = COMPL ? one_minus_decay(g, d[r][c]) * x : x;
+      if (COMPL) u[r][c] = one_minus_decay(g, d[r][c]) * (float)xraw[r].v[c];
       sum[c] += g;
     }
-    if (starts >> r & 1) {  // the sequence's first row: its initial state's share joins the term
-      if (a.s0) {
-        const Pack<float, VEC> s0 = load_pack<float, VEC>(a.s0 + (int64_t)sh.start_id[w * R + r] * a.D + ch);
+  }
+  auto advance = [&](int r) {
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) u[r][c] = fmaf(d[r][c], s0.v[c], u[r][c]);
-      }
+    for (int c = 0; c < VEC; ++c) h[c] = fmaf(d[r][c], h[c], COMPL ? u[r][c] : (float)xraw[r].v[c]);
+  };
+  if (starts == 0) {
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) h[c] = u[r][c];
-    } else {
+    for (int r = 0; r < R; ++r) advance(r);
+  } else {
 #pragma unroll
-      for (int c = 0; c < VEC; ++c) h[c] = fmaf(d[r][c], h[c], u[r][c]);
+    for (int r = 0; r < R; ++r) {
+      if (starts >> r & 1) restart(r);
+      advance(r);
     }
   }
 #pragma unroll
@@ -239,56 +273,64 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int ti
   }
   __syncthreads();
 
-  const bool needs = tile > 0 && !(marks.start & 1) && r0 >= c0 && r0 < cN;
-  const int col = tid % S::NCH;
-  const bool live = first + col < a.D;
-  float carry = 0.f;
-  if (hand_on) {
-    float A = 1.f, B = 0.f;
-    if (tid < S::NCH) {
+  if (tid < S::NCH) {  // lane tid: channel first + tid
+    const bool live = first + tid < a.D, covered = r0 >= c0 && r0 < cN;
+    float carry = 0.f;
+    if (hand_on) {
+      const bool needs = tile > 0 && sh.start_id[0] < 0 && covered;
+      float A = 1.f, B = 0.f;
 #pragma unroll
       for (int v = 0; v < WAVES; ++v) {
-        B = apply(sh.A[v][col], B, sh.B[v][col]);
-        A *= sh.A[v][col];
+        B = apply(sh.A[v][tid], B, sh.B[v][tid]);
+        A *= sh.A[v][tid];
       }
       if (!needs) A = 0.f;
+      uint64_t *words = (uint64_t *)((char *)a.ws + 256);
+      const uint32_t col = first + tid;
+      const bool publish = live && tile + 1 < tiles;
+      if (publish)
+        __hip_atomic_store(at(words + (int64_t)tile * a.D, col), make_word(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (needs) {
+        carry = entering(at(words + (int64_t)(tile - 1) * a.D, col), -a.D, tile, live);
+        if (publish && A != 0.f)
+          __hip_atomic_store(at(words + (int64_t)tile * a.D, col), make_word(0.f, fmaf(A, carry, B)), __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+      }
     }
-    uint64_t *words = (uint64_t *)((char *)a.ws + 256) + first + col;
-    const bool publish = tid < S::NCH && live && tile + 1 < tiles;
-    if (publish)
-      __hip_atomic_store(words + (int64_t)tile * a.D, make_word(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (needs) {
-      carry = entering(sh, tile, live, tid, [&](int i) { return words + (int64_t)(tile - 1 - i) * a.D; });
-      if (publish && A != 0.f)
-        __hip_atomic_store(words + (int64_t)tile * a.D, make_word(0.f, fmaf(A, carry, B)), __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
-    }
-  }
-  if (tid < S::NCH) {  // the state entering each wave's rows, in place of its A
-    if (a.checkpoints && live && r0 >= c0 && r0 < cN) a.checkpoints[(int64_t)tile * a.D + first + col] = carry;
 #pragma unroll
-    for (int v = 0; v < WAVES; ++v) {
-      const float next = apply(sh.A[v][col], carry, sh.B[v][col]);
-      sh.A[v][col] = carry;
+    for (int v = 0; v < WAVES; ++v) {  // the state entering each wave's rows, in place of its A
+      if (a.checkpoints && v * R % SCAN_ROWS == 0 && live && r0 + v * R >= c0 && r0 + v * R < cN)
+        a.checkpoints[(r0 + v * R) / SCAN_ROWS * a.D + first + tid] = carry;
+      const float next = apply(sh.A[v][tid], carry, sh.B[v][tid]);
+      sh.A[v][tid] = carry;
       carry = next;
     }
   }
   __syncthreads();
 
+  if (!a.o) return;  // states only
 #pragma unroll
   for (int c = 0; c < VEC; ++c) h[c] = sh.A[w][lane * VEC + c];
+  XT *out = (XT *)a.o + t0 * a.o_st;
+  if ((starts | ends) == 0 && t0 >= c0 && t0 + R <= cN) {
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < R; ++r, out += a.o_st) {
+      advance(r);
+      if (mine) store_pack<XT, VEC>(out, ch, h);
+    }
+    return;
+  }
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) h[c] = starts >> r & 1 ? u[r][c] : fmaf(d[r][c], h[c], u[r][c]);
-    const int64_t t = t0 + r;
-    if (a.o && mine && t >= c0 && t < cN) store_pack<XT, VEC>((XT *)a.o + t * a.o_st + ch, h);
+  for (int r = 0; r < R; ++r, out += a.o_st) {
+    if (starts >> r & 1) restart(r);
+    advance(r);
+    if (mine && t0 + r >= c0 && t0 + r < cN) store_pack<XT, VEC>(out, ch, h);
     if (ends >> r & 1) {
-      const int64_t i = sh.end_id[w * R + r];
-      if (a.final_state && mine) store_pack<float, VEC>(a.final_state + i * a.D + ch, h);
+      const int64_t i = uniform(sh.end_id[w * R + r]);
+      if (a.final_state && mine) store_pack<float, VEC>(a.final_state + i * a.D, ch, h);
       if (a.cache) {
         const int64_t slot = index_at(a.slots, a.slots_is64, i);
-        if (slot >= 0 && slot < a.num_slots && mine) store_pack<float, VEC>(a.cache + slot * a.D + ch, h);
+        if (slot >= 0 && slot < a.num_slots && mine) store_pack<float, VEC>(a.cache + slot * a.D, ch, h);
       }
     }
   }
@@ -300,40 +342,35 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int ti
 // handed on between tiles the same way.  The states are formed again from the
 // checkpoint at the tile's first row.
 template <typename XT, typename GT, int VEC, bool COMPL>
-__global__ void __launch_bounds__(THREADS, 2)
-    gdp_scan_backward_kernel(ScanArgs a, int tiles, int blocks) {
-  using S = Shared<VEC>;
+__global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs a, int tiles, int blocks) {
+  constexpr int R = SCAN_ROWS / WAVES;
+  using S = Shared<VEC, R>;
   __shared__ S sh;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool hand_on = tiles > 1;
   const int ticket = take_ticket(sh, a, hand_on, tid);
-  const int tile = __builtin_amdgcn_readfirstlane(tiles - 1 - ticket / blocks);
+  const int tile = tiles - 1 - ticket / blocks;
   if (tile < 0) {
     empty_sequences(a, ticket - tiles * blocks, a.dfinal, a.ds0, tid);
     return;
   }
-  const int64_t first = (int64_t)(ticket % blocks) * S::NCH;
+  const int first = (ticket % blocks) * S::NCH;
   const int64_t r0 = (int64_t)tile * SCAN_ROWS;
   const bool mine = first + lane * VEC < a.D;
-  const int64_t ch = mine ? first + lane * VEC : 0;
+  const uint32_t ch = mine ? first + lane * VEC : 0;
   const int64_t t0 = r0 + w * R;
 
   Pack<GT, VEC> graw[R];
   Pack<XT, VEC> xraw[R], draw[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int64_t t = t0 + r < a.T ? t0 + r : a.T - 1;
-    graw[r] = load_pack<GT, VEC>((const GT *)a.g + t * a.g_st + ch);
-    xraw[r] = load_pack<XT, VEC>((const XT *)a.x + t * a.x_st + ch);
-    draw[r] = load_pack<XT, VEC>((const XT *)a.dout + t * a.do_st + ch);
-  }
-  const int col = tid % S::NCH;
-  const bool live = first + col < a.D;
+  load_rows<R>(graw, (const GT *)a.g, a.g_st, t0, a.T, ch);
+  load_rows<R>(xraw, (const XT *)a.x, a.x_st, t0, a.T, ch);
+  load_rows<R>(draw, (const XT *)a.dout, a.do_st, t0, a.T, ch);
+  const bool live = tid < S::NCH && first + tid < a.D;  // lane tid < NCH: channel first + tid of the hand-over
   float state = 0.f;
-  if (tid < S::NCH && live) state = a.checkpoints[(int64_t)tile * a.D + first + col];
+  if (live) state = a.checkpoints[(int64_t)tile * a.D + first + tid];
   const int64_t c0 = bound_at(a.cu, a.cu_is64, 0, a.T), cN = bound_at(a.cu, a.cu_is64, a.N, a.T);
-  const Marks marks = mark_rows(sh, a, r0, tid);
-  const uint32_t starts = (uint32_t)(marks.start >> (w * R)) & 0xff, ends = (uint32_t)(marks.end >> (w * R)) & 0xff;
+  mark_rows(sh, a, r0, tid);
+  const uint32_t starts = marked<R>(sh.start_id, w, lane), ends = marked<R>(sh.end_id, w, lane);
 
   // the states before the wave's rows: the forward maps of the waves, composed
   float d[R][VEC], m[COMPL ? R : 1][VEC], h[VEC] = {}, sum[VEC] = {};
@@ -341,7 +378,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   for (int r = 0; r < R; ++r) {
     float s0[VEC] = {};
     if ((starts >> r & 1) && a.s0) {
-      const Pack<float, VEC> p = load_pack<float, VEC>(a.s0 + (int64_t)sh.start_id[w * R + r] * a.D + ch);
+      const Pack<float, VEC> p = load_pack<float, VEC>(a.s0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch);
 #pragma unroll
       for (int c = 0; c < VEC; ++c) s0[c] = p.v[c];
     }
@@ -364,8 +401,8 @@ __global__ void __launch_bounds__(THREADS, 2)
   if (tid < S::NCH) {
 #pragma unroll
     for (int v = 0; v < WAVES; ++v) {
-      const float next = apply(sh.A[v][col], state, sh.B[v][col]);
-      sh.A[v][col] = state;
+      const float next = apply(sh.A[v][tid], state, sh.B[v][tid]);
+      sh.A[v][tid] = state;
       state = next;
     }
   }
@@ -378,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   for (int r = 0; r < R; ++r) {
     if (starts >> r & 1) {
       if (a.s0) {
-        const Pack<float, VEC> s0 = load_pack<float, VEC>(a.s0 + (int64_t)sh.start_id[w * R + r] * a.D + ch);
+        const Pack<float, VEC> s0 = load_pack<float, VEC>(a.s0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch);
 #pragma unroll
         for (int c = 0; c < VEC; ++c) h[c] = s0.v[c];
       } else {
@@ -396,7 +433,7 @@ __global__ void __launch_bounds__(THREADS, 2)
   float e[VEC] = {};
   auto last_row = [&](int r, float (&e)[VEC]) {  // a sequence's last row: e comes from d_final_state
     if (a.dfinal) {
-      const Pack<float, VEC> f = load_pack<float, VEC>(a.dfinal + (int64_t)sh.end_id[w * R + r] * a.D + ch);
+      const Pack<float, VEC> f = load_pack<float, VEC>(a.dfinal + (int64_t)uniform(sh.end_id[w * R + r]) * a.D, ch);
 #pragma unroll
       for (int c = 0; c < VEC; ++c) e[c] = f.v[c];
     } else {
@@ -418,35 +455,34 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
   __syncthreads();
 
-  const int64_t rl = r0 + SCAN_ROWS - 1;  // the tile's last row
-  const bool needs = tile + 1 < tiles && !(marks.end >> 63) && rl >= c0 && rl < cN;
-  float carry = 0.f;
-  if (hand_on) {
-    float A = 1.f, B = 0.f;
-    if (tid < S::NCH) {
+  if (tid < S::NCH) {
+    const int64_t rl = r0 + SCAN_ROWS - 1;  // the tile's last row
+    float carry = 0.f;
+    if (hand_on) {
+      const bool needs = tile + 1 < tiles && sh.end_id[SCAN_ROWS - 1] < 0 && rl >= c0 && rl < cN;
+      float A = 1.f, B = 0.f;
 #pragma unroll
       for (int v = WAVES - 1; v >= 0; --v) {
-        B = apply(sh.A[v][col], B, sh.B[v][col]);
-        A *= sh.A[v][col];
+        B = apply(sh.A[v][tid], B, sh.B[v][tid]);
+        A *= sh.A[v][tid];
       }
       if (!needs) A = 0.f;
+      uint64_t *words = (uint64_t *)((char *)a.ws + 256);
+      const uint32_t col = first + tid;
+      const bool publish = live && tile > 0;
+      if (publish)
+        __hip_atomic_store(at(words + (int64_t)tile * a.D, col), make_word(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (needs) {
+        carry = entering(at(words + (int64_t)(tile + 1) * a.D, col), a.D, tiles - 1 - tile, live);
+        if (publish && A != 0.f)
+          __hip_atomic_store(at(words + (int64_t)tile * a.D, col), make_word(0.f, fmaf(A, carry, B)), __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+      }
     }
-    uint64_t *words = (uint64_t *)((char *)a.ws + 256) + first + col;
-    const bool publish = tid < S::NCH && live && tile > 0;
-    if (publish)
-      __hip_atomic_store(words + (int64_t)tile * a.D, make_word(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (needs) {
-      carry = entering(sh, tiles - 1 - tile, live, tid, [&](int i) { return words + (int64_t)(tile + 1 + i) * a.D; });
-      if (publish && A != 0.f)
-        __hip_atomic_store(words + (int64_t)tile * a.D, make_word(0.f, fmaf(A, carry, B)), __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
-    }
-  }
-  if (tid < S::NCH) {
 #pragma unroll
     for (int v = WAVES - 1; v >= 0; --v) {
-      const float next = apply(sh.A[v][col], carry, sh.B[v][col]);
-      sh.A[v][col] = carry;
+      const float next = apply(sh.A[v][tid], carry, sh.B[v][tid]);
+      sh.A[v][tid] = carry;
       carry = next;
     }
   }
@@ -468,13 +504,13 @@ __global__ void __launch_bounds__(THREADS, 2)
       e[c] *= d[r][c];
     }
     if (mine && t < a.T) {
-      if (a.dx_f32) store_pack<float, VEC>((float *)a.dx + t * a.dx_st + ch, dx);
-      else store_pack<XT, VEC>((XT *)a.dx + t * a.dx_st + ch, dx);
-      if (a.dg_f32) store_pack<float, VEC>((float *)a.dg + t * a.dg_st + ch, dg);
-      else store_pack<GT, VEC>((GT *)a.dg + t * a.dg_st + ch, dg);
+      if (a.dx_f32) store_pack<float, VEC>((float *)a.dx + t * a.dx_st, ch, dx);
+      else store_pack<XT, VEC>((XT *)a.dx + t * a.dx_st, ch, dx);
+      if (a.dg_f32) store_pack<float, VEC>((float *)a.dg + t * a.dg_st, ch, dg);
+      else store_pack<GT, VEC>((GT *)a.dg + t * a.dg_st, ch, dg);
     }
     if ((starts >> r & 1) && a.ds0 && mine)
-      store_pack<float, VEC>(a.ds0 + (int64_t)sh.start_id[w * R + r] * a.D + ch, e);
+      store_pack<float, VEC>(a.ds0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch, e);
   }
 }
 
@@ -508,23 +544,44 @@ __global__ void __launch_bounds__(256) gdp_scan_fill_kernel(uint4 *p, int64_t n)
     p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
 }
 
-bool aligned(const void *p, int64_t stride, int es) { return !p || (((uintptr_t)p & (4 * es - 1)) == 0 && stride % 4 == 0); }
+// whether pieces of `vec` elements of es bytes are aligned in every row
+bool aligned(const void *p, int64_t stride, int es, int vec) {
+  return !p || (((uintptr_t)p & (vec * es - 1)) == 0 && stride % vec == 0);
+}
 
 struct Grid { int tiles, blocks; unsigned jobs; };
 
-template <int VEC> Grid grid_of(const ScanArgs &a, bool empties) {
+Grid grid_of(const ScanArgs &a, int rows, int channels, bool empties) {
   Grid g;
-  g.tiles = (int)((a.T + SCAN_ROWS - 1) / SCAN_ROWS);
-  g.blocks = (int)((a.D + 64 * VEC - 1) / (64 * VEC));
+  g.tiles = (int)((a.T + rows - 1) / rows);
+  g.blocks = (int)((a.D + channels - 1) / channels);
   g.jobs = (unsigned)((int64_t)g.tiles * g.blocks + (empties ? (a.N + 63) / 64 : 0));
   return g;
 }
 
 hipError_t fill_words(const ScanArgs &a, const Grid &g, hipStream_t stream) {
   if (g.tiles <= 1) return hipSuccess;
-  const int64_t n = (int64_t)scan_state_bytes(a.T, a.D) / 16, want = (n + 255) / 256;
+  const int64_t n = (256 + (int64_t)g.tiles * a.D * 8 + 15) / 16, want = (n + 255) / 256;
   hipLaunchKernelGGL(gdp_scan_fill_kernel, dim3((unsigned)(want < 2048 ? want : 2048)), dim3(256), 0, stream,
                      (uint4 *)a.ws, n);
+  return hipGetLastError();
+}
+
+template <typename XT, typename GT, int VEC, int R> hipError_t run_scan(const ScanArgs &a, hipStream_t stream) {
+  const Grid k = grid_of(a, WAVES * R, 64 * VEC, a.N > 0 && (a.final_state || a.cache));
+  if (k.jobs == 0) return hipSuccess;
+  if (hipError_t e = fill_words(a, k, stream)) return e;
+  auto *kernel = a.complement ? gdp_scan_kernel<XT, GT, VEC, R, true> : gdp_scan_kernel<XT, GT, VEC, R, false>;
+  hipLaunchKernelGGL(kernel, dim3(k.jobs), dim3(THREADS), 0, stream, a, k.tiles, k.blocks);
+  return hipGetLastError();
+}
+
+template <typename XT, typename GT, int VEC> hipError_t run_backward(const ScanArgs &a, hipStream_t stream) {
+  const Grid k = grid_of(a, SCAN_ROWS, 64 * VEC, a.N > 0 && a.ds0);
+  if (k.jobs == 0) return hipSuccess;
+  if (hipError_t e = fill_words(a, k, stream)) return e;
+  auto *kernel = a.complement ? gdp_scan_backward_kernel<XT, GT, VEC, true> : gdp_scan_backward_kernel<XT, GT, VEC, false>;
+  hipLaunchKernelGGL(kernel, dim3(k.jobs), dim3(THREADS), 0, stream, a, k.tiles, k.blocks);
   return hipGetLastError();
 }
 
@@ -544,17 +601,11 @@ hipError_t launch_scan(const ScanArgs &a, int xt, int gt, hipStream_t stream) {
   return by_types(xt, gt, [&](auto x, auto g) {
     using XT = decltype(x);
     using GT = decltype(g);
-    const bool vec = a.D % 4 == 0 && aligned(a.x, a.x_st, sizeof(XT)) && aligned(a.g, a.g_st, sizeof(GT)) &&
-                     aligned(a.o, a.o_st, sizeof(XT)) && aligned(a.s0, 0, 4) && aligned(a.final_state, 0, 4) &&
-                     aligned(a.cache, 0, 4);
-    const bool empties = a.N > 0 && (a.final_state || a.cache);
-    const Grid k = vec ? grid_of<4>(a, empties) : grid_of<1>(a, empties);
-    if (k.jobs == 0) return hipSuccess;
-    if (hipError_t e = fill_words(a, k, stream)) return e;
-    auto *kernel = vec ? (a.complement ? gdp_scan_kernel<XT, GT, 4, true> : gdp_scan_kernel<XT, GT, 4, false>)
-                       : (a.complement ? gdp_scan_kernel<XT, GT, 1, true> : gdp_scan_kernel<XT, GT, 1, false>);
-    hipLaunchKernelGGL(kernel, dim3(k.jobs), dim3(THREADS), 0, stream, a, k.tiles, k.blocks);
-    return hipGetLastError();
+    constexpr int VEC = 2;
+    const bool vec = a.D % VEC == 0 && aligned(a.x, a.x_st, sizeof(XT), VEC) && aligned(a.g, a.g_st, sizeof(GT), VEC) &&
+                     aligned(a.o, a.o_st, sizeof(XT), VEC) && aligned(a.s0, 0, 4, VEC) &&
+                     aligned(a.final_state, 0, 4, VEC) && aligned(a.cache, 0, 4, VEC);
+    return vec ? run_scan<XT, GT, VEC, 16>(a, stream) : run_scan<XT, GT, 1, 16>(a, stream);
   });
 }
 
@@ -562,19 +613,12 @@ hipError_t launch_scan_backward(const ScanArgs &a, int xt, int gt, hipStream_t s
   return by_types(xt, gt, [&](auto x, auto g) {
     using XT = decltype(x);
     using GT = decltype(g);
-    const bool vec = a.D % 4 == 0 && aligned(a.x, a.x_st, sizeof(XT)) && aligned(a.g, a.g_st, sizeof(GT)) &&
-                     aligned(a.dout, a.do_st, sizeof(XT)) && aligned(a.dx, a.dx_st, a.dx_f32 ? 4 : sizeof(XT)) &&
-                     aligned(a.dg, a.dg_st, a.dg_f32 ? 4 : sizeof(GT)) && aligned(a.s0, 0, 4) &&
-                     aligned(a.dfinal, 0, 4) && aligned(a.ds0, 0, 4);
-    const bool empties = a.N > 0 && a.ds0;
-    const Grid k = vec ? grid_of<4>(a, empties) : grid_of<1>(a, empties);
-    if (k.jobs == 0) return hipSuccess;
-    if (hipError_t e = fill_words(a, k, stream)) return e;
-    auto *kernel =
-        vec ? (a.complement ? gdp_scan_backward_kernel<XT, GT, 4, true> : gdp_scan_backward_kernel<XT, GT, 4, false>)
-            : (a.complement ? gdp_scan_backward_kernel<XT, GT, 1, true> : gdp_scan_backward_kernel<XT, GT, 1, false>);
-    hipLaunchKernelGGL(kernel, dim3(k.jobs), dim3(THREADS), 0, stream, a, k.tiles, k.blocks);
-    return hipGetLastError();
+    constexpr int VEC = 2;
+    const bool vec = a.D % VEC == 0 && aligned(a.x, a.x_st, sizeof(XT), VEC) && aligned(a.g, a.g_st, sizeof(GT), VEC) &&
+                     aligned(a.dout, a.do_st, sizeof(XT), VEC) && aligned(a.dx, a.dx_st, a.dx_f32 ? 4 : sizeof(XT), VEC) &&
+                     aligned(a.dg, a.dg_st, a.dg_f32 ? 4 : sizeof(GT), VEC) && aligned(a.s0, 0, 4, VEC) &&
+                     aligned(a.dfinal, 0, 4, VEC) && aligned(a.ds0, 0, 4, VEC);
+    return vec ? run_backward<XT, GT, VEC>(a, stream) : run_backward<XT, GT, 1>(a, stream);
   });
 }
 
