@@ -374,21 +374,41 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs 
 
   // the states before the wave's rows: the forward maps of the waves, composed
   float d[R][VEC], m[COMPL ? R : 1][VEC], h[VEC] = {}, sum[VEC] = {};
+  auto restart = [&](int r) {  // a sequence's first row
+    if (a.s0) {
+      const Pack<float, VEC> s0 = load_pack<float, VEC>(a.s0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch);
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) h[c] = s0.v[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) h[c] = 0.f;
+    }
+  };
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    float s0[VEC] = {};
-    if ((starts >> r & 1) && a.s0) {
-      const Pack<float, VEC> p = load_pack<float, VEC>(a.s0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch);
-#pragma unroll
-      for (int c = 0; c < VEC; ++c) s0[c] = p.v[c];
-    }
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
-      const float g = (float)graw[r].v[c], x = (float)xraw[r].v[c];
+      const float g = (float)graw[r].v[c];
       d[r][c] = decay(g);
       if (COMPL) m[r][c] = one_minus_decay(g, d[r][c]);
       sum[c] += g;
-      h[c] = fmaf(d[r][c], starts >> r & 1 ? s0[c] : h[c], COMPL ? m[r][c] * x : x);
+    }
+  }
+  auto advance = [&](int r) {
+#pragma unroll
+    for (int c = 0; c < VEC; ++c) {
+      const float x = (float)xraw[r].v[c];
+      h[c] = fmaf(d[r][c], h[c], COMPL ? m[r][c] * x : x);
+    }
+  };
+  if (starts == 0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) advance(r);
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (starts >> r & 1) restart(r);
+      advance(r);
     }
   }
 #pragma unroll
@@ -411,23 +431,19 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs 
   float p[R][VEC];
 #pragma unroll
   for (int c = 0; c < VEC; ++c) h[c] = sh.A[w][lane * VEC + c];
+  auto weigh = [&](int r) {
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (starts >> r & 1) {
-      if (a.s0) {
-        const Pack<float, VEC> s0 = load_pack<float, VEC>(a.s0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch);
+    for (int c = 0; c < VEC; ++c) p[r][c] = d[r][c] * (COMPL ? h[c] - (float)xraw[r].v[c] : h[c]);
+    advance(r);
+  };
+  if (starts == 0) {
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) h[c] = s0.v[c];
-      } else {
+    for (int r = 0; r < R; ++r) weigh(r);
+  } else {
 #pragma unroll
-        for (int c = 0; c < VEC; ++c) h[c] = 0.f;
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < VEC; ++c) {
-      const float x = (float)xraw[r].v[c];
-      p[r][c] = d[r][c] * (COMPL ? h[c] - x : h[c]);
-      h[c] = fmaf(d[r][c], h[c], COMPL ? m[r][c] * x : x);
+    for (int r = 0; r < R; ++r) {
+      if (starts >> r & 1) restart(r);
+      weigh(r);
     }
   }
   float e[VEC] = {};
@@ -441,11 +457,19 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs 
       for (int c = 0; c < VEC; ++c) e[c] = 0.f;
     }
   };
-#pragma unroll
-  for (int r = R - 1; r >= 0; --r) {
-    if (ends >> r & 1) last_row(r, e);
+  auto retreat = [&](int r) {
 #pragma unroll
     for (int c = 0; c < VEC; ++c) e[c] = d[r][c] * ((float)draw[r].v[c] + e[c]);
+  };
+  if (ends == 0) {
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) retreat(r);
+  } else {
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {
+      if (ends >> r & 1) last_row(r, e);
+      retreat(r);
+    }
   }
   __syncthreads();
 #pragma unroll
@@ -490,27 +514,55 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs 
 
 #pragma unroll
   for (int c = 0; c < VEC; ++c) e[c] = sh.A[w][lane * VEC + c];
-#pragma unroll
-  for (int r = R - 1; r >= 0; --r) {
-    const int64_t t = t0 + r;
-    const bool covered = t >= c0 && t < cN;
-    if (ends >> r & 1) last_row(r, e);
-    float dx[VEC], dg[VEC];
+  float dx[VEC], dg[VEC];
+  auto gradients = [&](int r) {
 #pragma unroll
     for (int c = 0; c < VEC; ++c) {
       e[c] += (float)draw[r].v[c];
-      dx[c] = covered ? (COMPL ? m[r][c] * e[c] : e[c]) : 0.f;
-      dg[c] = covered ? e[c] * p[r][c] : 0.f;
+      dx[c] = COMPL ? m[r][c] * e[c] : e[c];
+      dg[c] = e[c] * p[r][c];
       e[c] *= d[r][c];
     }
-    if (mine && t < a.T) {
-      if (a.dx_f32) store_pack<float, VEC>((float *)a.dx + t * a.dx_st, ch, dx);
-      else store_pack<XT, VEC>((XT *)a.dx + t * a.dx_st, ch, dx);
-      if (a.dg_f32) store_pack<float, VEC>((float *)a.dg + t * a.dg_st, ch, dg);
-      else store_pack<GT, VEC>((GT *)a.dg + t * a.dg_st, ch, dg);
+  };
+  // the rows' gradients, stored as float32 or as the inputs' types
+  auto rows = [&](auto dx_type, auto dg_type) {
+    using DX = decltype(dx_type);
+    using DG = decltype(dg_type);
+    DX *dx_row = (DX *)a.dx + (t0 + R - 1) * a.dx_st;
+    DG *dg_row = (DG *)a.dg + (t0 + R - 1) * a.dg_st;
+    if ((starts | ends) == 0 && t0 >= c0 && t0 + R <= cN) {
+#pragma unroll
+      for (int r = R - 1; r >= 0; --r, dx_row -= a.dx_st, dg_row -= a.dg_st) {
+        gradients(r);
+        if (mine) {
+          store_pack<DX, VEC>(dx_row, ch, dx);
+          store_pack<DG, VEC>(dg_row, ch, dg);
+        }
+      }
+      return;
     }
-    if ((starts >> r & 1) && a.ds0 && mine)
-      store_pack<float, VEC>(a.ds0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch, e);
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r, dx_row -= a.dx_st, dg_row -= a.dg_st) {
+      if (ends >> r & 1) last_row(r, e);
+      gradients(r);
+      if (t0 + r < c0 || t0 + r >= cN) {
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) dx[c] = dg[c] = 0.f;
+      }
+      if (mine && t0 + r < a.T) {
+        store_pack<DX, VEC>(dx_row, ch, dx);
+        store_pack<DG, VEC>(dg_row, ch, dg);
+      }
+      if ((starts >> r & 1) && a.ds0 && mine)
+        store_pack<float, VEC>(a.ds0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch, e);
+    }
+  };
+  if (a.dx_f32) {
+    if (a.dg_f32) rows(0.f, 0.f);
+    else rows(0.f, (GT)0);
+  } else {
+    if (a.dg_f32) rows((XT)0, 0.f);
+    else rows((XT)0, (GT)0);
   }
 }
 
