@@ -42,7 +42,7 @@ namespace gdp {
 namespace {
 
 constexpr int WAVES = 8, THREADS = 64 * WAVES;
-constexpr int WINDOW = 16;  // tiles before this one that a lane looks at
+constexpr int WINDOW = 8;  // tiles before this one that a lane looks at
 constexpr uint64_t NOT_WRITTEN = ~0ull;
 
 template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Pack { T v[VEC]; };
