@@ -312,31 +312,38 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_norm_backwar
   }
 }
 
-// dw and db from the partial rows of a group (row r: r * stride + blockIdx.y), 64
-// channels per workgroup, the rows dealt over 16 waves.
+// dw (blockIdx.z = 0) and db from the partial rows of a group (row r: r * stride +
+// blockIdx.y): 16 channels per workgroup, the rows dealt over 64 lane groups, eight
+// loads ahead.  A fixed order: the result does not depend on timing.  With 64
+// channels and 16 lane groups per workgroup the sums of 1024 rows of 128 channels
+// took 23 us, waiting for 64 loads one after another.
 __global__ void __launch_bounds__(1024) gdp_norm_weight_kernel(NormArgs a, int rows, int stride) {
-  __shared__ float red[2][16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int v = (int)blockIdx.x * 64 + lane;
-  float s[2] = {0.f, 0.f};
+  __shared__ float red[64][17];
+  const int c = threadIdx.x & 15, part = threadIdx.x >> 4;
+  const int v = (int)blockIdx.x * 16 + c;
+  float *out = blockIdx.z == 0 ? a.dw : a.db;
+  if (!out) return;
+  float s = 0.f;
   if (v < a.V) {
-#pragma unroll 8
-    for (int r = wave; r < rows; r += 16) {
-      const float *row = a.ws + ((int64_t)r * stride + blockIdx.y) * 2 * a.V + v;
-      if (a.dw) s[0] += row[0];
-      if (a.db) s[1] += row[a.V];
-    }
-  }
-  red[0][wave][lane] = s[0];
-  red[1][wave][lane] = s[1];
-  __syncthreads();
-  if (wave < 2 && v < a.V) {
-    float *out = wave == 0 ? a.dw : a.db;
-    float sum = 0.f;
+    const float *p = a.ws + ((int64_t)blockIdx.y * 2 + blockIdx.z) * a.V + v;
+    const int64_t step = (int64_t)stride * 2 * a.V;
+    int r = part;
+    for (; r + 64 * 7 < rows; r += 64 * 8) {
+      float x[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum += red[wave][i][lane];
-    if (out) out[(int64_t)blockIdx.y * a.V + v] = sum;
+      for (int i = 0; i < 8; ++i) x[i] = p[(r + 64 * i) * step];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += x[i];
+    }
+    for (; r < rows; r += 64) s += p[r * step];
   }
+  red[part][c] = s;
+  __syncthreads();
+  for (int n = 32; n > 0; n >>= 1) {
+    if (part < n) red[part][c] += red[part + n][c];
+    __syncthreads();
+  }
+  if (part == 0 && v < a.V) out[(int64_t)blockIdx.y * a.V + v] = red[0][c];
 }
 
 // How the groups are laid over lanes.  E pieces of VEC channels per lane: one while
@@ -459,7 +466,7 @@ hipError_t launch_norm_backward(const NormArgs &a, int xt, hipStream_t stream) {
     if (!a.dw && !a.db) return hipSuccess;
     const bool shared = a.w_sh == 0, fold = shared && p.lpg <= 64 && p.teams > 1;
     const int64_t rows = fold ? blocks : blocks * p.teams;
-    const dim3 grid((unsigned)((a.V + 63) / 64), shared ? 1u : (unsigned)a.G);
+    const dim3 grid((unsigned)((a.V + 15) / 16), shared ? 1u : (unsigned)a.G, 2);
     hipLaunchKernelGGL(gdp_norm_weight_kernel, grid, dim3(1024), 0, stream, a, (int)(shared ? rows : rows / a.G),
                        shared ? 1 : a.G);
     return hipGetLastError();
