@@ -33,6 +33,7 @@ struct ScanArgs {
   void *dg; int64_t dg_st; int dg_f32;  // [T, D] float32 or g's type
   float *ds0;                           // [N, D] or null
   void *ws;                             // scan_state_bytes(T, D)
+  int streamed;                         // set by the launch: the rows' loads bypass the caches
 };
 size_t scan_state_bytes(int64_t T, int64_t D);
 // whether the launch grids of these sizes fit

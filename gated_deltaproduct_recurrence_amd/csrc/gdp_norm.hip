@@ -69,8 +69,6 @@ template <int WIDE> struct Team {
   }
 };
 
-template <typename T, int N> struct alignas(sizeof(T) * N) Pack { T v[N]; };
-
 // s = sigmoid(v): the hardware's exponential and reciprocal, each good to one step
 __device__ __forceinline__ float sigmoid(float v) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -LOG2E_L));
@@ -79,17 +77,17 @@ __device__ __forceinline__ float sigmoid(float v) {
 // E pieces of one (token, group)
 template <typename T, int VEC, int E> struct Values {
   Pack<T, VEC> p[E];
-  __device__ __forceinline__ void load(const T *row, int lane, int lpg, int V) {
+  template <bool STREAMED> __device__ __forceinline__ void load(const T *row, int lane, int lpg, int V) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int v = (e * lpg + lane) * VEC;
-      if (v < V) p[e] = *(const Pack<T, VEC> *)(row + v);
-      else p[e] = {};
+      p[e] = {};
+      if (v < V) p[e] = STREAMED ? load_streamed<T, VEC>(row + v) : *(const Pack<T, VEC> *)(row + v);
     }
   }
 };
 
-template <typename T, int VEC, int E>
+template <bool STREAMED, typename T, int VEC, int E>
 __device__ __forceinline__ void store_values(T *row, const float (&y)[E][VEC], int lane, int lpg, int V) {
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -97,7 +95,10 @@ __device__ __forceinline__ void store_values(T *row, const float (&y)[E][VEC], i
     Pack<T, VEC> s;
 #pragma unroll
     for (int c = 0; c < VEC; ++c) s.v[c] = (T)y[e][c];
-    if (v < V) *(Pack<T, VEC> *)(row + v) = s;
+    if (v < V) {
+      if (STREAMED) store_streamed<T, VEC>(row + v, s);
+      else *(Pack<T, VEC> *)(row + v) = s;
+    }
   }
 }
 
@@ -159,7 +160,7 @@ __device__ __forceinline__ Place place_of(const NormArgs &a, int teams, int team
   return p;
 }
 
-template <typename T, int VEC, int E, int WIDE>
+template <typename T, int VEC, int E, int WIDE, bool STREAMED>
 __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_norm_kernel(NormArgs a, int lpg) {
   __shared__ float slots[WIDE ? 2 : 1][16];
   const int tid = threadIdx.x;
@@ -174,8 +175,8 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_norm_kernel(
   Values<T, VEC, E> xv{}, zv{}, xn{}, zn{};
   auto fetch = [&](int64_t t) {
     if (t < a.T) {
-      xn.load(x + t * a.x_st, team.lane, lpg, a.V);
-      if (a.z) zn.load(z + t * a.z_st, team.lane, lpg, a.V);
+      xn.template load<STREAMED>(x + t * a.x_st, team.lane, lpg, a.V);
+      if (a.z) zn.template load<STREAMED>(z + t * a.z_st, team.lane, lpg, a.V);
     }
   };
   int64_t t = at.t;
@@ -207,14 +208,14 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_norm_kernel(
           n[e][c] = a.act == GDP_ACT_SILU ? n[e][c] * s : s;
         }
     }
-    if (t < a.T) store_values<T, VEC, E>(y + t * a.y_st, n, team.lane, lpg, a.V);
+    if (t < a.T) store_values<STREAMED, T, VEC, E>(y + t * a.y_st, n, team.lane, lpg, a.V);
   }
 }
 
 // The gradients; partial sums of dw and db to the workspace: one row [2][V] per
 // workgroup when the groups share their weights (the teams' sums added in LDS),
 // else one per team.
-template <typename T, int VEC, int E, int WIDE>
+template <typename T, int VEC, int E, int WIDE, bool STREAMED>
 __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_norm_backward_kernel(NormArgs a, int lpg) {
   __shared__ float slots[WIDE ? 2 : 1][16];
   __shared__ float part[WIDE ? 1 : 256 * MAX_VALUES];
@@ -231,9 +232,9 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_norm_backwar
   Values<T, VEC, E> xv{}, zv{}, dv{}, xn{}, zn{}, dn_{};
   auto fetch = [&](int64_t t) {
     if (t < a.T) {
-      xn.load(x + t * a.x_st, team.lane, lpg, a.V);
-      dn_.load(dy + t * a.dy_st, team.lane, lpg, a.V);
-      if (a.z) zn.load(z + t * a.z_st, team.lane, lpg, a.V);
+      xn.template load<STREAMED>(x + t * a.x_st, team.lane, lpg, a.V);
+      dn_.template load<STREAMED>(dy + t * a.dy_st, team.lane, lpg, a.V);
+      if (a.z) zn.template load<STREAMED>(z + t * a.z_st, team.lane, lpg, a.V);
     }
   };
   int64_t t = at.t;
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_norm_backwar
     s1 = a.center ? team.sum(s1) * inv_v : 0.f;
     s2 = team.sum(s2) * inv_v;
     if (t < a.T) {
-      if (a.z) store_values<T, VEC, E>(dz + t * a.dz_st, g, team.lane, lpg, a.V);
+      if (a.z) store_values<STREAMED, T, VEC, E>(dz + t * a.dz_st, g, team.lane, lpg, a.V);
 #pragma unroll
       for (int e = 0; e < E; ++e)
 #pragma unroll
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_norm_backwar
           db[e][c] += dn[e][c];
           g[e][c] = (dn[e][c] * w[e][c] - s1 - xhat[e][c] * s2) * rstd;
         }
-      store_values<T, VEC, E>(dx + t * a.dx_st, g, team.lane, lpg, a.V);
+      store_values<STREAMED, T, VEC, E>(dx + t * a.dx_st, g, team.lane, lpg, a.V);
     }
   }
   if (!a.dw && !a.db) return;
@@ -376,7 +377,7 @@ int64_t grid_of(const Plan &p, int64_t T, int G, int64_t per_team, int64_t most)
   }
   return (n + unit - 1) / unit * unit;
 }
-constexpr int64_t FORWARD_GRID = 2048, BACKWARD_GRID = 1024;
+constexpr int64_t FORWARD_GRID = 1024, BACKWARD_GRID = 768;
 
 template <typename F> hipError_t by_type(int xt, F f) {
   if (xt == EL_F32) return f((float)0);
@@ -438,12 +439,16 @@ hipError_t launch_norm(const NormArgs &a, int xt, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
   return by_type(xt, [&](auto x) {
     using T = decltype(x);
+    const bool streamed = a.T * a.G * a.V * (int64_t)sizeof(T) * (a.z ? 3 : 2) > STREAM_BYTES;
     const Plan p = plan_of(a.V, vec_of(a, sizeof(T), false));
     const int64_t blocks = grid_of(p, a.T, a.G, 1, FORWARD_GRID);
     return by_plan<T>(p, [&](auto s) {
       using S = decltype(s);
-      hipLaunchKernelGGL((gdp_norm_kernel<T, S::vec, S::pieces, S::wide>), dim3((unsigned)blocks), dim3(p.threads), 0,
-                         stream, a, p.lpg);
+      auto *kernel = gdp_norm_kernel<T, S::vec, S::pieces, S::wide, false>;
+      // only whole 16-byte pieces: the narrower forms are bound elsewhere
+      if constexpr (S::vec * sizeof(T) == 16)
+        if (streamed) kernel = gdp_norm_kernel<T, S::vec, S::pieces, S::wide, true>;
+      hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(p.threads), 0, stream, a, p.lpg);
       return hipGetLastError();
     });
   });
@@ -452,13 +457,16 @@ hipError_t launch_norm(const NormArgs &a, int xt, hipStream_t stream) {
 hipError_t launch_norm_backward(const NormArgs &a, int xt, hipStream_t stream) {
   return by_type(xt, [&](auto x) {
     using T = decltype(x);
+    const bool streamed = a.T * a.G * a.V * (int64_t)sizeof(T) * (a.z ? 5 : 3) > STREAM_BYTES;
     const Plan p = plan_of(a.V, vec_of(a, sizeof(T), true));
     const int64_t blocks = a.T ? grid_of(p, a.T, a.G, 8, BACKWARD_GRID) : 0;
     if (blocks) {
       const hipError_t e = by_plan<T>(p, [&](auto s) {
         using S = decltype(s);
-        hipLaunchKernelGGL((gdp_norm_backward_kernel<T, S::vec, S::pieces, S::wide>), dim3((unsigned)blocks),
-                           dim3(p.threads), 0, stream, a, p.lpg);
+        auto *kernel = gdp_norm_backward_kernel<T, S::vec, S::pieces, S::wide, false>;
+        if constexpr (S::vec * sizeof(T) == 16)
+          if (streamed) kernel = gdp_norm_backward_kernel<T, S::vec, S::pieces, S::wide, true>;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(p.threads), 0, stream, a, p.lpg);
         return hipGetLastError();
       });
       if (e != hipSuccess) return e;

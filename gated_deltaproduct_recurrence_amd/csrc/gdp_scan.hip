@@ -45,8 +45,6 @@ constexpr int WAVES = 8, THREADS = 64 * WAVES;
 constexpr int WINDOW = 8;  // tiles before this one that a lane looks at
 constexpr uint64_t NOT_WRITTEN = ~0ull;
 
-template <typename T, int VEC> struct alignas(sizeof(T) * VEC) Pack { T v[VEC]; };
-
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // channel ch of a row: the row's address is the same for a whole wave (scalar
@@ -69,15 +67,18 @@ template <typename T, int VEC> __device__ __forceinline__ void store_pack(T *row
 
 // R rows from t0 on; rows behind the last one (T > 0) read that row again
 template <int R, typename T, int VEC>
-__device__ __forceinline__ void load_rows(Pack<T, VEC> (&v)[R], const T *base, int64_t stride, int64_t t0, int64_t T_,
-                                          uint32_t ch) {
-  if (t0 + R <= T_) {
-    const T *row = base + t0 * stride;
+__device__ __forceinline__ void load_rows(Pack<T, VEC> (&v)[R], const T *base, int64_t stride, int64_t t0, int64_t rows,
+                                          uint32_t ch, int streamed) {
+  const T *row = base + t0 * stride;
+  if (t0 + R > rows) {
 #pragma unroll
-    for (int r = 0; r < R; ++r, row += stride) v[r] = load_pack<T, VEC>(row, ch);
+    for (int r = 0; r < R; ++r) v[r] = load_pack<T, VEC>(base + (t0 + r < rows ? t0 + r : rows - 1) * stride, ch);
+  } else if (streamed) {
+#pragma unroll
+    for (int r = 0; r < R; ++r, row += stride) v[r] = load_streamed<T, VEC>(at(row, ch));
   } else {
 #pragma unroll
-    for (int r = 0; r < R; ++r) v[r] = load_pack<T, VEC>(base + (t0 + r < T_ ? t0 + r : T_ - 1) * stride, ch);
+    for (int r = 0; r < R; ++r, row += stride) v[r] = load_pack<T, VEC>(row, ch);
   }
 }
 
@@ -225,8 +226,8 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int ti
 
   Pack<GT, VEC> graw[R];
   Pack<XT, VEC> xraw[R];
-  load_rows<R>(graw, (const GT *)a.g, a.g_st, t0, a.T, ch);
-  load_rows<R>(xraw, (const XT *)a.x, a.x_st, t0, a.T, ch);
+  load_rows<R>(graw, (const GT *)a.g, a.g_st, t0, a.T, ch, a.streamed);
+  load_rows<R>(xraw, (const XT *)a.x, a.x_st, t0, a.T, ch, a.streamed);
   const int64_t c0 = bound_at(a.cu, a.cu_is64, 0, a.T), cN = bound_at(a.cu, a.cu_is64, a.N, a.T);
   mark_rows(sh, a, r0, tid);
   const uint32_t starts = marked<R>(sh.start_id, w, lane), ends = marked<R>(sh.end_id, w, lane);
@@ -362,9 +363,9 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs 
 
   Pack<GT, VEC> graw[R];
   Pack<XT, VEC> xraw[R], draw[R];
-  load_rows<R>(graw, (const GT *)a.g, a.g_st, t0, a.T, ch);
-  load_rows<R>(xraw, (const XT *)a.x, a.x_st, t0, a.T, ch);
-  load_rows<R>(draw, (const XT *)a.dout, a.do_st, t0, a.T, ch);
+  load_rows<R>(graw, (const GT *)a.g, a.g_st, t0, a.T, ch, a.streamed);
+  load_rows<R>(xraw, (const XT *)a.x, a.x_st, t0, a.T, ch, a.streamed);
+  load_rows<R>(draw, (const XT *)a.dout, a.do_st, t0, a.T, ch, a.streamed);
   const bool live = tid < S::NCH && first + tid < a.D;  // lane tid < NCH: channel first + tid of the hand-over
   float state = 0.f;
   if (live) state = a.checkpoints[(int64_t)tile * a.D + first + tid];
@@ -619,7 +620,8 @@ hipError_t fill_words(const ScanArgs &a, const Grid &g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <typename XT, typename GT, int VEC, int R> hipError_t run_scan(const ScanArgs &a, hipStream_t stream) {
+template <typename XT, typename GT, int VEC, int R> hipError_t run_scan(ScanArgs a, hipStream_t stream) {
+  a.streamed = a.T * a.D * (int64_t)(2 * sizeof(XT) + sizeof(GT)) > STREAM_BYTES;
   const Grid k = grid_of(a, WAVES * R, 64 * VEC, a.N > 0 && (a.final_state || a.cache));
   if (k.jobs == 0) return hipSuccess;
   if (hipError_t e = fill_words(a, k, stream)) return e;
@@ -628,7 +630,8 @@ template <typename XT, typename GT, int VEC, int R> hipError_t run_scan(const Sc
   return hipGetLastError();
 }
 
-template <typename XT, typename GT, int VEC> hipError_t run_backward(const ScanArgs &a, hipStream_t stream) {
+template <typename XT, typename GT, int VEC> hipError_t run_backward(ScanArgs a, hipStream_t stream) {
+  a.streamed = a.T * a.D * (int64_t)(3 * sizeof(XT) + 2 * sizeof(GT)) > STREAM_BYTES;
   const Grid k = grid_of(a, SCAN_ROWS, 64 * VEC, a.N > 0 && a.ds0);
   if (k.jobs == 0) return hipSuccess;
   if (hipError_t e = fill_words(a, k, stream)) return e;
