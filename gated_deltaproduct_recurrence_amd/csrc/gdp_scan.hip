@@ -42,43 +42,62 @@ namespace gdp {
 namespace {
 
 constexpr int WAVES = 8, THREADS = 64 * WAVES;
-constexpr int WINDOW = 8;  // tiles before this one that a lane looks at
+constexpr int VEC = 2, NCH = 64 * VEC;  // channels per lane and per workgroup
+constexpr int WINDOW = 8;               // tiles before its own that a lane looks at
+constexpr int MOST_TEAMS = THREADS / NCH;  // lanes per channel that can look
 constexpr uint64_t NOT_WRITTEN = ~0ull;
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-// channel ch of a row: the row's address is the same for a whole wave (scalar
-// registers), the lane's part a 32-bit byte offset
+// Channels ch, ch + 1 of a row: the row's address is the same for a whole wave
+// (scalar registers), the lane's part a 32-bit byte offset.  The pair need not be
+// aligned: rows of an odd number of channels, or of a view that starts anywhere,
+// are read and written in pairs all the same, but for the last block of an odd D
+// (`tail`), which goes channel by channel.
+template <typename T> struct __attribute__((packed, aligned(sizeof(T)))) Pair { T v[VEC]; };
 template <typename T> __device__ __forceinline__ T *at(T *row, uint32_t ch) {
   return (T *)((char *)row + (uint32_t)(ch * sizeof(T)));
 }
 template <typename T> __device__ __forceinline__ const T *at(const T *row, uint32_t ch) {
   return (const T *)((const char *)row + (uint32_t)(ch * sizeof(T)));
 }
-template <typename T, int VEC> __device__ __forceinline__ Pack<T, VEC> load_pack(const T *row, uint32_t ch) {
-  return *(const Pack<T, VEC> *)at(row, ch);
+template <typename T> __device__ __forceinline__ Pair<T> load_pair(const T *row, uint32_t ch) {
+  return *(const Pair<T> *)at(row, ch);
 }
-template <typename T, int VEC> __device__ __forceinline__ void store_pack(T *row, uint32_t ch, const float (&x)[VEC]) {
-  Pack<T, VEC> s;
-#pragma unroll
-  for (int c = 0; c < VEC; ++c) s.v[c] = (T)x[c];
-  *(Pack<T, VEC> *)at(row, ch) = s;
+template <typename T> __device__ __forceinline__ Pair<T> load_streamed(const T *row, uint32_t ch) {
+  typedef T vec __attribute__((ext_vector_type(VEC), aligned(sizeof(T))));
+  const vec v = __builtin_nontemporal_load((const vec *)at(row, ch));
+  return Pair<T>{{v.x, v.y}};
+}
+template <typename T> __device__ __forceinline__ void store_pair(T *row, uint32_t ch, const float (&x)[VEC]) {
+  *(Pair<T> *)at(row, ch) = Pair<T>{{(T)x[0], (T)x[1]}};
+}
+struct Tail { bool on; uint32_t last; };  // last: the tensor's last channel
+template <typename T> __device__ __forceinline__ Pair<T> load_pair(const T *row, uint32_t ch, Tail tail) {
+  if (!tail.on) return load_pair(row, ch);
+  return Pair<T>{{*at(row, ch), *at(row, ch < tail.last ? ch + 1 : ch)}};
+}
+template <typename T>
+__device__ __forceinline__ void store_pair(T *row, uint32_t ch, const float (&x)[VEC], Tail tail) {
+  if (!tail.on) return store_pair(row, ch, x);
+  *at(row, ch) = (T)x[0];
+  if (ch < tail.last) *at(row, ch + 1) = (T)x[1];
 }
 
-// R rows from t0 on; rows behind the last one (T > 0) read that row again
-template <int R, typename T, int VEC>
-__device__ __forceinline__ void load_rows(Pack<T, VEC> (&v)[R], const T *base, int64_t stride, int64_t t0, int64_t rows,
-                                          uint32_t ch, int streamed) {
+// R rows from t0 on; rows behind the last one read that row again
+template <int R, typename T>
+__device__ __forceinline__ void load_rows(Pair<T> (&v)[R], const T *base, int64_t stride, int64_t t0, int64_t rows,
+                                          uint32_t ch, Tail tail, int streamed) {
   const T *row = base + t0 * stride;
-  if (t0 + R > rows) {
+  if (t0 + R > rows || tail.on) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) v[r] = load_pack<T, VEC>(base + (t0 + r < rows ? t0 + r : rows - 1) * stride, ch);
+    for (int r = 0; r < R; ++r) v[r] = load_pair(base + (t0 + r < rows ? t0 + r : rows - 1) * stride, ch, tail);
   } else if (streamed) {
 #pragma unroll
-    for (int r = 0; r < R; ++r, row += stride) v[r] = load_streamed<T, VEC>(at(row, ch));
+    for (int r = 0; r < R; ++r, row += stride) v[r] = load_streamed(row, ch);
   } else {
 #pragma unroll
-    for (int r = 0; r < R; ++r, row += stride) v[r] = load_pack<T, VEC>(row, ch);
+    for (int r = 0; r < R; ++r, row += stride) v[r] = load_pair(row, ch);
   }
 }
 
@@ -90,9 +109,11 @@ __device__ __forceinline__ uint64_t make_word(float A, float B) {
   return ((uint64_t)a << 32) | __float_as_uint(B);
 }
 
-template <int VEC, int R> struct Shared {
-  static constexpr int NCH = 64 * VEC, ROWS = WAVES * R;
+template <int R> struct Shared {
+  static constexpr int ROWS = WAVES * R;
   float A[WAVES][NCH], B[WAVES][NCH];
+  float found[MOST_TEAMS][NCH];   // a team's state for the one before it ...
+  int there[MOST_TEAMS][VEC];     // ... and whether it is there, of each half of the channels
   int start_id[ROWS], end_id[ROWS];  // sequence that starts / ends at a row of the tile, or -1
   int ticket;
 };
@@ -133,34 +154,51 @@ template <int R> __device__ __forceinline__ uint32_t marked(const int *ids, int 
 }
 
 // The state entering this tile, of one channel, from the words of the `count` tiles
-// before it: `word` is the nearest one's, the others lie `step` words apart.
-__device__ __forceinline__ float entering(const uint64_t *word, int64_t step, int count, bool live) {
+// before it: `word` is the nearest one's, the others lie `step` words apart.  Team
+// `team` of TEAMS looks at the words team * WINDOW and on; a team that finds all of
+// its words but none with A = 0 goes on from the state that the next team found.
+// Only team 0's value is used; the others stop when it has one.
+template <int TEAMS, typename S>
+__device__ __forceinline__ float entering(S &sh, const uint64_t *word, int64_t step, int64_t count, bool live, int team,
+                                          int c) {
+  const int half = c >> 6;
+  if (TEAMS > 1) {
+    count -= team * WINDOW;
+    word += team * WINDOW * step;
+  }
   uint64_t v[WINDOW];
   auto read = [&](const uint64_t *w, int i) {  // tiles before the first count as a state of 0
     return live && i < count ? __hip_atomic_load(w + i * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
   };
   auto first_part = [](uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); };
-  // the nearest word with A = 0 among the first n, if all words before it are there
-  auto resolved = [&](int n) {
-    bool open = true, found = false;
+  auto signal = [&](int t) { return __hip_atomic_load(&sh.there[t][half], __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP); };
+  bool found, open;  // a word with A = 0 and all before it are there; all are there, none has A = 0
+  auto look = [&](int n) {
+    open = true;
+    found = false;
 #pragma unroll
-    for (int i = 0; i < WINDOW; ++i) {
-      if (i >= n) break;
+    for (int i = 0; i < n; ++i) {
       const bool there = v[i] != NOT_WRITTEN;
       found = found || (open && there && first_part(v[i]) == 0.f);
       open = open && there && !found;
     }
-    return found;
   };
-  constexpr int NEAR = WINDOW / 2;
+  // a single team looks at the nearer half first: mostly it is enough, and the words are
+  // a good part of what is read
+  constexpr int NEAR = TEAMS > 1 ? WINDOW : WINDOW / 2;
 #pragma unroll
-  for (int i = 0; i < NEAR; ++i) v[i] = read(word, i);
-#pragma unroll
-  for (int i = NEAR; i < WINDOW; ++i) v[i] = NOT_WRITTEN;
-  if (!__all(resolved(NEAR))) {
+  for (int i = 0; i < WINDOW; ++i) v[i] = i < NEAR ? read(word, i) : NOT_WRITTEN;
+  float h = 0.f;
+  look(NEAR);
+  if (!__all(found)) {
 #pragma unroll
     for (int i = NEAR; i < WINDOW; ++i) v[i] = read(word, i);
-    while (!__all(resolved(WINDOW))) {
+    for (;;) {
+      look(WINDOW);
+      const bool beyond = TEAMS > 1 && team + 1 < TEAMS && !__all(found) && signal(team + 1);
+      if (beyond) h = sh.found[team + 1][c];
+      if (__all(found || (open && beyond))) break;
+      if (TEAMS > 1 && team > 0 && signal(0)) return 0.f;
       __builtin_amdgcn_s_sleep(1);
       asm volatile("" : "+v"(word));  // or every word's address is kept in registers over the loop
 #pragma unroll
@@ -168,17 +206,60 @@ __device__ __forceinline__ float entering(const uint64_t *word, int64_t step, in
         if (i == WINDOW - 1 || v[i] == NOT_WRITTEN) v[i] = read(word, i);
     }
   }
-  float h = 0.f;
 #pragma unroll
   for (int i = WINDOW - 1; i >= 0; --i)
     if (v[i] != NOT_WRITTEN) h = apply(first_part(v[i]), h, __uint_as_float((uint32_t)v[i]));
+  if (TEAMS > 1) {
+    sh.found[team][c] = h;
+    __hip_atomic_store(&sh.there[team][half], 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
+  }
   return h;
+}
+
+// The waves' maps in sh.A, sh.B: composes the tile's, publishes it, and leaves in
+// sh.A the state entering each wave's rows (of the channels first + 0 .. NCH - 1).
+// REVERSE: from the last tile and wave to the first.
+template <int TEAMS, bool REVERSE, typename S>
+__device__ __forceinline__ void hand_over(S &sh, const ScanArgs &a, int tile, int tiles, bool needs, int first, int tid) {
+  const int c = tid % NCH, team = tid / NCH, step = REVERSE ? 1 : -1;  // to the tile before, in this direction
+  const int before = REVERSE ? tiles - 1 - tile : tile;
+  const bool live = first + c < a.D, publish = live && team == 0 && before + 1 < tiles;
+  uint64_t *words = at((uint64_t *)((char *)a.ws + 256) + (int64_t)tile * a.D, first + c);
+  float A = 1.f, B = 0.f, carry = 0.f;
+  if (team < (needs ? TEAMS : 1) && tiles > 1) {
+    if (team == 0) {
+#pragma unroll
+      for (int v = 0; v < WAVES; ++v) {
+        const int w = REVERSE ? WAVES - 1 - v : v;
+        B = apply(sh.A[w][c], B, sh.B[w][c]);
+        A *= sh.A[w][c];
+      }
+      if (!needs) A = 0.f;
+    }
+    if (publish) __hip_atomic_store(words, make_word(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (needs) {
+      carry = entering<TEAMS>(sh, words + step * a.D, step * a.D, before, live, team, c);
+      if (publish && A != 0.f)
+        __hip_atomic_store(words, make_word(0.f, fmaf(A, carry, B)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  if (team == 0) {
+    float h = carry;
+#pragma unroll
+    for (int v = 0; v < WAVES; ++v) {
+      const int w = REVERSE ? WAVES - 1 - v : v;
+      const float next = apply(sh.A[w][c], h, sh.B[w][c]);
+      sh.A[w][c] = h;
+      h = next;
+    }
+  }
 }
 
 // The workgroup's job: its ticket (the counter starts at -1), or the block's own
 // index when nothing is handed on.  Clears the row marks.
 template <typename S> __device__ __forceinline__ int take_ticket(S &sh, const ScanArgs &a, bool hand_on, int tid) {
   if (tid < S::ROWS) sh.start_id[tid] = sh.end_id[tid] = -1;
+  if (tid < MOST_TEAMS * VEC) sh.there[tid / VEC][tid % VEC] = 0;
   if (!hand_on) {
     __syncthreads();
     return (int)blockIdx.x;
@@ -206,9 +287,9 @@ __device__ __forceinline__ void empty_sequences(const ScanArgs &a, int64_t job, 
   }
 }
 
-template <typename XT, typename GT, int VEC, int R, bool COMPL>
+template <typename XT, typename GT, int R, bool COMPL, int TEAMS>
 __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int tiles, int blocks) {
-  using S = Shared<VEC, R>;
+  using S = Shared<R>;
   __shared__ S sh;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool hand_on = tiles > 1;
@@ -218,16 +299,17 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int ti
     empty_sequences(a, ticket - tiles * blocks, a.s0, a.final_state, tid);
     return;
   }
-  const int first = (ticket % blocks) * S::NCH;  // the block's first channel
+  const int first = (ticket % blocks) * NCH;  // the block's first channel
   const int64_t r0 = (int64_t)tile * S::ROWS;
   const bool mine = first + lane * VEC < a.D;
   const uint32_t ch = mine ? first + lane * VEC : 0;
+  const Tail tail{first + NCH > a.D && (a.D & 1), (uint32_t)a.D - 1};
   const int64_t t0 = r0 + w * R;
 
-  Pack<GT, VEC> graw[R];
-  Pack<XT, VEC> xraw[R];
-  load_rows<R>(graw, (const GT *)a.g, a.g_st, t0, a.T, ch, a.streamed);
-  load_rows<R>(xraw, (const XT *)a.x, a.x_st, t0, a.T, ch, a.streamed);
+  Pair<GT> graw[R];
+  Pair<XT> xraw[R];
+  load_rows<R>(graw, (const GT *)a.g, a.g_st, t0, a.T, ch, tail, a.streamed);
+  load_rows<R>(xraw, (const XT *)a.x, a.x_st, t0, a.T, ch, tail, a.streamed);
   const int64_t c0 = bound_at(a.cu, a.cu_is64, 0, a.T), cN = bound_at(a.cu, a.cu_is64, a.N, a.T);
   mark_rows(sh, a, r0, tid);
   const uint32_t starts = marked<R>(sh.start_id, w, lane), ends = marked<R>(sh.end_id, w, lane);
@@ -235,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int ti
   float d[R][VEC], u[COMPL ? R : 1][VEC], sum[VEC] = {}, h[VEC] = {};
   auto restart = [&](int r) {  // a sequence's first row
     if (a.s0) {
-      const Pack<float, VEC> s0 = load_pack<float, VEC>(a.s0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch);
+      const Pair<float> s0 = load_pair(a.s0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch, tail);
 #pragma unroll
       for (int c = 0; c < VEC; ++c) h[c] = s0.v[c];
     } else {
@@ -274,50 +356,24 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int ti
   }
   __syncthreads();
 
-  if (tid < S::NCH) {  // lane tid: channel first + tid
-    const bool live = first + tid < a.D, covered = r0 >= c0 && r0 < cN;
-    float carry = 0.f;
-    if (hand_on) {
-      const bool needs = tile > 0 && sh.start_id[0] < 0 && covered;
-      float A = 1.f, B = 0.f;
-#pragma unroll
-      for (int v = 0; v < WAVES; ++v) {
-        B = apply(sh.A[v][tid], B, sh.B[v][tid]);
-        A *= sh.A[v][tid];
-      }
-      if (!needs) A = 0.f;
-      uint64_t *words = (uint64_t *)((char *)a.ws + 256);
-      const uint32_t col = first + tid;
-      const bool publish = live && tile + 1 < tiles;
-      if (publish)
-        __hip_atomic_store(at(words + (int64_t)tile * a.D, col), make_word(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (needs) {
-        carry = entering(at(words + (int64_t)(tile - 1) * a.D, col), -a.D, tile, live);
-        if (publish && A != 0.f)
-          __hip_atomic_store(at(words + (int64_t)tile * a.D, col), make_word(0.f, fmaf(A, carry, B)), __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < WAVES; ++v) {  // the state entering each wave's rows, in place of its A
-      if (a.checkpoints && v * R % SCAN_ROWS == 0 && live && r0 + v * R >= c0 && r0 + v * R < cN)
-        a.checkpoints[(r0 + v * R) / SCAN_ROWS * a.D + first + tid] = carry;
-      const float next = apply(sh.A[v][tid], carry, sh.B[v][tid]);
-      sh.A[v][tid] = carry;
-      carry = next;
-    }
-  }
+  hand_over<TEAMS, false>(sh, a, tile, tiles, tile > 0 && sh.start_id[0] < 0 && r0 >= c0 && r0 < cN, first, tid);
   __syncthreads();
 
+  if (a.checkpoints && tid < NCH && first + tid < a.D) {
+#pragma unroll
+    for (int v = 0; v < WAVES; v += SCAN_ROWS / R)
+      if (r0 + v * R >= c0 && r0 + v * R < cN)
+        a.checkpoints[(r0 + v * R) / SCAN_ROWS * a.D + first + tid] = sh.A[v][tid];
+  }
   if (!a.o) return;  // states only
 #pragma unroll
   for (int c = 0; c < VEC; ++c) h[c] = sh.A[w][lane * VEC + c];
   XT *out = (XT *)a.o + t0 * a.o_st;
-  if ((starts | ends) == 0 && t0 >= c0 && t0 + R <= cN) {
+  if ((starts | ends) == 0 && t0 >= c0 && t0 + R <= cN && !tail.on) {
 #pragma unroll
     for (int r = 0; r < R; ++r, out += a.o_st) {
       advance(r);
-      if (mine) store_pack<XT, VEC>(out, ch, h);
+      if (mine) store_pair(out, ch, h);
     }
     return;
   }
@@ -325,13 +381,13 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int ti
   for (int r = 0; r < R; ++r, out += a.o_st) {
     if (starts >> r & 1) restart(r);
     advance(r);
-    if (mine && t0 + r >= c0 && t0 + r < cN) store_pack<XT, VEC>(out, ch, h);
+    if (mine && t0 + r >= c0 && t0 + r < cN) store_pair(out, ch, h, tail);
     if (ends >> r & 1) {
       const int64_t i = uniform(sh.end_id[w * R + r]);
-      if (a.final_state && mine) store_pack<float, VEC>(a.final_state + i * a.D, ch, h);
+      if (a.final_state && mine) store_pair(a.final_state + i * a.D, ch, h, tail);
       if (a.cache) {
         const int64_t slot = index_at(a.slots, a.slots_is64, i);
-        if (slot >= 0 && slot < a.num_slots && mine) store_pack<float, VEC>(a.cache + slot * a.D, ch, h);
+        if (slot >= 0 && slot < a.num_slots && mine) store_pair(a.cache + slot * a.D, ch, h, tail);
       }
     }
   }
@@ -342,10 +398,10 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int ti
 // behind, cut at the sequences' last rows (where d_final_state enters), and is
 // handed on between tiles the same way.  The states are formed again from the
 // checkpoint at the tile's first row.
-template <typename XT, typename GT, int VEC, bool COMPL>
+template <typename XT, typename GT, bool COMPL, int TEAMS>
 __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs a, int tiles, int blocks) {
   constexpr int R = SCAN_ROWS / WAVES;
-  using S = Shared<VEC, R>;
+  using S = Shared<R>;
   __shared__ S sh;
   const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const bool hand_on = tiles > 1;
@@ -355,18 +411,19 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs 
     empty_sequences(a, ticket - tiles * blocks, a.dfinal, a.ds0, tid);
     return;
   }
-  const int first = (ticket % blocks) * S::NCH;
+  const int first = (ticket % blocks) * NCH;
   const int64_t r0 = (int64_t)tile * SCAN_ROWS;
   const bool mine = first + lane * VEC < a.D;
   const uint32_t ch = mine ? first + lane * VEC : 0;
+  const Tail tail{first + NCH > a.D && (a.D & 1), (uint32_t)a.D - 1};
   const int64_t t0 = r0 + w * R;
 
-  Pack<GT, VEC> graw[R];
-  Pack<XT, VEC> xraw[R], draw[R];
-  load_rows<R>(graw, (const GT *)a.g, a.g_st, t0, a.T, ch, a.streamed);
-  load_rows<R>(xraw, (const XT *)a.x, a.x_st, t0, a.T, ch, a.streamed);
-  load_rows<R>(draw, (const XT *)a.dout, a.do_st, t0, a.T, ch, a.streamed);
-  const bool live = tid < S::NCH && first + tid < a.D;  // lane tid < NCH: channel first + tid of the hand-over
+  Pair<GT> graw[R];
+  Pair<XT> xraw[R], draw[R];
+  load_rows<R>(graw, (const GT *)a.g, a.g_st, t0, a.T, ch, tail, a.streamed);
+  load_rows<R>(xraw, (const XT *)a.x, a.x_st, t0, a.T, ch, tail, a.streamed);
+  load_rows<R>(draw, (const XT *)a.dout, a.do_st, t0, a.T, ch, tail, a.streamed);
+  const bool live = tid < NCH && first + tid < a.D;  // lane tid < NCH: channel first + tid of the hand-over
   float state = 0.f;
   if (live) state = a.checkpoints[(int64_t)tile * a.D + first + tid];
   const int64_t c0 = bound_at(a.cu, a.cu_is64, 0, a.T), cN = bound_at(a.cu, a.cu_is64, a.N, a.T);
@@ -377,7 +434,7 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs 
   float d[R][VEC], m[COMPL ? R : 1][VEC], h[VEC] = {}, sum[VEC] = {};
   auto restart = [&](int r) {  // a sequence's first row
     if (a.s0) {
-      const Pack<float, VEC> s0 = load_pack<float, VEC>(a.s0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch);
+      const Pair<float> s0 = load_pair(a.s0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch, tail);
 #pragma unroll
       for (int c = 0; c < VEC; ++c) h[c] = s0.v[c];
     } else {
@@ -419,7 +476,7 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs 
     sh.B[w][lane * VEC + c] = h[c];
   }
   __syncthreads();
-  if (tid < S::NCH) {
+  if (tid < NCH) {
 #pragma unroll
     for (int v = 0; v < WAVES; ++v) {
       const float next = apply(sh.A[v][tid], state, sh.B[v][tid]);
@@ -450,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs 
   float e[VEC] = {};
   auto last_row = [&](int r, float (&e)[VEC]) {  // a sequence's last row: e comes from d_final_state
     if (a.dfinal) {
-      const Pack<float, VEC> f = load_pack<float, VEC>(a.dfinal + (int64_t)uniform(sh.end_id[w * R + r]) * a.D, ch);
+      const Pair<float> f = load_pair(a.dfinal + (int64_t)uniform(sh.end_id[w * R + r]) * a.D, ch, tail);
 #pragma unroll
       for (int c = 0; c < VEC; ++c) e[c] = f.v[c];
     } else {
@@ -480,37 +537,9 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs 
   }
   __syncthreads();
 
-  if (tid < S::NCH) {
-    const int64_t rl = r0 + SCAN_ROWS - 1;  // the tile's last row
-    float carry = 0.f;
-    if (hand_on) {
-      const bool needs = tile + 1 < tiles && sh.end_id[SCAN_ROWS - 1] < 0 && rl >= c0 && rl < cN;
-      float A = 1.f, B = 0.f;
-#pragma unroll
-      for (int v = WAVES - 1; v >= 0; --v) {
-        B = apply(sh.A[v][tid], B, sh.B[v][tid]);
-        A *= sh.A[v][tid];
-      }
-      if (!needs) A = 0.f;
-      uint64_t *words = (uint64_t *)((char *)a.ws + 256);
-      const uint32_t col = first + tid;
-      const bool publish = live && tile > 0;
-      if (publish)
-        __hip_atomic_store(at(words + (int64_t)tile * a.D, col), make_word(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (needs) {
-        carry = entering(at(words + (int64_t)(tile + 1) * a.D, col), a.D, tiles - 1 - tile, live);
-        if (publish && A != 0.f)
-          __hip_atomic_store(at(words + (int64_t)tile * a.D, col), make_word(0.f, fmaf(A, carry, B)), __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
-      }
-    }
-#pragma unroll
-    for (int v = WAVES - 1; v >= 0; --v) {
-      const float next = apply(sh.A[v][tid], carry, sh.B[v][tid]);
-      sh.A[v][tid] = carry;
-      carry = next;
-    }
-  }
+  const int64_t rl = r0 + SCAN_ROWS - 1;  // the tile's last row
+  hand_over<TEAMS, true>(sh, a, tile, tiles, tile + 1 < tiles && sh.end_id[SCAN_ROWS - 1] < 0 && rl >= c0 && rl < cN,
+                         first, tid);
   __syncthreads();
 
 #pragma unroll
@@ -531,13 +560,13 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs 
     using DG = decltype(dg_type);
     DX *dx_row = (DX *)a.dx + (t0 + R - 1) * a.dx_st;
     DG *dg_row = (DG *)a.dg + (t0 + R - 1) * a.dg_st;
-    if ((starts | ends) == 0 && t0 >= c0 && t0 + R <= cN) {
+    if ((starts | ends) == 0 && t0 >= c0 && t0 + R <= cN && !tail.on) {
 #pragma unroll
       for (int r = R - 1; r >= 0; --r, dx_row -= a.dx_st, dg_row -= a.dg_st) {
         gradients(r);
         if (mine) {
-          store_pack<DX, VEC>(dx_row, ch, dx);
-          store_pack<DG, VEC>(dg_row, ch, dg);
+          store_pair(dx_row, ch, dx);
+          store_pair(dg_row, ch, dg);
         }
       }
       return;
@@ -551,11 +580,11 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs 
         for (int c = 0; c < VEC; ++c) dx[c] = dg[c] = 0.f;
       }
       if (mine && t0 + r < a.T) {
-        store_pack<DX, VEC>(dx_row, ch, dx);
-        store_pack<DG, VEC>(dg_row, ch, dg);
+        store_pair(dx_row, ch, dx, tail);
+        store_pair(dg_row, ch, dg, tail);
       }
       if ((starts >> r & 1) && a.ds0 && mine)
-        store_pack<float, VEC>(a.ds0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch, e);
+        store_pair(a.ds0 + (int64_t)uniform(sh.start_id[w * R + r]) * a.D, ch, e, tail);
     }
   };
   if (a.dx_f32) {
@@ -597,20 +626,20 @@ __global__ void __launch_bounds__(256) gdp_scan_fill_kernel(uint4 *p, int64_t n)
     p[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
 }
 
-// whether pieces of `vec` elements of es bytes are aligned in every row
-bool aligned(const void *p, int64_t stride, int es, int vec) {
-  return !p || (((uintptr_t)p & (vec * es - 1)) == 0 && stride % vec == 0);
-}
-
 struct Grid { int tiles, blocks; unsigned jobs; };
 
-Grid grid_of(const ScanArgs &a, int rows, int channels, bool empties) {
+Grid grid_of(const ScanArgs &a, int rows, bool empties) {
   Grid g;
   g.tiles = (int)((a.T + rows - 1) / rows);
-  g.blocks = (int)((a.D + channels - 1) / channels);
+  g.blocks = (int)((a.D + NCH - 1) / NCH);
   g.jobs = (unsigned)((int64_t)g.tiles * g.blocks + (empties ? (a.N + 63) / 64 : 0));
   return g;
 }
+
+// Channel blocks up to which four lanes per channel look back, over 32 tiles.  The
+// workgroups that run at once then work on more tiles of each block, and how far the
+// known states come per look bounds the rate, not the memory.
+constexpr int NARROW = 4;
 
 hipError_t fill_words(const ScanArgs &a, const Grid &g, hipStream_t stream) {
   if (g.tiles <= 1) return hipSuccess;
@@ -620,22 +649,29 @@ hipError_t fill_words(const ScanArgs &a, const Grid &g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <typename XT, typename GT, int VEC, int R> hipError_t run_scan(ScanArgs a, hipStream_t stream) {
+template <typename XT, typename GT> hipError_t run_scan(ScanArgs a, hipStream_t stream) {
+  constexpr int R = 16;
   a.streamed = a.T * a.D * (int64_t)(2 * sizeof(XT) + sizeof(GT)) > STREAM_BYTES;
-  const Grid k = grid_of(a, WAVES * R, 64 * VEC, a.N > 0 && (a.final_state || a.cache));
+  const Grid k = grid_of(a, WAVES * R, a.N > 0 && (a.final_state || a.cache));
   if (k.jobs == 0) return hipSuccess;
   if (hipError_t e = fill_words(a, k, stream)) return e;
-  auto *kernel = a.complement ? gdp_scan_kernel<XT, GT, VEC, R, true> : gdp_scan_kernel<XT, GT, VEC, R, false>;
+  auto *kernel = k.blocks <= NARROW ? (a.complement ? gdp_scan_kernel<XT, GT, R, true, MOST_TEAMS>
+                                                    : gdp_scan_kernel<XT, GT, R, false, MOST_TEAMS>)
+                                    : (a.complement ? gdp_scan_kernel<XT, GT, R, true, 1>
+                                                    : gdp_scan_kernel<XT, GT, R, false, 1>);
   hipLaunchKernelGGL(kernel, dim3(k.jobs), dim3(THREADS), 0, stream, a, k.tiles, k.blocks);
   return hipGetLastError();
 }
 
-template <typename XT, typename GT, int VEC> hipError_t run_backward(ScanArgs a, hipStream_t stream) {
+template <typename XT, typename GT> hipError_t run_backward(ScanArgs a, hipStream_t stream) {
   a.streamed = a.T * a.D * (int64_t)(3 * sizeof(XT) + 2 * sizeof(GT)) > STREAM_BYTES;
-  const Grid k = grid_of(a, SCAN_ROWS, 64 * VEC, a.N > 0 && a.ds0);
+  const Grid k = grid_of(a, SCAN_ROWS, a.N > 0 && a.ds0);
   if (k.jobs == 0) return hipSuccess;
   if (hipError_t e = fill_words(a, k, stream)) return e;
-  auto *kernel = a.complement ? gdp_scan_backward_kernel<XT, GT, VEC, true> : gdp_scan_backward_kernel<XT, GT, VEC, false>;
+  auto *kernel = k.blocks <= NARROW ? (a.complement ? gdp_scan_backward_kernel<XT, GT, true, MOST_TEAMS>
+                                                    : gdp_scan_backward_kernel<XT, GT, false, MOST_TEAMS>)
+                                    : (a.complement ? gdp_scan_backward_kernel<XT, GT, true, 1>
+                                                    : gdp_scan_backward_kernel<XT, GT, false, 1>);
   hipLaunchKernelGGL(kernel, dim3(k.jobs), dim3(THREADS), 0, stream, a, k.tiles, k.blocks);
   return hipGetLastError();
 }
@@ -653,28 +689,11 @@ bool scan_served(int64_t T, int64_t N, int64_t D) {
 }
 
 hipError_t launch_scan(const ScanArgs &a, int xt, int gt, hipStream_t stream) {
-  return by_types(xt, gt, [&](auto x, auto g) {
-    using XT = decltype(x);
-    using GT = decltype(g);
-    constexpr int VEC = 2;
-    const bool vec = a.D % VEC == 0 && aligned(a.x, a.x_st, sizeof(XT), VEC) && aligned(a.g, a.g_st, sizeof(GT), VEC) &&
-                     aligned(a.o, a.o_st, sizeof(XT), VEC) && aligned(a.s0, 0, 4, VEC) &&
-                     aligned(a.final_state, 0, 4, VEC) && aligned(a.cache, 0, 4, VEC);
-    return vec ? run_scan<XT, GT, VEC, 16>(a, stream) : run_scan<XT, GT, 1, 16>(a, stream);
-  });
+  return by_types(xt, gt, [&](auto x, auto g) { return run_scan<decltype(x), decltype(g)>(a, stream); });
 }
 
 hipError_t launch_scan_backward(const ScanArgs &a, int xt, int gt, hipStream_t stream) {
-  return by_types(xt, gt, [&](auto x, auto g) {
-    using XT = decltype(x);
-    using GT = decltype(g);
-    constexpr int VEC = 2;
-    const bool vec = a.D % VEC == 0 && aligned(a.x, a.x_st, sizeof(XT), VEC) && aligned(a.g, a.g_st, sizeof(GT), VEC) &&
-                     aligned(a.dout, a.do_st, sizeof(XT), VEC) && aligned(a.dx, a.dx_st, a.dx_f32 ? 4 : sizeof(XT), VEC) &&
-                     aligned(a.dg, a.dg_st, a.dg_f32 ? 4 : sizeof(GT), VEC) && aligned(a.s0, 0, 4, VEC) &&
-                     aligned(a.dfinal, 0, 4, VEC) && aligned(a.ds0, 0, 4, VEC);
-    return vec ? run_backward<XT, GT, VEC>(a, stream) : run_backward<XT, GT, 1>(a, stream);
-  });
+  return by_types(xt, gt, [&](auto x, auto g) { return run_backward<decltype(x), decltype(g)>(a, stream); });
 }
 
 hipError_t launch_scan_decode(const ScanDecodeArgs &a, int xt, int gt, hipStream_t stream) {
