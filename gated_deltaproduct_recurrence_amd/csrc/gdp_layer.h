@@ -11,8 +11,9 @@
 
 namespace gdp {
 
-// rows of the token stream per tile of the recurrence and per checkpoint
-constexpr int SCAN_ROWS = 64;
+// rows of the token stream per checkpoint and per tile of the gradients, and per tile
+// of the forward pass
+constexpr int SCAN_ROWS = 64, SCAN_FORWARD_ROWS = 128;
 
 struct ScanArgs {
   const void *x; int64_t x_st;          // [T, D]
@@ -32,10 +33,11 @@ struct ScanArgs {
   void *dx; int64_t dx_st; int dx_f32;  // [T, D] float32 or x's type
   void *dg; int64_t dg_st; int dg_f32;  // [T, D] float32 or g's type
   float *ds0;                           // [N, D] or null
-  void *ws;                             // scan_state_bytes(T, D)
+  void *ws;                             // scan_state_bytes(T, D, rows per tile)
   int streamed;                         // set by the launch: the rows' loads bypass the caches
 };
-size_t scan_state_bytes(int64_t T, int64_t D);
+// the counter and the words through which tiles of `rows` rows hand their states on
+size_t scan_state_bytes(int64_t T, int64_t D, int rows);
 // whether the launch grids of these sizes fit
 bool scan_served(int64_t T, int64_t N, int64_t D);
 hipError_t launch_scan(const ScanArgs &a, int x_type, int g_type, hipStream_t stream);

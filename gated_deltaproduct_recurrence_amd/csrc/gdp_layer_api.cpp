@@ -100,12 +100,12 @@ extern "C" {
 
 size_t gdp_gated_scan_workspace_bytes(int64_t T, int64_t N, int64_t D) {
   if (!scan_sizes_ok(T, N, D)) return 0;
-  return align256(scan_state_bytes(T, D));
+  return scan_state_bytes(T, D, SCAN_FORWARD_ROWS);
 }
 
 size_t gdp_gated_scan_backward_workspace_bytes(int64_t T, int64_t N, int64_t D) {
   if (!scan_sizes_ok(T, N, D)) return 0;
-  return align256(scan_state_bytes(T, D)) + align256((size_t)checkpoint_rows(T) * D * 4);
+  return scan_state_bytes(T, D, SCAN_ROWS) + align256((size_t)checkpoint_rows(T) * D * 4);
 }
 
 int gdp_gated_scan(const gdp_tensor *x, const gdp_tensor *g_log, const gdp_tensor *cu_seqlens,
@@ -294,7 +294,7 @@ int gdp_gated_scan_backward(const gdp_tensor *x, const gdp_tensor *g_log, const 
     a.checkpoints = (float *)checkpoints->data;
   } else {
     // the states at the checkpoints again, into the workspace behind the scan's words
-    a.checkpoints = (float *)((char *)workspace + align256(scan_state_bytes(T, D)));
+    a.checkpoints = (float *)((char *)workspace + scan_state_bytes(T, D, SCAN_ROWS));
     if ((e = launch_scan(a, xt, gt, (hipStream_t)stream)) != hipSuccess)
       return fail(GDP_EHIP, "scan launch: %s", hipGetErrorString(e));
   }

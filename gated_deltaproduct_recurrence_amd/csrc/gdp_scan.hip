@@ -650,7 +650,7 @@ hipError_t fill_words(const ScanArgs &a, const Grid &g, hipStream_t stream) {
 }
 
 template <typename XT, typename GT> hipError_t run_scan(ScanArgs a, hipStream_t stream) {
-  constexpr int R = 16;
+  constexpr int R = SCAN_FORWARD_ROWS / WAVES;
   a.streamed = a.T * a.D * (int64_t)(2 * sizeof(XT) + sizeof(GT)) > STREAM_BYTES;
   const Grid k = grid_of(a, WAVES * R, a.N > 0 && (a.final_state || a.cache));
   if (k.jobs == 0) return hipSuccess;
@@ -678,14 +678,16 @@ template <typename XT, typename GT> hipError_t run_backward(ScanArgs a, hipStrea
 
 }  // namespace
 
-size_t scan_state_bytes(int64_t T, int64_t D) {
-  const int64_t tiles = (T + SCAN_ROWS - 1) / SCAN_ROWS;
+size_t scan_state_bytes(int64_t T, int64_t D, int rows) {
+  const int64_t tiles = (T + rows - 1) / rows;
   return tiles <= 1 ? 0 : (256 + (size_t)tiles * D * 8 + 255) & ~(size_t)255;
 }
 
+// The grids are 32-bit (one workgroup per 64 rows and 128 channels at most, and one
+// per 64 sequences), a row's channels are reached by 32-bit byte offsets.
 bool scan_served(int64_t T, int64_t N, int64_t D) {
-  const int64_t tiles = T / SCAN_ROWS + 1, blocks = D / 64 + 1;
-  return N < INT32_MAX && D / 256 < 65535 && tiles < INT32_MAX && blocks < INT32_MAX / tiles - N / 64 - 1;
+  if (T >= (int64_t)1 << 36 || N >= INT32_MAX || D >= (int64_t)1 << 24) return false;
+  return (T / SCAN_ROWS + 1) * (D / NCH + 1) + N / 64 + 1 < INT32_MAX;
 }
 
 hipError_t launch_scan(const ScanArgs &a, int xt, int gt, hipStream_t stream) {

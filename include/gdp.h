@@ -344,10 +344,10 @@ int gdp_chunk_gated_delta_product(const gdp_tensor *q, const gdp_tensor *k, cons
 #define GDP_SCAN_CHECKPOINT_ROWS 64
 
 /* Host-only.  Workspace bytes gdp_gated_scan needs for T rows, N sequences and D
- * channels: a ticket counter and, per 64 rows and channel, one 8-byte word through
+ * channels: a ticket counter and, per 128 rows and channel, one 8-byte word through
  * which the workgroups of a long sequence hand their states on.  The call writes
  * it before use and leaves nothing in it that a later call reads.  Returns 0 for
- * invalid sizes. */
+ * invalid sizes and where none is needed (up to 128 rows). */
 size_t gdp_gated_scan_workspace_bytes(int64_t T, int64_t N, int64_t D);
 
 /* Device.  The gated linear recurrence over packed sequences.  For every sequence
@@ -356,8 +356,10 @@ size_t gdp_gated_scan_workspace_bytes(int64_t T, int64_t N, int64_t D);
  *     u_t = x[t, d], or (1 - a_t) x[t, d] with complement_input.
  *   x            [T, D]    f32, bf16 or f16; rows may be strided
  *   g_log        [T, D]    f32 or x's dtype; log decays, g_log <= 0 (a positive
- *                          entry is served while the products of decays over 64
- *                          rows stay finite in float32); -inf restarts the channel
+ *                          entry is served while the products of decays over 128
+ *                          rows stay finite in float32); -inf drops the state before
+ *                          (the rows behind a -inf that meets a state which is not
+ *                          finite are unspecified)
  *   cu_seqlens   [N+1]     int32 or int64, contiguous
  *   initial_state [N, D]   f32 contiguous, or data == NULL for zeros
  *   output_final_state     write final_state when nonzero
@@ -442,7 +444,8 @@ enum gdp_activation { GDP_ACT_NONE = 0, GDP_ACT_SILU = 1, GDP_ACT_SIGMOID = 2 };
  *   activation   a gdp_activation
  *   eps          > 0
  *   y            [T, G, V]  x's dtype, may be strided
- * Statistics and products are float32; y is rounded once.  y may not overlap an input
+ * Statistics and products are float32 (the squares of x - mean must stay finite
+ * there); y is rounded once.  y may not overlap an input
  * (GDP_EALIAS).  V <= 16384 and G <= 65535 (GDP_EUNSUPPORTED otherwise).  One launch on
  * `stream`; capturable. */
 int gdp_group_norm(const gdp_tensor *x, const gdp_tensor *weight, const gdp_tensor *bias, const gdp_tensor *gate,

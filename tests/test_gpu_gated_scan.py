@@ -218,6 +218,13 @@ def test_long_axis_few_channels(gdp):
     check_scan(gdp, x, g, cu, s0, False)
 
 
+@pytest.mark.parametrize("D,dtype,gate,complement", [(700, F32, F32, True), (769, BF16, F32, False), (640, F16, F16, True)])
+def test_long_axis_many_channels(gdp, D, dtype, gate, complement):
+    """Many blocks handed on in more than four channel blocks; the last of 769 channels is alone in its block."""
+    x, g, cu, s0 = make([2500, 1, 700, 129], D, dtype, gate, seed=23, shift=5.0)
+    check_scan(gdp, x, g, cu, s0, complement)
+
+
 def test_two_runs_give_the_same_bits(gdp):
     x, g, cu, s0 = (dev(t) for t in make([5000, 1, 3000, 900], 512, BF16, F32, seed=16))
     d_o = torch.randn(x.shape, device="cuda").to(BF16)
@@ -311,7 +318,7 @@ def test_other_streams_and_workspaces(gdp):
 
 
 def test_graph_replay(gdp):
-    """Forward, gradients and norm-free decode captured with shared workspaces in two graphs; each replay,
+    """Forward pass, gradients and single-token step captured with shared workspaces in two graphs; each replay,
     with new boundaries and eager work between them, gives the eager result."""
     x, g, cu, s0 = (dev(t) for t in make([700, 300, 24], 256, BF16, F32, seed=21))
     d_o = torch.randn(x.shape, device="cuda").to(BF16)
