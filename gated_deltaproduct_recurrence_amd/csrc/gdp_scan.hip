@@ -156,8 +156,9 @@ template <int R> __device__ __forceinline__ uint32_t marked(const int *ids, int 
 // The state entering this tile, of one channel, from the words of the `count` tiles
 // before it: `word` is the nearest one's, the others lie `step` words apart.  Team
 // `team` of TEAMS looks at the words team * WINDOW and on; a team that finds all of
-// its words but none with A = 0 goes on from the state that the next team found.
-// Only team 0's value is used; the others stop when it has one.
+// its words but none with A = 0 waits (in LDS) for the state that the next team finds,
+// which the known states reach first.  Only team 0's value is used; the others stop
+// when it has one.
 template <int TEAMS, typename S>
 __device__ __forceinline__ float entering(S &sh, const uint64_t *word, int64_t step, int64_t count, bool live, int team,
                                           int c) {
@@ -195,9 +196,15 @@ __device__ __forceinline__ float entering(S &sh, const uint64_t *word, int64_t s
     for (int i = NEAR; i < WINDOW; ++i) v[i] = read(word, i);
     for (;;) {
       look(WINDOW);
-      const bool beyond = TEAMS > 1 && team + 1 < TEAMS && !__all(found) && signal(team + 1);
-      if (beyond) h = sh.found[team + 1][c];
-      if (__all(found || (open && beyond))) break;
+      if (__all(found)) break;
+      if (TEAMS > 1 && team + 1 < TEAMS && __all(found || open)) {  // nothing more to read: the next team's state
+        while (!signal(team + 1)) {
+          if (team > 0 && signal(0)) return 0.f;
+          __builtin_amdgcn_s_sleep(1);
+        }
+        h = sh.found[team + 1][c];
+        break;
+      }
       if (TEAMS > 1 && team > 0 && signal(0)) return 0.f;
       __builtin_amdgcn_s_sleep(1);
       asm volatile("" : "+v"(word));  // or every word's address is kept in registers over the loop
