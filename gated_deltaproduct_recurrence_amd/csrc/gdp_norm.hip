@@ -16,6 +16,15 @@
 // weights and, in the backward pass, its partial sums of dw and db, in registers.
 // The raw values of a team's next token are loaded before the current one is
 // computed.
+//
+// What bounds it, measured on MI355X (a 1 GiB copy reaches 5.0 TB/s): the memory.
+// 65536 x 32 x 128 bfloat16 with a gate: 266 us, 6.0 TB/s; the gradients of 32768 x 16
+// x 128: 118 us, 5.7 TB/s.  Operands that fit the memory-side cache and are left to it
+// stay below that: 8195 x 8 x 512 float16 without a gate 34 us, 3.9 TB/s (dropping the
+// reductions or the sigmoid changes it by 1 to 2 us).
+//   Grid: 1024 workgroups forward and 768 backward, about one resident round.  Twice
+// as many cost 13% forward, one for every 32 pairs 5%.
+// Two tokens per step and team cost 20%.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

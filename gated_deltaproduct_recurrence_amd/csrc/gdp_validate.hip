@@ -7,7 +7,7 @@
 // the calls do not check them by default: every kernel clamps sequence ranges to
 // [0, T] and skips slots outside the cache, which keeps a bad value in bounds
 // but gives undefined results.  With GDP_DEBUG_VALIDATE=1 in the environment the
-// prefill and decode calls first launch gdp_validate_kernel, which ORs a bit per
+// prefill, scan and decode calls first launch gdp_validate_kernel, which ORs a bit per
 // kind of fault into a device-global word:
 //   GDP_DBG_CU    cu_seqlens decreases somewhere, or an entry lies outside [0, T]
 //   GDP_DBG_SLOT  a state index is below -1 or not below the number of cache slots

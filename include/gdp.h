@@ -475,8 +475,8 @@ int gdp_group_norm_backward(const gdp_tensor *x, const gdp_tensor *weight, const
  * in bounds (every kernel clamps sequence ranges to [0, T] and skips slots
  * outside the cache), but the results are then undefined.  With the environment
  * variable GDP_DEBUG_VALIDATE=1, gdp_chunk_prefill (and the entries built on it),
- * gdp_recurrent_decode, gdp_gated_scan and gdp_gated_scan_decode first launch a
- * check on their stream.  The check ORs
+ * gdp_recurrent_decode, gdp_gated_scan, gdp_gated_scan_decode and
+ * gdp_gated_scan_backward first launch a check on their stream.  The check ORs
  * these bits into a word kept per device:
  *   GDP_DBG_CU    cu_seqlens decreases somewhere, or an entry lies outside [0, T]
  *                 (Megatron Core page, chunk_gated_delta_product_varlen: the
