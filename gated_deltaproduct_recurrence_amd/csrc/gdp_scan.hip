@@ -42,8 +42,8 @@
 //   Tile: 128 rows x 128 channels (16 rows and a pair of channels per lane).  With 64
 // rows the second shape took 1045 us instead of 743 (twice the words, twice the hops);
 // 4 channels per lane and 8 rows 838; one channel per lane 1012.
-//   Window: 8 tiles; 16 cost 3% on the wide shapes (registers, words read), 4 cost 30%
-// where there are few channel blocks.
+//   Window: 8 tiles; 16 cost 3% on the wide shapes (registers, words read), 4 gained 1%
+// there and cost 25% at 1024 channels.
 //   Three workgroups per CU (80 registers) spill: 1650 us.  Workgroups that stay and
 // draw their next ticket ahead: 853 us.
 
@@ -58,8 +58,8 @@ namespace {
 
 constexpr int WAVES = 8, THREADS = 64 * WAVES;
 constexpr int VEC = 2, NCH = 64 * VEC;  // channels per lane and per workgroup
-constexpr int WINDOW = 8;               // tiles before its own that a lane looks at
-constexpr int MOST_TEAMS = THREADS / NCH;  // lanes per channel that can look
+constexpr int MOST_TEAMS = THREADS / NCH;  // lanes per channel that can look at the tiles before
+template <int TEAMS> constexpr int WINDOW_OF = TEAMS > 1 ? 12 : 8;  // tiles that each of them looks at
 constexpr uint64_t NOT_WRITTEN = ~0ull;
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -177,6 +177,7 @@ template <int R> __device__ __forceinline__ uint32_t marked(const int *ids, int 
 template <int TEAMS, typename S>
 __device__ __forceinline__ float entering(S &sh, const uint64_t *word, int64_t step, int64_t count, bool live, int team,
                                           int c) {
+  constexpr int WINDOW = WINDOW_OF<TEAMS>;
   const int half = c >> 6;
   if (TEAMS > 1) {
     count -= team * WINDOW;
@@ -663,10 +664,11 @@ Grid grid_of(const ScanArgs &a, int rows, bool empties) {
   return g;
 }
 
-// Channel blocks up to which four lanes per channel look back, over 32 tiles.  The
+// Channel blocks up to which four lanes per channel look back, over 48 tiles.  The
 // workgroups that run at once then work on more tiles of each block, and how far the
-// known states come per look bounds the rate, not the memory: 131072 rows of 64, 512
-// and 1024 channels take 98, 127 and 227 us with four lanes and 149, 177 and 222 with one.
+// known states come per look bounds the rate, not the memory: 131072 rows of 64, 256
+// and 512 channels take 86, 99 and 130 us with four lanes and 149, 167 and 177 with one
+// (98, 113 and 127 with windows of 8); 1024 channels 227 and 222.
 constexpr int NARROW = 4;
 
 hipError_t fill_words(const ScanArgs &a, const Grid &g, hipStream_t stream) {
