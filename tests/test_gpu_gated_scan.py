@@ -77,7 +77,7 @@ def check_scan(gdp, x, g, cu, s0, complement, xd=None, gd=None, out=None):
             assert r["d_initial_state"] is None
 
 
-LENGTHS = [[1], [63], [64], [65], [1] * 200, [0, 5, 0, 0, 130, 0], [200, 57, 64, 128, 1], [700], []]
+LENGTHS = [[1], [63], [64], [65], [127], [128], [129], [128, 256, 1], [1] * 200, [0, 5, 0, 0, 130, 0], [200, 57, 64, 128, 1], [700], []]
 
 
 @pytest.mark.parametrize("lens", LENGTHS, ids=lambda v: "x".join(map(str, v[:6])) or "none")
@@ -113,6 +113,70 @@ def test_many_short_sequences(gdp, count):
 
 def test_many_empty_sequences(gdp):
     check_scan(gdp, *make([0] * 1500 + [70] + [0] * 1500 + [1, 65], 12, F32, F32), False)
+
+
+def test_very_many_sequences(gdp):
+    """More than 512 x 512 sequences, mostly empty: the search for a tile's sequences takes two steps."""
+    N, D = 300000, 4
+    lens = torch.zeros(N, dtype=torch.int64)
+    lens[500::1000] = 3
+    cu = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    gen = torch.Generator().manual_seed(24)
+    T = int(cu[-1])
+    x, g, s0 = torch.randn(T, D, generator=gen), -torch.rand(T, D, generator=gen), torch.randn(N, D, generator=gen)
+    full = lens > 0
+    ref = layers.scan(x, g, list(range(0, T + 1, 3)), s0[full])
+    o, fs = gdp.gated_scan(x.cuda(), g.cuda(), cu.cuda(), initial_state=s0.cuda(), output_final_state=True)
+    close(o, ref["o"], ref["o_bound"], ("o", F32))
+    close(fs[full.cuda()], ref["final"], ref["final_bound"], ("final", F32))
+    assert torch.equal(fs[~full.cuda()].cpu(), s0[~full])
+    d = gdp.gated_scan_backward(x.cuda(), g.cuda(), cu.cuda(), x.cuda(), d_final_state=s0.cuda(), initial_state=s0.cuda())
+    want = layers.scan_backward(x, g, list(range(0, T + 1, 3)), x, s0[full], s0[full])
+    close(d["dx"], want["dx"], want["dx_bound"], ("dx", F32))
+    close(d["d_initial_state"][full.cuda()], want["ds0"], want["ds0_bound"], ("ds0", F32))
+    assert torch.equal(d["d_initial_state"][~full.cuda()].cpu(), s0[~full])
+
+
+@pytest.mark.parametrize("D", [96, 131])
+def test_strided_gradients_and_decode_rows(gdp, D):
+    """Gradients and single-token rows inside wider buffers, through the direct calls."""
+    x, g, cu, s0 = make([90, 64, 33], D, BF16, BF16, seed=25, first=5, behind=9)
+    T, N = x.shape[0], 3
+    d_o = torch.randn(T, D, generator=torch.Generator().manual_seed(26)).to(BF16)
+    want = layers.scan_backward(x, g, cu.tolist(), d_o, None, s0)
+    wide = {k: torch.full((T, D + 7), 9.0, dtype=t, device="cuda") for k, t in (("do", BF16), ("dx", F32), ("dg", BF16))}
+    wide["do"][:, 3:3 + D] = d_o.cuda()
+    views = {k: t[:, 3:3 + D] for k, t in wide.items()}
+    ds0 = torch.empty(N, D, device="cuda")
+    ws = torch.empty(gdp.gdp_gated_scan_backward_workspace_bytes(T, N, D), dtype=torch.uint8, device="cuda")
+    gdp.gdp_gated_scan_backward(x.cuda(), g.cuda(), cu.cuda(), False, s0.cuda(), None, views["do"], None, views["dx"],
+                                views["dg"], ds0, ws)
+    close(views["dx"], want["dx"], want["dx_bound"], ("dx", F32))
+    close(views["dg"], want["dg"], want["dg_bound"], ("dg", BF16))
+    close(ds0, want["ds0"], want["ds0_bound"], ("ds0", F32))
+    for k in ("dx", "dg"):
+        assert (wide[k][:, :3] == 9).all() and (wide[k][:, 3 + D:] == 9).all(), k
+    cache, slots = torch.randn(8, D), torch.tensor([7, 1, 4])
+    ref = layers.decode(x[:3], g[:3], cache, slots, True)
+    xw, ow = (torch.full((3, D + 5), 9.0, dtype=BF16, device="cuda") for _ in range(2))
+    xw[:, 2:2 + D] = x[:3].cuda()
+    cd = cache.cuda()
+    gdp.gated_scan_decode(xw[:, 2:2 + D], g[:3].cuda(), cd, slots.cuda(), complement_input=True, out=ow[:, 2:2 + D])
+    close(ow[:, 2:2 + D], ref["o"], ref["o_bound"], ("o", BF16))
+    close(cd, ref["cache"], ref["cache_bound"], ("cache", F32))
+    assert (ow[:, :2] == 9).all() and (ow[:, 2 + D:] == 9).all()
+
+
+def test_operands_elsewhere_are_refused(gdp):
+    x, g = torch.randn(10, 8, device="cuda"), -torch.rand(10, 8, device="cuda")
+    with pytest.raises(ValueError, match="expected a tensor on cuda"):
+        gdp.gated_scan(x, g, torch.tensor([0, 10], dtype=torch.int32))
+    with pytest.raises(ValueError, match="expected a tensor on cuda"):
+        gdp.gated_scan_decode(x, g, torch.zeros(10, 8, device="cuda"), torch.zeros(10, dtype=torch.int32))
+    with pytest.raises(ValueError, match="unsupported dtype"):
+        gdp.gated_scan(x.double(), g, torch.tensor([0, 10], dtype=torch.int32, device="cuda"))
+    with pytest.raises(gdp.GdpError, match="x and o must share one dtype"):
+        gdp.gated_scan(x, g, torch.tensor([0, 10], dtype=torch.int32, device="cuda"), out=torch.empty_like(x, dtype=BF16))
 
 
 def test_int64_boundaries_and_strided_rows(gdp):

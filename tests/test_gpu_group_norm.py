@@ -106,6 +106,22 @@ def test_strided_operands(gdp):
     check_norm(gdp, x, w, b, z, dyb, "silu", True, dyd=dy[:, :1].cuda().expand(-1, 4, -1))
 
 
+@pytest.mark.parametrize("V", [64, 65])
+def test_strided_gradients(gdp, V):
+    """Gradients written into wider buffers and with the groups as the outer dimension, through the direct call."""
+    x, w, b, z, dy = make(30, 3, V, F32, weight="channel", bias=True, seed=17)
+    want = layers.norm(x, w, b, z, "sigmoid", True, 1e-5, dy)
+    wide = torch.full((30, 3, V + 9), 9.0, device="cuda")
+    outer = torch.full((3, 31, V), 9.0, device="cuda")
+    dx, dz = wide[:, :, 4:4 + V], outer[:, :30].transpose(0, 1)
+    dw, db = torch.empty(3, V, device="cuda"), torch.empty(3, V, device="cuda")
+    ws = torch.empty(gdp.gdp_group_norm_backward_workspace_bytes(30, 3, V), dtype=torch.uint8, device="cuda")
+    gdp.gdp_group_norm_backward(x.cuda(), w.cuda(), b.cuda(), z.cuda(), "sigmoid", True, 1e-5, dy.cuda(), dx, dw, db, dz, ws)
+    for name, got in (("dx", dx), ("dgate", dz), ("dweight", dw), ("dbias", db)):
+        close(got, want[name], want[name + "_bound"], name, F32)
+    assert (wide[:, :, :4] == 9).all() and (wide[:, :, 4 + V:] == 9).all() and (outer[:, 30] == 9).all()
+
+
 def test_large_means_and_flat_groups(gdp):
     """A mean far above the spread (two passes over the values), and groups of equal values."""
     x, w, b, z, dy = make(16, 2, 256, F32, bias=True, seed=6)
