@@ -30,7 +30,9 @@
 // Tiles are handed out by an atomic counter, rows ascending, so a workgroup waits
 // only for tiles whose workgroups are running, and those publish their pairs before
 // they wait themselves: the first of the waiting tiles finds its predecessor's word
-// at A = 0, so every wait ends.
+// at A = 0, so every wait ends.  (It is bounded all the same, at 2^21 looks, seconds:
+// when calls on two streams share a workspace against the contract, tickets can be
+// lost, and the rows behind then become NaN instead of the GPU hanging.)
 //
 // What bounds it, measured on MI355X (a 1 GiB copy reaches 5.0 TB/s).  32768 x 2048
 // bfloat16 with float32 gates: 112 us, 4.8 TB/s of the operands' bytes; 131104 x 4096
@@ -61,6 +63,7 @@ constexpr int VEC = 2, NCH = 64 * VEC;  // channels per lane and per workgroup
 constexpr int MOST_TEAMS = THREADS / NCH;  // lanes per channel that can look at the tiles before
 template <int TEAMS> constexpr int WINDOW_OF = TEAMS > 1 ? 12 : 8;  // tiles that each of them looks at
 constexpr uint64_t NOT_WRITTEN = ~0ull;
+constexpr int MOST_LOOKS = 1 << 21;
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
@@ -210,11 +213,15 @@ __device__ __forceinline__ float entering(S &sh, const uint64_t *word, int64_t s
   if (!__all(found)) {
 #pragma unroll
     for (int i = NEAR; i < WINDOW; ++i) v[i] = read(word, i);
-    for (;;) {
+    for (int looks = 0;; ++looks) {
       look(WINDOW);
       if (__all(found)) break;
+      if (looks == MOST_LOOKS) {
+        h = __uint_as_float(0x7fc00000u);
+        break;
+      }
       if (TEAMS > 1 && team + 1 < TEAMS && __all(found || open)) {  // nothing more to read: the next team's state
-        while (!signal(team + 1)) {
+        while (!signal(team + 1)) {  // which is there at the latest when that team has looked MOST_LOOKS times
           if (team > 0 && signal(0)) return 0.f;
           __builtin_amdgcn_s_sleep(1);
         }
