@@ -173,12 +173,11 @@ def _pack(t, device):
     return _RECORDS[n].pack(t.data_ptr() or 16, code, n, *shape, *t.stride())
 
 
-# the current stream's handle without the Python object around it (2 us less a call), where torch has it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _current_stream(device):
-    return _raw_stream(device.index) if _raw_stream is not None else _stream(device)
+# the current stream's handle and the current device without the Python objects around them (2 us less
+# a call), where torch has them
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _empty(like, shape=None, dtype=None):
@@ -378,63 +377,70 @@ def gdp_group_norm_backward_workspace_bytes(T, G, V):
     return int(LIB.gdp_group_norm_backward_workspace_bytes(T, G, V))
 
 
-def _call(device, entry, *args, workspace=(), stream=None):
-    """Calls a C entry point with its workspace and the stream to launch on (by default the current one
-    of `device`, which is made the current device for the call)."""
-    if device.type != "cuda":
+def _call(device, stream, entry, *args):
+    """Calls a C entry point on the stream to launch on (None: the current one of `device`), with
+    `device` as the current device.  The tensors were checked by _pack to be on `device`."""
+    index = device.index
+    if index is None:
         raise ValueError(f"expected tensors on a GPU, got {device}")
-    if workspace is None:
-        workspace = (None, 0)
-    elif len(workspace):
-        workspace = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    if device.index == torch.cuda.current_device():
-        _check(entry(*args, *workspace, _current_stream(device) if stream is None else stream))
+    if index == _current_device():
+        rc = entry(*args, _raw_stream(index) if stream is None else stream)
     else:
         with torch.cuda.device(device):
-            _check(entry(*args, *workspace, _current_stream(device) if stream is None else stream))
+            rc = entry(*args, _raw_stream(index) if stream is None else stream)
+    if rc:
+        _check(rc)
+
+
+def _workspace_args(workspace, device):
+    if workspace is None:
+        return None, 0
+    if workspace.device != device:
+        raise ValueError(f"expected a workspace on {device}, got one on {workspace.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def gdp_gated_scan(x, g_log, cu_seqlens, complement_input, initial_state, output_final_state, state_cache,
                    state_indices, return_checkpoints, o, final_state, checkpoints, workspace, stream=None):
     """Direct call of the C entry point (caller-allocated outputs and workspace)."""
     dev = x.device
-    _call(dev, LIB.gdp_gated_scan, _pack(x, dev), _pack(g_log, dev), _pack(cu_seqlens, dev),
+    _call(dev, stream, LIB.gdp_gated_scan, _pack(x, dev), _pack(g_log, dev), _pack(cu_seqlens, dev),
           int(bool(complement_input)), _pack(initial_state, dev), int(bool(output_final_state)),
           _pack(state_cache, dev), _pack(state_indices, dev), int(bool(return_checkpoints)), _pack(o, dev),
-          _pack(final_state, dev), _pack(checkpoints, dev), workspace=workspace, stream=stream)
+          _pack(final_state, dev), _pack(checkpoints, dev), *_workspace_args(workspace, dev))
 
 
 def gdp_gated_scan_decode(x, g_log, complement_input, state_cache, state_indices, o, stream=None):
     """Direct call of the C entry point; o is caller-allocated, state_cache is updated in place."""
     dev = x.device
-    _call(dev, LIB.gdp_gated_scan_decode, _pack(x, dev), _pack(g_log, dev), int(bool(complement_input)),
-          _pack(state_cache, dev), _pack(state_indices, dev), _pack(o, dev), stream=stream)
+    _call(dev, stream, LIB.gdp_gated_scan_decode, _pack(x, dev), _pack(g_log, dev), int(bool(complement_input)),
+          _pack(state_cache, dev), _pack(state_indices, dev), _pack(o, dev))
 
 
 def gdp_gated_scan_backward(x, g_log, cu_seqlens, complement_input, initial_state, checkpoints, d_o, d_final_state,
                             dx, dg_log, d_initial_state, workspace, stream=None):
     """Direct call of the C entry point (caller-allocated gradients and workspace)."""
     dev = x.device
-    _call(dev, LIB.gdp_gated_scan_backward, _pack(x, dev), _pack(g_log, dev), _pack(cu_seqlens, dev),
+    _call(dev, stream, LIB.gdp_gated_scan_backward, _pack(x, dev), _pack(g_log, dev), _pack(cu_seqlens, dev),
           int(bool(complement_input)), _pack(initial_state, dev), _pack(checkpoints, dev), _pack(d_o, dev),
           _pack(d_final_state, dev), _pack(dx, dev), _pack(dg_log, dev), _pack(d_initial_state, dev),
-          workspace=workspace, stream=stream)
+          *_workspace_args(workspace, dev))
 
 
 def gdp_group_norm(x, weight, bias, gate, activation, subtract_mean, eps, y, stream=None):
     """Direct call of the C entry point; `activation` is a key of ACTIVATIONS, y is caller-allocated."""
     dev = x.device
-    _call(dev, LIB.gdp_group_norm, _pack(x, dev), _pack(weight, dev), _pack(bias, dev), _pack(gate, dev),
-          _activation(activation), int(bool(subtract_mean)), float(eps), _pack(y, dev), stream=stream)
+    _call(dev, stream, LIB.gdp_group_norm, _pack(x, dev), _pack(weight, dev), _pack(bias, dev), _pack(gate, dev),
+          _activation(activation), int(bool(subtract_mean)), float(eps), _pack(y, dev))
 
 
 def gdp_group_norm_backward(x, weight, bias, gate, activation, subtract_mean, eps, d_y, dx, dweight, dbias, dgate,
                             workspace, stream=None):
     """Direct call of the C entry point (caller-allocated gradients and workspace)."""
     dev = x.device
-    _call(dev, LIB.gdp_group_norm_backward, _pack(x, dev), _pack(weight, dev), _pack(bias, dev), _pack(gate, dev),
+    _call(dev, stream, LIB.gdp_group_norm_backward, _pack(x, dev), _pack(weight, dev), _pack(bias, dev), _pack(gate, dev),
           _activation(activation), int(bool(subtract_mean)), float(eps), _pack(d_y, dev), _pack(dx, dev),
-          _pack(dweight, dev), _pack(dbias, dev), _pack(dgate, dev), workspace=workspace, stream=stream)
+          _pack(dweight, dev), _pack(dbias, dev), _pack(dgate, dev), *_workspace_args(workspace, dev))
 
 
 def _activation(name):

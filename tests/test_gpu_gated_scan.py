@@ -173,6 +173,9 @@ def test_operands_elsewhere_are_refused(gdp):
         gdp.gated_scan(x, g, torch.tensor([0, 10], dtype=torch.int32))
     with pytest.raises(ValueError, match="expected a tensor on cuda"):
         gdp.gated_scan_decode(x, g, torch.zeros(10, 8, device="cuda"), torch.zeros(10, dtype=torch.int32))
+    with pytest.raises(ValueError, match="expected a workspace on cuda"):
+        gdp.gdp_gated_scan(x, g, torch.tensor([0, 10], dtype=torch.int32, device="cuda"), False, None, False, None, None,
+                           False, torch.empty_like(x), None, None, torch.empty(4096, dtype=torch.uint8))
     with pytest.raises(ValueError, match="unsupported dtype"):
         gdp.gated_scan(x.double(), g, torch.tensor([0, 10], dtype=torch.int32, device="cuda"))
     with pytest.raises(gdp.GdpError, match="x and o must share one dtype"):
