@@ -302,3 +302,39 @@ def test_prefill_then_norm_and_back(gdp):
     yd = gdp.group_norm(od, w.cuda(), gate=z[:2].cuda(), activation="silu", subtract_mean=False)
     wd = layers.norm(od.cpu(), w, None, z[:2], "silu", False)
     close(yd, wd["y"], wd["y_bound"], "y", BF16)
+
+
+def test_captured_layer_step(gdp):
+    """The allocating front ends of a whole layer step (scan, norm, both gradients) captured into a graph; each
+    replay, with new inputs and eager work in between, gives the eager step's bits."""
+    H, V = 3, 64
+    lens, D = [190, 0, 70], H * V
+    T = sum(lens)
+    cu = torch.tensor([0, 190, 190, 260], dtype=torch.int32, device="cuda")
+    gen = torch.Generator().manual_seed(18)
+    x, z, dy = (torch.randn(T, D, generator=gen).to(BF16).cuda() for _ in range(3))
+    g = -torch.rand(T, D, generator=gen).cuda()
+    w = (1 + 0.2 * torch.randn(V, generator=gen)).cuda()
+
+    def step():
+        heads = lambda t: t.view(T, H, V)  # noqa: E731
+        o, fs, cp = gdp.gated_scan(x, g, cu, output_final_state=True, return_checkpoints=True)
+        form = dict(weight=w, gate=heads(z), activation="silu", subtract_mean=False)
+        y = gdp.group_norm(heads(o), **form)
+        d = gdp.group_norm_backward(heads(o), heads(dy), **form)
+        ds = gdp.gated_scan_backward(x, g, cu, d["dx"].view(T, D), checkpoints=cp, grads_like_inputs=True)
+        return [y, fs, d["dgate"], d["dweight"], ds["dx"], ds["dg_log"]]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for _ in range(4):
+        x.copy_(torch.randn(T, D, generator=gen))
+        dy.copy_(torch.randn(T, D, generator=gen))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held]
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)

@@ -131,8 +131,17 @@ def test_scan_overlaps(b):
 
 
 def test_scan_workspace(b):
-    # 200 rows of 96 channels need no hand-over words in a build that takes them in one launch; the backward
-    # call needs room for the states when it gets no checkpoints
+    # more than 128 rows hand their states on through words: a counter and 8 bytes per tile and channel
+    need = b.gdp_gated_scan_workspace_bytes(200, 3, 96)
+    assert need >= 256 + 2 * 96 * 8
+    a = scan_args(b)
+    a["wsb"] = need - 1
+    refused(b, scan, a, b.GDP_EWORKSPACE, "needed")
+    a = scan_args(b)
+    a["ws"] = a["o"].data
+    refused(b, scan, a, b.GDP_EALIAS, "overlaps workspace")
+    assert b.gdp_gated_scan_workspace_bytes(128, 3, 96) == 0
+    # the gradients without checkpoints also form the states again
     need = b.gdp_gated_scan_backward_workspace_bytes(200, 3, 96)
     assert need >= 4 * 96 * 4
     a = scan_args(b)
@@ -143,9 +152,18 @@ def test_scan_workspace(b):
     refused(b, backward, a, b.GDP_EWORKSPACE, "aligned")
     a["ws"] = None
     refused(b, backward, a, b.GDP_EWORKSPACE, "needed")
-    for bad in ((-1, 1, 8), (1, -1, 8), (1, 1, 0)):
+    for bad in ((-1, 1, 8), (1, -1, 8), (1, 1, 0), (1 << 40, 1, 8), (1, 1, 1 << 24), (1 << 34, 1, 4096)):
         assert b.gdp_gated_scan_workspace_bytes(*bad) == 0
         assert b.gdp_gated_scan_backward_workspace_bytes(*bad) == 0
+
+
+def test_scan_sizes_past_the_launch(b):
+    """Sizes whose grid does not fit 32 bits are refused, with or without room for them."""
+    a = change(b, scan_args(b, T=1 << 20, N=3, D=96), s0=None, cache=None, slots=None, fs=None, cp=None)
+    a["ofs"], a["rcp"] = 0, 0
+    for t in (a["x"], a["g"], a["o"]):
+        t.shape[0], t.shape[1], t.stride[0] = 1 << 34, 4096, 0 if t is not a["o"] else 4096
+    refused(b, scan, a, b.GDP_EUNSUPPORTED, "launch limits")
 
 
 def test_decode_refusals(b):
