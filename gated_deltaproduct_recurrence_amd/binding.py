@@ -154,14 +154,14 @@ def _stream(device):
 _RECORDS = [struct.Struct("@Pii" + f"{n}q{8 * (4 - n)}x" * 2) for n in range(5)]
 
 
-def _pack(t, device):
+def _pack(t, index):
     """The gdp_tensor record of a torch tensor as bytes (None -> absent): a fifth of the time of
-    as_gdp_tensor, which counts in a call of a few microseconds.  Refuses a tensor elsewhere than on
-    `device`."""
+    as_gdp_tensor, which counts in a call of a few microseconds.  Refuses a tensor that is not on the
+    GPU `index` (-1: the host; _call refuses that)."""
     if t is None:
         return None
-    if t.device != device:
-        raise ValueError(f"expected a tensor on {device}, got one on {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"expected a tensor on cuda:{index}, got one on {t.device}")
     code = _DT.get(t.dtype)
     if code is None:
         raise ValueError(f"unsupported dtype {t.dtype}")
@@ -183,7 +183,7 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 def _empty(like, shape=None, dtype=None):
     """A new contiguous tensor on `like`'s device, by default of its shape and dtype."""
     if shape is None:
-        return torch.empty_like(like, memory_format=torch.contiguous_format)
+        return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
     return like.new_empty(shape, dtype=dtype)
 
 
@@ -377,33 +377,32 @@ def gdp_group_norm_backward_workspace_bytes(T, G, V):
     return int(LIB.gdp_group_norm_backward_workspace_bytes(T, G, V))
 
 
-def _call(device, stream, entry, *args):
-    """Calls a C entry point on the stream to launch on (None: the current one of `device`), with
-    `device` as the current device.  The tensors were checked by _pack to be on `device`."""
-    index = device.index
-    if index is None:
-        raise ValueError(f"expected tensors on a GPU, got {device}")
+def _call(index, stream, entry, *args):
+    """Calls a C entry point on the stream to launch on (None: the current one of the GPU `index`), with
+    that GPU as the current device.  The tensors were checked by _pack to be there."""
+    if index < 0:
+        raise ValueError("expected tensors on a GPU, got tensors on the host")
     if index == _current_device():
         rc = entry(*args, _raw_stream(index) if stream is None else stream)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = entry(*args, _raw_stream(index) if stream is None else stream)
     if rc:
         _check(rc)
 
 
-def _workspace_args(workspace, device):
+def _workspace_args(workspace, index):
     if workspace is None:
         return None, 0
-    if workspace.device != device:
-        raise ValueError(f"expected a workspace on {device}, got one on {workspace.device}")
+    if workspace.get_device() != index:
+        raise ValueError(f"expected a workspace on cuda:{index}, got one on {workspace.device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def gdp_gated_scan(x, g_log, cu_seqlens, complement_input, initial_state, output_final_state, state_cache,
                    state_indices, return_checkpoints, o, final_state, checkpoints, workspace, stream=None):
     """Direct call of the C entry point (caller-allocated outputs and workspace)."""
-    dev = x.device
+    dev = x.get_device()
     _call(dev, stream, LIB.gdp_gated_scan, _pack(x, dev), _pack(g_log, dev), _pack(cu_seqlens, dev),
           int(bool(complement_input)), _pack(initial_state, dev), int(bool(output_final_state)),
           _pack(state_cache, dev), _pack(state_indices, dev), int(bool(return_checkpoints)), _pack(o, dev),
@@ -412,7 +411,7 @@ def gdp_gated_scan(x, g_log, cu_seqlens, complement_input, initial_state, output
 
 def gdp_gated_scan_decode(x, g_log, complement_input, state_cache, state_indices, o, stream=None):
     """Direct call of the C entry point; o is caller-allocated, state_cache is updated in place."""
-    dev = x.device
+    dev = x.get_device()
     _call(dev, stream, LIB.gdp_gated_scan_decode, _pack(x, dev), _pack(g_log, dev), int(bool(complement_input)),
           _pack(state_cache, dev), _pack(state_indices, dev), _pack(o, dev))
 
@@ -420,7 +419,7 @@ def gdp_gated_scan_decode(x, g_log, complement_input, state_cache, state_indices
 def gdp_gated_scan_backward(x, g_log, cu_seqlens, complement_input, initial_state, checkpoints, d_o, d_final_state,
                             dx, dg_log, d_initial_state, workspace, stream=None):
     """Direct call of the C entry point (caller-allocated gradients and workspace)."""
-    dev = x.device
+    dev = x.get_device()
     _call(dev, stream, LIB.gdp_gated_scan_backward, _pack(x, dev), _pack(g_log, dev), _pack(cu_seqlens, dev),
           int(bool(complement_input)), _pack(initial_state, dev), _pack(checkpoints, dev), _pack(d_o, dev),
           _pack(d_final_state, dev), _pack(dx, dev), _pack(dg_log, dev), _pack(d_initial_state, dev),
@@ -429,7 +428,7 @@ def gdp_gated_scan_backward(x, g_log, cu_seqlens, complement_input, initial_stat
 
 def gdp_group_norm(x, weight, bias, gate, activation, subtract_mean, eps, y, stream=None):
     """Direct call of the C entry point; `activation` is a key of ACTIVATIONS, y is caller-allocated."""
-    dev = x.device
+    dev = x.get_device()
     _call(dev, stream, LIB.gdp_group_norm, _pack(x, dev), _pack(weight, dev), _pack(bias, dev), _pack(gate, dev),
           _activation(activation), int(bool(subtract_mean)), float(eps), _pack(y, dev))
 
@@ -437,10 +436,11 @@ def gdp_group_norm(x, weight, bias, gate, activation, subtract_mean, eps, y, str
 def gdp_group_norm_backward(x, weight, bias, gate, activation, subtract_mean, eps, d_y, dx, dweight, dbias, dgate,
                             workspace, stream=None):
     """Direct call of the C entry point (caller-allocated gradients and workspace)."""
-    dev = x.device
-    _call(dev, stream, LIB.gdp_group_norm_backward, _pack(x, dev), _pack(weight, dev), _pack(bias, dev), _pack(gate, dev),
-          _activation(activation), int(bool(subtract_mean)), float(eps), _pack(d_y, dev), _pack(dx, dev),
-          _pack(dweight, dev), _pack(dbias, dev), _pack(dgate, dev), *_workspace_args(workspace, dev))
+    dev = x.get_device()
+    _call(dev, stream, LIB.gdp_group_norm_backward, _pack(x, dev), _pack(weight, dev), _pack(bias, dev),
+          _pack(gate, dev), _activation(activation), int(bool(subtract_mean)), float(eps), _pack(d_y, dev),
+          _pack(dx, dev), _pack(dweight, dev), _pack(dbias, dev), _pack(dgate, dev),
+          *_workspace_args(workspace, dev))
 
 
 def _activation(name):
@@ -580,9 +580,9 @@ def gated_scan_backward(x, g_log, cu_seqlens, d_o, d_final_state=None, initial_s
     state).  Without the forward call's `checkpoints` the states are formed again first."""
     T, D = x.shape
     N = cu_seqlens.shape[0] - 1
-    dx = _empty(x, (T, D), x.dtype if grads_like_inputs else torch.float32)
-    dg = _empty(x, (T, D), g_log.dtype if grads_like_inputs else torch.float32)
-    ds0 = _empty(x, (N, D), torch.float32) if initial_state is not None else None
+    dx = _empty(x, dtype=None if grads_like_inputs else torch.float32)
+    dg = _empty(g_log, dtype=None if grads_like_inputs else torch.float32)
+    ds0 = _empty(initial_state) if initial_state is not None else None
     gdp_gated_scan_backward(x, g_log, cu_seqlens, complement_input, initial_state, checkpoints, d_o, d_final_state,
                             dx, dg, ds0, _workspace(x, gdp_gated_scan_backward_workspace_bytes(T, N, D)))
     return {"dx": dx, "dg_log": dg, "d_initial_state": ds0}
@@ -604,7 +604,7 @@ def group_norm_backward(x, d_y, weight=None, bias=None, gate=None, activation=No
     T, G, V = x.shape
     dx = _empty(x)
     dz = _empty(x) if gate is not None else None
-    dw, db = (None if p is None else _empty(x, p.shape, torch.float32) for p in (weight, bias))
+    dw, db = (None if p is None else _empty(p, dtype=torch.float32) for p in (weight, bias))
     gdp_group_norm_backward(x, weight, bias, gate, activation, subtract_mean, eps, d_y, dx, dw, db, dz,
                             _workspace(x, gdp_group_norm_backward_workspace_bytes(T, G, V)))
     return {"dx": dx, "dweight": dw, "dbias": db, "dgate": dz}

@@ -139,7 +139,8 @@ def decode(x, g, cache, slots, complement=False):
 def _activation(name, v):
     """act(v), act'(v) and bounds of their float32 evaluations.  exp(-v) is off by (2 |v| + 4) U relative,
     the sum and the quotient add 3 U, so s by (2 |v| + 8) U absolute at most (s (1 - s) <= 1/4 scales the
-    exponential's part), and by 2^-126 more: exp(-v) past 2^126 makes s a subnormal or, past 2^128, 0; s v and s (1 + v (1 - s)) carry that on with the factors they multiply it by."""
+    exponential's part), and by 2^-126 more: exp(-v) past 2^126 makes s a subnormal or, past 2^128, 0.
+    s v and s (1 + v (1 - s)) carry that on with the factors they multiply it by."""
     if name in (None, "none"):
         return v, torch.ones_like(v), torch.zeros_like(v), torch.zeros_like(v)
     s = torch.sigmoid(v)
