@@ -24,13 +24,19 @@
 // composes them from that one forward.  That is the sequential fold, whichever tile
 // the fold starts from, so the result does not depend on timing.  While none has
 // A = 0 only the farthest is read again: the known states reach it first.
+// With few channel blocks (GROUPS) the known states come that way through groups of
+// 16 tiles instead, each with a word of its own: a tile reads the pairs of the tiles
+// before it in its group, other lanes the state entering the group, and the group's
+// last tile publishes the group's pair and then its state.  There the tiles' words
+// are pairs only, so that the order of the sums is fixed here too.
 // The words are written and read with relaxed agent-scope atomics (8 bytes, so a
 // pair is whole), which go past the XCDs' own caches; all-ones bits (two NaNs that
 // no published pair has) mean not yet written, and a fill kernel sets them before.
 // Tiles are handed out by an atomic counter, rows ascending, so a workgroup waits
 // only for tiles whose workgroups are running, and those publish their pairs before
-// they wait themselves: the first of the waiting tiles finds its predecessor's word
-// at A = 0, so every wait ends.  (It is bounded all the same, at 2^21 looks, seconds:
+// they wait themselves; with all pairs there, a group's pair waits for nothing else,
+// and the first of the waiting tiles (or groups) finds its predecessor's word at
+// A = 0: every wait ends.  (It is bounded all the same, at 2^21 looks, seconds:
 // when calls on two streams share a workspace against the contract, tickets can be
 // lost, and the rows behind then become NaN instead of the GPU hanging.)
 //
@@ -44,8 +50,8 @@
 //   Tile: 128 rows x 128 channels (16 rows and a pair of channels per lane).  With 64
 // rows the second shape took 1045 us instead of 743 (twice the words, twice the hops);
 // 4 channels per lane and 8 rows 838; one channel per lane 1012.
-//   Window: 8 tiles; 16 cost 3% on the wide shapes (registers, words read), 4 gained 1%
-// there and cost 25% at 1024 channels.
+//   Window: 8 tiles; 16 cost 3% (registers, words read), 4 gained 1% on the wide shapes
+// and cost 25% at 1024 channels.
 //   Three workgroups per CU (80 registers) spill: 1650 us.  Workgroups that stay and
 // draw their next ticket ahead: 853 us.
 
@@ -60,8 +66,8 @@ namespace {
 
 constexpr int WAVES = 8, THREADS = 64 * WAVES;
 constexpr int VEC = 2, NCH = 64 * VEC;  // channels per lane and per workgroup
-constexpr int MOST_TEAMS = THREADS / NCH;  // lanes per channel that can look at the tiles before
-template <int TEAMS> constexpr int WINDOW_OF = TEAMS > 1 ? 12 : 8;  // tiles that each of them looks at
+constexpr int GROUP = 16;               // tiles per group
+constexpr int WINDOW = 8;               // words before its own that a lane looks at
 constexpr uint64_t NOT_WRITTEN = ~0ull;
 constexpr int MOST_LOOKS = 1 << 21;
 
@@ -130,8 +136,8 @@ __device__ __forceinline__ uint64_t make_word(float A, float B) {
 template <int R> struct Shared {
   static constexpr int ROWS = WAVES * R;
   float A[WAVES][NCH], B[WAVES][NCH];
-  float found[MOST_TEAMS][NCH];   // a team's state for the one before it ...
-  int there[MOST_TEAMS][VEC];     // ... and whether it is there, of each half of the channels
+  float state[NCH];                  // the state entering the tile's group ...
+  int there[VEC];                    // ... and whether it is there, of each half of the channels
   int start_id[ROWS], end_id[ROWS];  // sequence that starts / ends at a row of the tile, or -1
   int ticket;
 };
@@ -171,41 +177,35 @@ template <int R> __device__ __forceinline__ uint32_t marked(const int *ids, int 
   return (uint32_t)__ballot(lane < R && ids[w * R + (lane & (R - 1))] >= 0);
 }
 
-// The state entering this tile, of one channel, from the words of the `count` tiles
-// before it: `word` is the nearest one's, the others lie `step` words apart.  Team
-// `team` of TEAMS looks at the words team * WINDOW and on; a team that finds all of
-// its words but none with A = 0 waits (in LDS) for the state that the next team finds,
-// which the known states reach first.  Only team 0's value is used; the others stop
-// when it has one.
-template <int TEAMS, typename S>
-__device__ __forceinline__ float entering(S &sh, const uint64_t *word, int64_t step, int64_t count, bool live, int team,
-                                          int c) {
-  constexpr int WINDOW = WINDOW_OF<TEAMS>;
-  const int half = c >> 6;
-  if (TEAMS > 1) {
-    count -= team * WINDOW;
-    word += team * WINDOW * step;
-  }
+__device__ __forceinline__ uint64_t read_word(const uint64_t *w) {
+  return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void write_word(uint64_t *w, float A, float B) {
+  __hip_atomic_store(w, make_word(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float part_a(uint64_t word) { return __uint_as_float((uint32_t)(word >> 32)); }
+__device__ __forceinline__ float part_b(uint64_t word) { return __uint_as_float((uint32_t)word); }
+
+// The state that the `count` words before hand on, of one channel: `word` is the
+// nearest one, the others lie `step` words apart.
+__device__ __forceinline__ float entering(const uint64_t *word, int64_t step, int count, bool live) {
   uint64_t v[WINDOW];
-  auto read = [&](const uint64_t *w, int i) {  // tiles before the first count as a state of 0
-    return live && i < count ? __hip_atomic_load(w + i * step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+  auto read = [&](const uint64_t *w, int i) {  // before the first there is a state of 0
+    return live && i < count ? read_word(w + i * step) : 0;
   };
-  auto first_part = [](uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); };
-  auto signal = [&](int t) { return __hip_atomic_load(&sh.there[t][half], __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP); };
-  bool found, open;  // a word with A = 0 and all before it are there; all are there, none has A = 0
+  bool found;  // a word with A = 0 and all before it are there
   auto look = [&](int n) {
-    open = true;
+    bool open = true;
     found = false;
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const bool there = v[i] != NOT_WRITTEN;
-      found = found || (open && there && first_part(v[i]) == 0.f);
+      found = found || (open && there && part_a(v[i]) == 0.f);
       open = open && there && !found;
     }
   };
-  // a single team looks at the nearer half first: mostly it is enough, and the words are
-  // a good part of what is read
-  constexpr int NEAR = TEAMS > 1 ? WINDOW : WINDOW / 2;
+  // the nearer half first: mostly it is enough
+  constexpr int NEAR = WINDOW / 2;
 #pragma unroll
   for (int i = 0; i < WINDOW; ++i) v[i] = i < NEAR ? read(word, i) : NOT_WRITTEN;
   float h = 0.f;
@@ -220,15 +220,6 @@ __device__ __forceinline__ float entering(S &sh, const uint64_t *word, int64_t s
         h = __uint_as_float(0x7fc00000u);
         break;
       }
-      if (TEAMS > 1 && team + 1 < TEAMS && __all(found || open)) {  // nothing more to read: the next team's state
-        while (!signal(team + 1)) {  // which is there at the latest when that team has looked MOST_LOOKS times
-          if (team > 0 && signal(0)) return 0.f;
-          __builtin_amdgcn_s_sleep(1);
-        }
-        h = sh.found[team + 1][c];
-        break;
-      }
-      if (TEAMS > 1 && team > 0 && signal(0)) return 0.f;
       __builtin_amdgcn_s_sleep(1);
       asm volatile("" : "+v"(word));  // or every word's address is kept in registers over the loop
 #pragma unroll
@@ -238,50 +229,102 @@ __device__ __forceinline__ float entering(S &sh, const uint64_t *word, int64_t s
   }
 #pragma unroll
   for (int i = WINDOW - 1; i >= 0; --i)
-    if (v[i] != NOT_WRITTEN) h = apply(first_part(v[i]), h, __uint_as_float((uint32_t)v[i]));
-  if (TEAMS > 1) {
-    sh.found[team][c] = h;
-    __hip_atomic_store(&sh.there[team][half], 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
-  }
+    if (v[i] != NOT_WRITTEN) h = apply(part_a(v[i]), h, part_b(v[i]));
   return h;
+}
+
+// The map of the `count` tiles before this one in its group, of one channel.
+struct Map { float A, B; };
+__device__ __forceinline__ Map group_so_far(const uint64_t *word, int64_t step, int count, bool live) {
+  uint64_t v[GROUP - 1];
+#pragma unroll
+  for (int i = 0; i < GROUP - 1; ++i) v[i] = NOT_WRITTEN;
+  for (int looks = 0;; ++looks) {
+#pragma unroll
+    for (int i = 0; i < GROUP - 1; ++i)
+      if (i < count && v[i] == NOT_WRITTEN) v[i] = live ? read_word(word + i * step) : 0;
+    bool open = true, there = true;  // all that matter: up to the nearest with A = 0
+#pragma unroll
+    for (int i = 0; i < GROUP - 1; ++i) {
+      if (i < count) {
+        there = there && (!open || v[i] != NOT_WRITTEN);
+        open = open && !(v[i] != NOT_WRITTEN && part_a(v[i]) == 0.f);
+      }
+    }
+    if (__all(there)) break;
+    if (looks == MOST_LOOKS) return Map{0.f, __uint_as_float(0x7fc00000u)};
+    __builtin_amdgcn_s_sleep(1);
+    asm volatile("" : "+v"(word));
+  }
+  Map m{1.f, 0.f};
+#pragma unroll
+  for (int i = GROUP - 2; i >= 0; --i)
+    if (i < count && v[i] != NOT_WRITTEN) {
+      m.B = apply(part_a(v[i]), m.B, part_b(v[i]));
+      m.A = part_a(v[i]) == 0.f ? 0.f : m.A * part_a(v[i]);
+    }
+  return m;
 }
 
 // The waves' maps in sh.A, sh.B: composes the tile's, publishes it, and leaves in
 // sh.A the state entering each wave's rows (of the channels first + 0 .. NCH - 1).
 // REVERSE: from the last tile and wave to the first.
-template <int TEAMS, bool REVERSE, typename S>
+template <bool GROUPS, bool REVERSE, typename S>
 __device__ __forceinline__ void hand_over(S &sh, const ScanArgs &a, int tile, int tiles, bool needs, int first, int tid) {
-  const int c = tid % NCH, team = tid / NCH, step = REVERSE ? 1 : -1;  // to the tile before, in this direction
+  const int c = tid % NCH, role = tid / NCH;
+  if (role > (GROUPS ? 1 : 0)) return;
+  const int64_t step = REVERSE ? a.D : -a.D;  // to the tile before, in this direction
   const int before = REVERSE ? tiles - 1 - tile : tile;
-  const bool live = first + c < a.D, publish = live && team == 0 && before + 1 < tiles;
-  uint64_t *words = at((uint64_t *)((char *)a.ws + 256) + (int64_t)tile * a.D, first + c);
-  float A = 1.f, B = 0.f, carry = 0.f;
-  if (team < (needs ? TEAMS : 1) && tiles > 1) {
-    if (team == 0) {
-#pragma unroll
-      for (int v = 0; v < WAVES; ++v) {
-        const int w = REVERSE ? WAVES - 1 - v : v;
-        B = apply(sh.A[w][c], B, sh.B[w][c]);
-        A *= sh.A[w][c];
-      }
-      if (!needs) A = 0.f;
+  const int group = before / GROUP, place = before % GROUP;
+  const bool live = first + c < a.D;
+  uint64_t *words = (uint64_t *)((char *)a.ws + 256);
+  uint64_t *mine = at(words + (int64_t)tile * a.D, first + c);
+  uint64_t *groups = at(words + ((int64_t)tiles + group) * a.D, first + c);
+  if (GROUPS && role == 1) {  // the state entering the group
+    if (needs && tiles > 1) {
+      sh.state[c] = entering(groups - a.D, -a.D, group, live);
+      __hip_atomic_store(&sh.there[c >> 6], 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
     }
-    if (publish) __hip_atomic_store(words, make_word(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (needs) {
-      carry = entering<TEAMS>(sh, words + step * a.D, step * a.D, before, live, team, c);
-      if (publish && A != 0.f)
-        __hip_atomic_store(words, make_word(0.f, fmaf(A, carry, B)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
+    return;
   }
-  if (team == 0) {
-    float h = carry;
+  float carry = 0.f;
+  if (tiles > 1) {
+    float A = 1.f, B = 0.f;
 #pragma unroll
     for (int v = 0; v < WAVES; ++v) {
       const int w = REVERSE ? WAVES - 1 - v : v;
-      const float next = apply(sh.A[w][c], h, sh.B[w][c]);
-      sh.A[w][c] = h;
-      h = next;
+      B = apply(sh.A[w][c], B, sh.B[w][c]);
+      A *= sh.A[w][c];
     }
+    if (!needs) A = 0.f;
+    if (live && before + 1 < tiles) write_word(mine, A, B);
+    if (!GROUPS) {
+      if (needs) {
+        carry = entering(mine + step, step, before, live);
+        if (live && before + 1 < tiles && A != 0.f) write_word(mine, 0.f, fmaf(A, carry, B));
+      }
+    } else {
+      const bool last = place == GROUP - 1 && before + 1 < tiles && live;
+      Map m{0.f, 0.f};
+      if (needs) m = group_so_far(mine + step, step, place, live);
+      const float GA = A == 0.f ? 0.f : A * m.A, GB = apply(A, m.B, B);
+      if (last) write_word(groups, GA, GB);
+      if (needs) {
+        while (!__hip_atomic_load(&sh.there[c >> 6], __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP))
+          __builtin_amdgcn_s_sleep(1);
+        const float state = sh.state[c];
+        carry = apply(m.A, state, m.B);
+        if (last && GA != 0.f) write_word(groups, 0.f, fmaf(GA, state, GB));
+      }
+    }
+  }
+  float h = carry;
+#pragma unroll
+  for (int v = 0; v < WAVES; ++v) {
+    const int w = REVERSE ? WAVES - 1 - v : v;
+    const float next = apply(sh.A[w][c], h, sh.B[w][c]);
+    sh.A[w][c] = h;
+    h = next;
   }
 }
 
@@ -289,7 +332,7 @@ __device__ __forceinline__ void hand_over(S &sh, const ScanArgs &a, int tile, in
 // index when nothing is handed on.  Clears the row marks.
 template <typename S> __device__ __forceinline__ int take_ticket(S &sh, const ScanArgs &a, bool hand_on, int tid) {
   if (tid < S::ROWS) sh.start_id[tid] = sh.end_id[tid] = -1;
-  if (tid < MOST_TEAMS * VEC) sh.there[tid / VEC][tid % VEC] = 0;
+  if (tid < VEC) sh.there[tid] = 0;
   if (!hand_on) {
     __syncthreads();
     return (int)blockIdx.x;
@@ -317,7 +360,7 @@ __device__ __forceinline__ void empty_sequences(const ScanArgs &a, int64_t job, 
   }
 }
 
-template <typename XT, typename GT, int R, bool COMPL, int TEAMS>
+template <typename XT, typename GT, int R, bool COMPL, bool GROUPS>
 __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int tiles, int blocks) {
   using S = Shared<R>;
   __shared__ S sh;
@@ -386,7 +429,7 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int ti
   }
   __syncthreads();
 
-  hand_over<TEAMS, false>(sh, a, tile, tiles, tile > 0 && sh.start_id[0] < 0 && r0 >= c0 && r0 < cN, first, tid);
+  hand_over<GROUPS, false>(sh, a, tile, tiles, tile > 0 && sh.start_id[0] < 0 && r0 >= c0 && r0 < cN, first, tid);
   __syncthreads();
 
   if (a.checkpoints && tid < NCH && first + tid < a.D) {
@@ -431,7 +474,7 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int ti
 // factors of dg, d_o and (complement form) 1 - a of its rows, 116 registers for 8 rows
 // of a pair; at 80 registers, for three workgroups per CU, it spills (491 us instead
 // of 328 for a training step).
-template <typename XT, typename GT, bool COMPL, int TEAMS>
+template <typename XT, typename GT, bool COMPL, bool GROUPS>
 __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs a, int tiles, int blocks) {
   constexpr int R = SCAN_ROWS / WAVES;
   using S = Shared<R>;
@@ -571,7 +614,7 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs 
   __syncthreads();
 
   const int64_t rl = r0 + SCAN_ROWS - 1;  // the tile's last row
-  hand_over<TEAMS, true>(sh, a, tile, tiles, tile + 1 < tiles && sh.end_id[SCAN_ROWS - 1] < 0 && rl >= c0 && rl < cN,
+  hand_over<GROUPS, true>(sh, a, tile, tiles, tile + 1 < tiles && sh.end_id[SCAN_ROWS - 1] < 0 && rl >= c0 && rl < cN,
                          first, tid);
   __syncthreads();
 
@@ -671,16 +714,17 @@ Grid grid_of(const ScanArgs &a, int rows, bool empties) {
   return g;
 }
 
-// Channel blocks up to which four lanes per channel look back, over 48 tiles.  The
+// Channel blocks up to which the states are handed on through groups of tiles.  The
 // workgroups that run at once then work on more tiles of each block, and how far the
 // known states come per look bounds the rate, not the memory: 131072 rows of 64, 256
-// and 512 channels take 86, 99 and 130 us with four lanes and 149, 167 and 177 with one
-// (98, 113 and 127 with windows of 8); 1024 channels 227 and 222.
+// and 512 channels take 41, 82 and 130 us through groups and 149, 167 and 177 without;
+// 1024 channels 227 and 221, and 131104 rows of 4096 channels 784 and 703.
 constexpr int NARROW = 4;
 
 hipError_t fill_words(const ScanArgs &a, const Grid &g, hipStream_t stream) {
   if (g.tiles <= 1) return hipSuccess;
-  const int64_t n = (256 + (int64_t)g.tiles * a.D * 8 + 15) / 16, want = (n + 255) / 256;
+  const int64_t words = g.tiles + (g.blocks <= NARROW ? g.tiles / GROUP : 0);
+  const int64_t n = (256 + words * a.D * 8 + 15) / 16, want = (n + 255) / 256;
   hipLaunchKernelGGL(gdp_scan_fill_kernel, dim3((unsigned)(want < 2048 ? want : 2048)), dim3(256), 0, stream,
                      (uint4 *)a.ws, n);
   return hipGetLastError();
@@ -692,10 +736,10 @@ template <typename XT, typename GT> hipError_t run_scan(ScanArgs a, hipStream_t 
   const Grid k = grid_of(a, WAVES * R, a.N > 0 && (a.final_state || a.cache));
   if (k.jobs == 0) return hipSuccess;
   if (hipError_t e = fill_words(a, k, stream)) return e;
-  auto *kernel = k.blocks <= NARROW ? (a.complement ? gdp_scan_kernel<XT, GT, R, true, MOST_TEAMS>
-                                                    : gdp_scan_kernel<XT, GT, R, false, MOST_TEAMS>)
-                                    : (a.complement ? gdp_scan_kernel<XT, GT, R, true, 1>
-                                                    : gdp_scan_kernel<XT, GT, R, false, 1>);
+  auto *kernel = k.blocks <= NARROW ? (a.complement ? gdp_scan_kernel<XT, GT, R, true, true>
+                                                    : gdp_scan_kernel<XT, GT, R, false, true>)
+                                    : (a.complement ? gdp_scan_kernel<XT, GT, R, true, false>
+                                                    : gdp_scan_kernel<XT, GT, R, false, false>);
   hipLaunchKernelGGL(kernel, dim3(k.jobs), dim3(THREADS), 0, stream, a, k.tiles, k.blocks);
   return hipGetLastError();
 }
@@ -705,10 +749,10 @@ template <typename XT, typename GT> hipError_t run_backward(ScanArgs a, hipStrea
   const Grid k = grid_of(a, SCAN_ROWS, a.N > 0 && a.ds0);
   if (k.jobs == 0) return hipSuccess;
   if (hipError_t e = fill_words(a, k, stream)) return e;
-  auto *kernel = k.blocks <= NARROW ? (a.complement ? gdp_scan_backward_kernel<XT, GT, true, MOST_TEAMS>
-                                                    : gdp_scan_backward_kernel<XT, GT, false, MOST_TEAMS>)
-                                    : (a.complement ? gdp_scan_backward_kernel<XT, GT, true, 1>
-                                                    : gdp_scan_backward_kernel<XT, GT, false, 1>);
+  auto *kernel = k.blocks <= NARROW ? (a.complement ? gdp_scan_backward_kernel<XT, GT, true, true>
+                                                    : gdp_scan_backward_kernel<XT, GT, false, true>)
+                                    : (a.complement ? gdp_scan_backward_kernel<XT, GT, true, false>
+                                                    : gdp_scan_backward_kernel<XT, GT, false, false>);
   hipLaunchKernelGGL(kernel, dim3(k.jobs), dim3(THREADS), 0, stream, a, k.tiles, k.blocks);
   return hipGetLastError();
 }
@@ -717,7 +761,7 @@ template <typename XT, typename GT> hipError_t run_backward(ScanArgs a, hipStrea
 
 size_t scan_state_bytes(int64_t T, int64_t D, int rows) {
   const int64_t tiles = (T + rows - 1) / rows;
-  return tiles <= 1 ? 0 : (256 + (size_t)tiles * D * 8 + 255) & ~(size_t)255;
+  return tiles <= 1 ? 0 : (256 + (size_t)(tiles + tiles / GROUP) * D * 8 + 255) & ~(size_t)255;
 }
 
 // The grids are 32-bit (one workgroup per 64 rows and 128 channels at most, and one

@@ -344,8 +344,8 @@ int gdp_chunk_gated_delta_product(const gdp_tensor *q, const gdp_tensor *k, cons
 #define GDP_SCAN_CHECKPOINT_ROWS 64
 
 /* Host-only.  Workspace bytes gdp_gated_scan needs for T rows, N sequences and D
- * channels: a ticket counter and, per 128 rows and channel, one 8-byte word through
- * which the workgroups of a long sequence hand their states on.  The call writes
+ * channels: a ticket counter and, per 128 rows and channel (and per 2048), one 8-byte
+ * word through which the workgroups of a long sequence hand their states on.  The call writes
  * it before use and leaves nothing in it that a later call reads.  Returns 0 for
  * invalid sizes and where none is needed (up to 128 rows). */
 size_t gdp_gated_scan_workspace_bytes(int64_t T, int64_t N, int64_t D);

@@ -278,10 +278,11 @@ def test_a_continued_sequence_is_the_whole_one(gdp):
     close(o, ref["o"], ref["o_bound"], ("o", BF16))
 
 
-def test_long_axis_few_channels(gdp):
-    """Thousands of blocks handed on in one channel block."""
-    lens = [9000, 300, 11000]
-    x, g, cu, s0 = make(lens, 4, F32, F32, seed=15, shift=6.0)
+@pytest.mark.parametrize("lens,first,behind", [([9000, 300, 11000], 0, 0), ([2048, 4096, 100, 1948, 1024], 0, 300),
+                                               ([5000, 0, 1, 3000], 2100, 0)])
+def test_long_axis_few_channels(gdp, lens, first, behind):
+    """Hundreds of blocks handed on through groups in one channel block; sequences that end with a group."""
+    x, g, cu, s0 = make(lens, 5, F32, F32, seed=15, shift=6.0, first=first, behind=behind)
     check_scan(gdp, x, g, cu, s0, False)
 
 
