@@ -6,9 +6,14 @@ the library is missing this module raises on import -- there is no fallback.
 """
 import ctypes
 import os
-import struct
 
 import torch
+
+try:
+    from ._records import records as _records  # (after torch, whose libraries it needs)
+except ImportError as e:
+    raise ImportError(f"the binding's extension is not built ({e}); run __graft_entry__.build() "
+                      "(gated_deltaproduct_recurrence_amd/build.py)") from e
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # GDP_LIBRARY names another build of the library (the host-sanitized check
@@ -91,7 +96,7 @@ def _load(path=LIB_PATH):
                                                ctypes.c_void_p]
     lib.gdp_debug_status.restype = ctypes.c_int
     lib.gdp_debug_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int32, ctypes.c_void_p]
-    # the recurrence's and the norm's tensors cross as packed gdp_tensor records (_pack)
+    # the recurrence's and the norm's tensors cross as addresses of gdp_tensor records (_records)
     P, i32, i64, size = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     for name in ("gdp_gated_scan_workspace_bytes", "gdp_gated_scan_backward_workspace_bytes",
                  "gdp_group_norm_backward_workspace_bytes"):
@@ -148,29 +153,6 @@ def _check(rc):
 
 def _stream(device):
     return torch.cuda.current_stream(device).cuda_stream
-
-
-# the layout of gdp_tensor, for each number of dims
-_RECORDS = [struct.Struct("@Pii" + f"{n}q{8 * (4 - n)}x" * 2) for n in range(5)]
-
-
-def _pack(t, index):
-    """The gdp_tensor record of a torch tensor as bytes (None -> absent): a fifth of the time of
-    as_gdp_tensor, which counts in a call of a few microseconds.  Refuses a tensor that is not on the
-    GPU `index` (-1: the host; _call refuses that)."""
-    if t is None:
-        return None
-    if t.get_device() != index:
-        raise ValueError(f"expected a tensor on cuda:{index}, got one on {t.device}")
-    code = _DT.get(t.dtype)
-    if code is None:
-        raise ValueError(f"unsupported dtype {t.dtype}")
-    shape = t.shape
-    n = len(shape)
-    if n > 4:
-        raise ValueError("at most 4 dims")
-    # an empty tensor is still "present": a non-null dummy address
-    return _RECORDS[n].pack(t.data_ptr() or 16, code, n, *shape, *t.stride())
 
 
 # the current stream's handle and the current device without the Python objects around them (2 us less
@@ -379,7 +361,7 @@ def gdp_group_norm_backward_workspace_bytes(T, G, V):
 
 def _call(index, stream, entry, *args):
     """Calls a C entry point on the stream to launch on (None: the current one of the GPU `index`), with
-    that GPU as the current device.  The tensors were checked by _pack to be there."""
+    that GPU as the current device.  The tensors were checked by _records to be there."""
     if index < 0:
         raise ValueError("expected tensors on a GPU, got tensors on the host")
     if index == _current_device():
@@ -403,44 +385,43 @@ def gdp_gated_scan(x, g_log, cu_seqlens, complement_input, initial_state, output
                    state_indices, return_checkpoints, o, final_state, checkpoints, workspace, stream=None):
     """Direct call of the C entry point (caller-allocated outputs and workspace)."""
     dev = x.get_device()
-    _call(dev, stream, LIB.gdp_gated_scan, _pack(x, dev), _pack(g_log, dev), _pack(cu_seqlens, dev),
-          int(bool(complement_input)), _pack(initial_state, dev), int(bool(output_final_state)),
-          _pack(state_cache, dev), _pack(state_indices, dev), int(bool(return_checkpoints)), _pack(o, dev),
-          _pack(final_state, dev), _pack(checkpoints, dev), *_workspace_args(workspace, dev))
+    r = _records(dev, x, g_log, cu_seqlens, initial_state, state_cache, state_indices, o, final_state, checkpoints)
+    _call(dev, stream, LIB.gdp_gated_scan, r[0], r[1], r[2], bool(complement_input), r[3], bool(output_final_state),
+          r[4], r[5], bool(return_checkpoints), r[6], r[7], r[8], *_workspace_args(workspace, dev))
 
 
 def gdp_gated_scan_decode(x, g_log, complement_input, state_cache, state_indices, o, stream=None):
     """Direct call of the C entry point; o is caller-allocated, state_cache is updated in place."""
     dev = x.get_device()
-    _call(dev, stream, LIB.gdp_gated_scan_decode, _pack(x, dev), _pack(g_log, dev), int(bool(complement_input)),
-          _pack(state_cache, dev), _pack(state_indices, dev), _pack(o, dev))
+    r = _records(dev, x, g_log, state_cache, state_indices, o)
+    _call(dev, stream, LIB.gdp_gated_scan_decode, r[0], r[1], bool(complement_input), r[2], r[3], r[4])
 
 
 def gdp_gated_scan_backward(x, g_log, cu_seqlens, complement_input, initial_state, checkpoints, d_o, d_final_state,
                             dx, dg_log, d_initial_state, workspace, stream=None):
     """Direct call of the C entry point (caller-allocated gradients and workspace)."""
     dev = x.get_device()
-    _call(dev, stream, LIB.gdp_gated_scan_backward, _pack(x, dev), _pack(g_log, dev), _pack(cu_seqlens, dev),
-          int(bool(complement_input)), _pack(initial_state, dev), _pack(checkpoints, dev), _pack(d_o, dev),
-          _pack(d_final_state, dev), _pack(dx, dev), _pack(dg_log, dev), _pack(d_initial_state, dev),
+    r = _records(dev, x, g_log, cu_seqlens, initial_state, checkpoints, d_o, d_final_state, dx, dg_log,
+                 d_initial_state)
+    _call(dev, stream, LIB.gdp_gated_scan_backward, r[0], r[1], r[2], bool(complement_input), *r[3:10],
           *_workspace_args(workspace, dev))
 
 
 def gdp_group_norm(x, weight, bias, gate, activation, subtract_mean, eps, y, stream=None):
     """Direct call of the C entry point; `activation` is a key of ACTIVATIONS, y is caller-allocated."""
     dev = x.get_device()
-    _call(dev, stream, LIB.gdp_group_norm, _pack(x, dev), _pack(weight, dev), _pack(bias, dev), _pack(gate, dev),
-          _activation(activation), int(bool(subtract_mean)), float(eps), _pack(y, dev))
+    r = _records(dev, x, weight, bias, gate, y)
+    _call(dev, stream, LIB.gdp_group_norm, r[0], r[1], r[2], r[3], _activation(activation), bool(subtract_mean),
+          float(eps), r[4])
 
 
 def gdp_group_norm_backward(x, weight, bias, gate, activation, subtract_mean, eps, d_y, dx, dweight, dbias, dgate,
                             workspace, stream=None):
     """Direct call of the C entry point (caller-allocated gradients and workspace)."""
     dev = x.get_device()
-    _call(dev, stream, LIB.gdp_group_norm_backward, _pack(x, dev), _pack(weight, dev), _pack(bias, dev),
-          _pack(gate, dev), _activation(activation), int(bool(subtract_mean)), float(eps), _pack(d_y, dev),
-          _pack(dx, dev), _pack(dweight, dev), _pack(dbias, dev), _pack(dgate, dev),
-          *_workspace_args(workspace, dev))
+    r = _records(dev, x, weight, bias, gate, d_y, dx, dweight, dbias, dgate)
+    _call(dev, stream, LIB.gdp_group_norm_backward, r[0], r[1], r[2], r[3], _activation(activation),
+          bool(subtract_mean), float(eps), *r[4:9], *_workspace_args(workspace, dev))
 
 
 def _activation(name):

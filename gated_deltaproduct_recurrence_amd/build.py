@@ -1,4 +1,4 @@
-"""Build step: compiles the gfx950 HIP library libgdp.so in-tree with hipcc."""
+"""Build step: compiles the gfx950 HIP library libgdp.so and the binding's extension _records.so in-tree."""
 import os
 import subprocess
 import sys
@@ -17,6 +17,9 @@ SOURCES = [os.path.join(CSRC, "gdp_kernels.hip"), os.path.join(CSRC, "gdp_decode
            os.path.join(CSRC, "gdp_layer_api.cpp"),
            os.path.join(CSRC, "gdp_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+# the binding's CPython extension (host code only: torch tensors to gdp_tensor records)
+RECORDS_SOURCE = os.path.join(CSRC, "gdp_records.cpp")
+RECORDS = os.path.join(HERE, "_records.so")
 
 # Packed-fp32 VALU forms are disabled for every gfx950 compile.
 DEVICE_FLAGS = ["--offload-arch=gfx950", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
@@ -81,5 +84,22 @@ def build_library(out=LIB, verbose=False, sanitize=False):
     return out
 
 
+def build_records(out=RECORDS, verbose=False):
+    """Compile the binding's extension against the installed torch; raises CalledProcessError on failure."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    include = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths()]
+    tmp = out + ".tmp"
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          *(f"-I{i}" for i in include[:2]), *(f"-isystem{i}" for i in include[2:]), RECORDS_SOURCE, "-o", tmp,
+          *(f"-L{p}" for p in cpp_extension.library_paths()), "-ltorch_python", "-ltorch_cpu", "-lc10"], verbose)
+    os.replace(tmp, out)
+    return out
+
+
 if __name__ == "__main__":
     print(build_library(verbose=True))
+    print(build_records(verbose=True))
