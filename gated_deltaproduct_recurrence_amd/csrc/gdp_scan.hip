@@ -294,7 +294,7 @@ __device__ __forceinline__ void hand_over(S &sh, const ScanArgs &a, int tile, in
     for (int v = 0; v < WAVES; ++v) {
       const int w = REVERSE ? WAVES - 1 - v : v;
       B = apply(sh.A[w][c], B, sh.B[w][c]);
-      A *= sh.A[w][c];
+      A = sh.A[w][c] == 0.f ? 0.f : A * sh.A[w][c];  // also where A is not finite: another sequence's decays
     }
     if (!needs) A = 0.f;
     if (live && before + 1 < tiles) write_word(mine, A, B);

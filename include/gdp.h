@@ -376,8 +376,8 @@ size_t gdp_gated_scan_workspace_bytes(int64_t T, int64_t N, int64_t D);
  *                          token row 64 c where that row continues a sequence, and
  *                          unspecified elsewhere; what gdp_gated_scan_backward reads
  *   workspace    at least gdp_gated_scan_workspace_bytes(...), 256-byte aligned
- * States are held in float32.  A non-finite x stays within its sequence and
- * channel.  No output may overlap an input or another output (GDP_EALIAS).
+ * States are held in float32.  A non-finite x or g_log stays within its sequence
+ * and channel.  No output may overlap an input or another output (GDP_EALIAS).
  * Calls that share a workspace must be ordered.  Two runs on the same inputs give
  * the same bits.  One or two launches on `stream`, no allocation: capturable. */
 int gdp_gated_scan(const gdp_tensor *x, const gdp_tensor *g_log, const gdp_tensor *cu_seqlens,

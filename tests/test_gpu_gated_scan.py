@@ -237,6 +237,34 @@ def test_a_bad_value_stays_in_its_sequence_and_channel(gdp):
     assert torch.isfinite(fs.cpu()[ok]).all()
 
 
+@pytest.mark.parametrize("D", [40, 600])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 100.0])
+def test_a_bad_gate_stays_in_its_sequence_and_channel(gdp, D, bad):
+    """A decay that is not finite, in a tile that holds the end of one sequence and a part of the next:
+    neither the next one's states nor the gradients of the one before see it, to the bit."""
+    x, g, cu, s0 = make([150, 450], D, F32, F32, seed=21)
+    d_o, d_final = torch.randn_like(x), torch.randn_like(s0)
+    worse = g.clone()
+    worse[130, 3] = bad  # the first sequence's, in the tile's first wave
+    worse[190, 5] = bad  # the second one's, in the last wave of a tile of 64 rows
+    got = []
+    for gates in (g, worse):
+        o, fs, points = gdp.gated_scan(x.cuda(), gates.cuda(), cu.cuda(), initial_state=s0.cuda(),
+                                       output_final_state=True, return_checkpoints=True)
+        r = gdp.gated_scan_backward(x.cuda(), gates.cuda(), cu.cuda(), d_o.cuda(), d_final_state=d_final.cuda(),
+                                    initial_state=s0.cuda(), checkpoints=points)
+        got.append({"o": o.cpu(), "fs": fs.cpu(), **{k: v.cpu() for k, v in r.items()}})
+    good, poor = got
+    rows = torch.ones_like(x, dtype=torch.bool)
+    rows[:150, 3] = False
+    rows[150:, 5] = False
+    states = torch.ones_like(s0, dtype=torch.bool)
+    states[0, 3] = states[1, 5] = False
+    for name, value in good.items():
+        where = states if name in ("fs", "d_initial_state") else rows
+        assert torch.equal(poor[name][where], value[where]), name
+
+
 def test_no_rows(gdp):
     x, g = torch.empty(0, 24, device="cuda"), torch.empty(0, 24, device="cuda")
     s0 = torch.randn(3, 24, device="cuda")
