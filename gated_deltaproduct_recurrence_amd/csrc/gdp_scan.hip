@@ -764,11 +764,12 @@ size_t scan_state_bytes(int64_t T, int64_t D, int rows) {
   return tiles <= 1 ? 0 : (256 + (size_t)(tiles + tiles / GROUP) * D * 8 + 255) & ~(size_t)255;
 }
 
-// The grids are 32-bit (one workgroup per 64 rows and 128 channels at most, and one
-// per 64 sequences), a row's channels are reached by 32-bit byte offsets.
+// A launch holds less than 2^32 threads: one workgroup per 64 rows and 128 channels at
+// most, and one per 64 sequences; a decode step 256 threads per entry.  A row's
+// channels are reached by 32-bit byte offsets.
 bool scan_served(int64_t T, int64_t N, int64_t D) {
-  if (T >= (int64_t)1 << 36 || N >= INT32_MAX || D >= (int64_t)1 << 24) return false;
-  return (T / SCAN_ROWS + 1) * (D / NCH + 1) + N / 64 + 1 < INT32_MAX;
+  if (T >= (int64_t)1 << 36 || N >= (int64_t)1 << 24 || D >= ((int64_t)1 << 24) - 256) return false;
+  return (T / SCAN_ROWS + 1) * (D / NCH + 1) + N / 64 + 1 < ((int64_t)1 << 32) / THREADS;
 }
 
 hipError_t launch_scan(const ScanArgs &a, int xt, int gt, hipStream_t stream) {

@@ -166,6 +166,19 @@ def test_scan_sizes_past_the_launch(b):
     refused(b, scan, a, b.GDP_EUNSUPPORTED, "launch limits")
 
 
+def test_launches_of_too_many_threads(b):
+    """Each dimension of a launch holds less than 2^32 threads."""
+    for bad in ((1 << 30, 1, 1), (1 << 26, 1, 1024), (1, 1 << 24, 8)):
+        assert b.gdp_gated_scan_workspace_bytes(*bad) == 0
+    assert b.gdp_gated_scan_workspace_bytes(1 << 28, 1, 1) > 0
+    f = Fake()
+    n = 1 << 24
+    a = dict(x=f.tensor(b, b.GDP_BF16, [n, 1]), g=f.tensor(b, b.GDP_F32, [n, 1]), comp=0,
+             cache=f.tensor(b, b.GDP_F32, [9, 1]), slots=f.tensor(b, b.GDP_I64, [n]),
+             o=f.tensor(b, b.GDP_BF16, [n, 1]), fake=f)
+    refused(b, decode, a, b.GDP_EUNSUPPORTED, "launch limits")
+
+
 def test_decode_refusals(b):
     def args():
         f = Fake()
