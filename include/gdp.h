@@ -358,8 +358,8 @@ size_t gdp_gated_scan_workspace_bytes(int64_t T, int64_t N, int64_t D);
  *   g_log        [T, D]    f32 or x's dtype; log decays, g_log <= 0 (a positive
  *                          entry is served while the products of decays over 128
  *                          rows stay finite in float32); -inf drops the state before
- *                          (the rows behind a -inf that meets a state which is not
- *                          finite are unspecified)
+ *                          (a state which is not finite may end at a -inf, or where
+ *                          the product of its decays falls below 2^-126, or go on)
  *   cu_seqlens   [N+1]     int32 or int64, contiguous
  *   initial_state [N, D]   f32 contiguous, or data == NULL for zeros
  *   output_final_state     write final_state when nonzero
