@@ -28,7 +28,9 @@
 // 16 tiles instead, each with a word of its own: a tile reads the pairs of the tiles
 // before it in its group, other lanes the state entering the group, and the group's
 // last tile publishes the group's pair and then its state.  There the tiles' words
-// are pairs only, so that the order of the sums is fixed here too.
+// are pairs only, so that the order of the sums is fixed here too.  A group's pair
+// keeps its A with an exponent of its own (gdp_scan_words.h): 2048 rows of decays
+// leave float32 in both directions while the states between them do not.
 // The words are written and read with relaxed agent-scope atomics (8 bytes, so a
 // pair is whole), which go past the XCDs' own caches; all-ones bits (two NaNs that
 // no published pair has) mean not yet written, and a fill kernel sets them before.
@@ -60,6 +62,7 @@
 
 #include "gdp_layer.h"
 #include "gdp_layer_common.h"
+#include "gdp_scan_words.h"
 
 namespace gdp {
 namespace {
@@ -68,7 +71,6 @@ constexpr int WAVES = 8, THREADS = 64 * WAVES;
 constexpr int VEC = 2, NCH = 64 * VEC;  // channels per lane and per workgroup
 constexpr int GROUP = 16;               // tiles per group
 constexpr int WINDOW = 8;               // words before its own that a lane looks at
-constexpr uint64_t NOT_WRITTEN = ~0ull;
 constexpr int MOST_LOOKS = 1 << 21;
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -125,14 +127,6 @@ __device__ __forceinline__ void load_rows(Pair<T> (&v)[R], const T *base, int64_
   }
 }
 
-// the map (A, B) applied to h; A = 0 drops h, also one that is not finite
-__device__ __forceinline__ float apply(float A, float h, float B) { return A == 0.f ? B : fmaf(A, h, B); }
-
-__device__ __forceinline__ uint64_t make_word(float A, float B) {
-  const uint32_t a = A != A ? 0x7fc00000u : __float_as_uint(A);  // a NaN that is not NOT_WRITTEN's
-  return ((uint64_t)a << 32) | __float_as_uint(B);
-}
-
 template <int R> struct Shared {
   static constexpr int ROWS = WAVES * R;
   float A[WAVES][NCH], B[WAVES][NCH];
@@ -180,14 +174,13 @@ template <int R> __device__ __forceinline__ uint32_t marked(const int *ids, int 
 __device__ __forceinline__ uint64_t read_word(const uint64_t *w) {
   return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void write_word(uint64_t *w, float A, float B) {
-  __hip_atomic_store(w, make_word(A, B), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void write_word(uint64_t *w, uint64_t word) {
+  __hip_atomic_store(w, word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ float part_a(uint64_t word) { return __uint_as_float((uint32_t)(word >> 32)); }
-__device__ __forceinline__ float part_b(uint64_t word) { return __uint_as_float((uint32_t)word); }
 
 // The state that the `count` words before hand on, of one channel: `word` is the
 // nearest one, the others lie `step` words apart.
+template <bool GROUP_WORDS>
 __device__ __forceinline__ float entering(const uint64_t *word, int64_t step, int count, bool live) {
   uint64_t v[WINDOW];
   auto read = [&](const uint64_t *w, int i) {  // before the first there is a state of 0
@@ -200,7 +193,7 @@ __device__ __forceinline__ float entering(const uint64_t *word, int64_t step, in
 #pragma unroll
     for (int i = 0; i < n; ++i) {
       const bool there = v[i] != NOT_WRITTEN;
-      found = found || (open && there && part_a(v[i]) == 0.f);
+      found = found || (open && there && drops_all(v[i]));
       open = open && there && !found;
     }
   };
@@ -217,7 +210,7 @@ __device__ __forceinline__ float entering(const uint64_t *word, int64_t step, in
       look(WINDOW);
       if (__all(found)) break;
       if (looks == MOST_LOOKS) {
-        h = __uint_as_float(0x7fc00000u);
+        h = float_of(QUIET_NAN);
         break;
       }
       __builtin_amdgcn_s_sleep(1);
@@ -229,13 +222,12 @@ __device__ __forceinline__ float entering(const uint64_t *word, int64_t step, in
   }
 #pragma unroll
   for (int i = WINDOW - 1; i >= 0; --i)
-    if (v[i] != NOT_WRITTEN) h = apply(part_a(v[i]), h, part_b(v[i]));
+    if (v[i] != NOT_WRITTEN) h = behind<GROUP_WORDS>(v[i], h);
   return h;
 }
 
 // The map of the `count` tiles before this one in its group, of one channel.
-struct Map { float A, B; };
-__device__ __forceinline__ Map group_so_far(const uint64_t *word, int64_t step, int count, bool live) {
+__device__ __forceinline__ Span group_so_far(const uint64_t *word, int64_t step, int count, bool live) {
   uint64_t v[GROUP - 1];
 #pragma unroll
   for (int i = 0; i < GROUP - 1; ++i) v[i] = NOT_WRITTEN;
@@ -248,22 +240,19 @@ __device__ __forceinline__ Map group_so_far(const uint64_t *word, int64_t step, 
     for (int i = 0; i < GROUP - 1; ++i) {
       if (i < count) {
         there = there && (!open || v[i] != NOT_WRITTEN);
-        open = open && !(v[i] != NOT_WRITTEN && part_a(v[i]) == 0.f);
+        open = open && !(v[i] != NOT_WRITTEN && drops_all(v[i]));
       }
     }
     if (__all(there)) break;
-    if (looks == MOST_LOOKS) return Map{0.f, __uint_as_float(0x7fc00000u)};
+    if (looks == MOST_LOOKS) return Span{0.f, 0, float_of(QUIET_NAN)};
     __builtin_amdgcn_s_sleep(1);
     asm volatile("" : "+v"(word));
   }
-  Map m{1.f, 0.f};
+  Span s = no_rows();
 #pragma unroll
   for (int i = GROUP - 2; i >= 0; --i)
-    if (i < count && v[i] != NOT_WRITTEN) {
-      m.B = apply(part_a(v[i]), m.B, part_b(v[i]));
-      m.A = part_a(v[i]) == 0.f ? 0.f : m.A * part_a(v[i]);
-    }
-  return m;
+    if (i < count && v[i] != NOT_WRITTEN) s = then(s, part_a(v[i]), part_b(v[i]));
+  return normal(s);
 }
 
 // The waves' maps in sh.A, sh.B: composes the tile's, publishes it, and leaves in
@@ -282,7 +271,7 @@ __device__ __forceinline__ void hand_over(S &sh, const ScanArgs &a, int tile, in
   uint64_t *groups = at(words + ((int64_t)tiles + group) * a.D, first + c);
   if (GROUPS && role == 1) {  // the state entering the group
     if (needs && tiles > 1) {
-      sh.state[c] = entering(groups - a.D, -a.D, group, live);
+      sh.state[c] = entering<true>(groups - a.D, -a.D, group, live);
       __hip_atomic_store(&sh.there[c >> 6], 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_WORKGROUP);
     }
     return;
@@ -297,24 +286,25 @@ __device__ __forceinline__ void hand_over(S &sh, const ScanArgs &a, int tile, in
       A = sh.A[w][c] == 0.f ? 0.f : A * sh.A[w][c];  // also where A is not finite: another sequence's decays
     }
     if (!needs) A = 0.f;
-    if (live && before + 1 < tiles) write_word(mine, A, B);
+    if (live && before + 1 < tiles) write_word(mine, make_word(A, B));
     if (!GROUPS) {
       if (needs) {
-        carry = entering(mine + step, step, before, live);
-        if (live && before + 1 < tiles && A != 0.f) write_word(mine, 0.f, fmaf(A, carry, B));
+        carry = entering<false>(mine + step, step, before, live);
+        if (live && before + 1 < tiles && A != 0.f) write_word(mine, make_word(0.f, fmaf(A, carry, B)));
       }
     } else {
       const bool last = place == GROUP - 1 && before + 1 < tiles && live;
-      Map m{0.f, 0.f};
-      if (needs) m = group_so_far(mine + step, step, place, live);
-      const float GA = A == 0.f ? 0.f : A * m.A, GB = apply(A, m.B, B);
-      if (last) write_word(groups, GA, GB);
+      Span sofar{0.f, 0, 0.f};
+      if (needs) sofar = group_so_far(mine + step, step, place, live);
+      const Span group_map = normal(then(sofar, A, B));
+      const uint64_t word = make_word(group_map);
+      if (last) write_word(groups, word);
       if (needs) {
         while (!__hip_atomic_load(&sh.there[c >> 6], __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_WORKGROUP))
           __builtin_amdgcn_s_sleep(1);
         const float state = sh.state[c];
-        carry = apply(m.A, state, m.B);
-        if (last && GA != 0.f) write_word(groups, 0.f, fmaf(GA, state, GB));
+        carry = apply(sofar, state);
+        if (last && !drops_all(word)) write_word(groups, make_word(0.f, apply(group_map, state)));
       }
     }
   }

@@ -357,7 +357,9 @@ size_t gdp_gated_scan_workspace_bytes(int64_t T, int64_t N, int64_t D);
  *   x            [T, D]    f32, bf16 or f16; rows may be strided
  *   g_log        [T, D]    f32 or x's dtype; log decays, g_log <= 0 (a positive
  *                          entry is served while the products of decays over 128
- *                          rows stay finite in float32); -inf drops the state before
+ *                          rows and fewer stay finite in float32, for any number of
+ *                          channels); what such a product below 2^-126 leaves of a
+ *                          state may be taken for 0; -inf drops the state before
  *                          (a state which is not finite may end at a -inf, or where
  *                          the product of its decays falls below 2^-126, or go on)
  *   cu_seqlens   [N+1]     int32 or int64, contiguous
