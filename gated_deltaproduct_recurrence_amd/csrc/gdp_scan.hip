@@ -40,7 +40,8 @@
 // and the first of the waiting tiles (or groups) finds its predecessor's word at
 // A = 0: every wait ends.  (It is bounded all the same, at 2^21 looks, seconds:
 // when calls on two streams share a workspace against the contract, tickets can be
-// lost, and the rows behind then become NaN instead of the GPU hanging.)
+// lost.  The lost tiles' rows are then left as they are, and the sequences' rows behind
+// become NaN, instead of the GPU hanging.)
 //
 // What bounds it, measured on MI355X (a 1 GiB copy reaches 5.0 TB/s).  32768 x 2048
 // bfloat16 with float32 gates: 112 us, 4.8 TB/s of the operands' bytes; 131104 x 4096
@@ -179,7 +180,7 @@ __device__ __forceinline__ void write_word(uint64_t *w, uint64_t word) {
 }
 
 // The state that the `count` words before hand on, of one channel: `word` is the
-// nearest one, the others lie `step` words apart.
+// nearest one, the others lie `step` words apart.  NaN where the wait is given up.
 template <bool GROUP_WORDS>
 __device__ __forceinline__ float entering(const uint64_t *word, int64_t step, int count, bool live) {
   uint64_t v[WINDOW];
@@ -201,18 +202,13 @@ __device__ __forceinline__ float entering(const uint64_t *word, int64_t step, in
   constexpr int NEAR = WINDOW / 2;
 #pragma unroll
   for (int i = 0; i < WINDOW; ++i) v[i] = i < NEAR ? read(word, i) : NOT_WRITTEN;
-  float h = 0.f;
   look(NEAR);
   if (!__all(found)) {
 #pragma unroll
     for (int i = NEAR; i < WINDOW; ++i) v[i] = read(word, i);
     for (int looks = 0;; ++looks) {
       look(WINDOW);
-      if (__all(found)) break;
-      if (looks == MOST_LOOKS) {
-        h = float_of(QUIET_NAN);
-        break;
-      }
+      if (__all(found) || looks == MOST_LOOKS) break;
       __builtin_amdgcn_s_sleep(1);
       asm volatile("" : "+v"(word));  // or every word's address is kept in registers over the loop
 #pragma unroll
@@ -220,39 +216,30 @@ __device__ __forceinline__ float entering(const uint64_t *word, int64_t step, in
         if (i == WINDOW - 1 || v[i] == NOT_WRITTEN) v[i] = read(word, i);
     }
   }
-#pragma unroll
-  for (int i = WINDOW - 1; i >= 0; --i)
-    if (v[i] != NOT_WRITTEN) h = behind<GROUP_WORDS>(v[i], h);
-  return h;
+  return fold<GROUP_WORDS>(v);
 }
 
-// The map of the `count` tiles before this one in its group, of one channel.
+// The map of the `count` tiles before this one in its group, of one channel; its B is
+// NaN where the wait is given up.
 __device__ __forceinline__ Span group_so_far(const uint64_t *word, int64_t step, int count, bool live) {
   uint64_t v[GROUP - 1];
 #pragma unroll
-  for (int i = 0; i < GROUP - 1; ++i) v[i] = NOT_WRITTEN;
+  for (int i = 0; i < GROUP - 1; ++i) v[i] = i < count ? NOT_WRITTEN : NOTHING;
   for (int looks = 0;; ++looks) {
 #pragma unroll
     for (int i = 0; i < GROUP - 1; ++i)
-      if (i < count && v[i] == NOT_WRITTEN) v[i] = live ? read_word(word + i * step) : 0;
+      if (v[i] == NOT_WRITTEN) v[i] = live ? read_word(word + i * step) : 0;
     bool open = true, there = true;  // all that matter: up to the nearest with A = 0
 #pragma unroll
     for (int i = 0; i < GROUP - 1; ++i) {
-      if (i < count) {
-        there = there && (!open || v[i] != NOT_WRITTEN);
-        open = open && !(v[i] != NOT_WRITTEN && drops_all(v[i]));
-      }
+      there = there && (!open || v[i] != NOT_WRITTEN);
+      open = open && !(v[i] != NOT_WRITTEN && drops_all(v[i]));
     }
-    if (__all(there)) break;
-    if (looks == MOST_LOOKS) return Span{0.f, 0, float_of(QUIET_NAN)};
+    if (__all(there) || looks == MOST_LOOKS) break;
     __builtin_amdgcn_s_sleep(1);
     asm volatile("" : "+v"(word));
   }
-  Span s = no_rows();
-#pragma unroll
-  for (int i = GROUP - 2; i >= 0; --i)
-    if (i < count && v[i] != NOT_WRITTEN) s = then(s, part_a(v[i]), part_b(v[i]));
-  return normal(s);
+  return span_over(v);
 }
 
 // The waves' maps in sh.A, sh.B: composes the tile's, publishes it, and leaves in

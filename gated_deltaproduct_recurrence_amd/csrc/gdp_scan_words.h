@@ -7,7 +7,9 @@
 // whose decays can multiply to far less, or (positive log decays) far more, than a
 // float32 although every state on the way is one.  Its A is kept as m 2^e with m in
 // [1/2, 1): 23 bits of m and 9 of e, which leaves 2^-255 .. 2^255.
-// A = 0 says that nothing before matters; all-ones bits mean not yet written.
+// A = 0 says that nothing before matters; all-ones bits mean not yet written.  Read as
+// a pair those are (not 0, NaN): a word that is missing where a state is formed
+// makes it NaN, unless a nearer word drops what was before.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -75,10 +77,23 @@ __host__ __device__ __forceinline__ Span span_of(uint64_t word) {
 
 __host__ __device__ __forceinline__ bool drops_all(uint64_t word) { return (uint32_t)(word >> 32) == 0; }
 
-// h behind the rows of a tile's (group's) word
-template <bool GROUP_WORD> __host__ __device__ __forceinline__ float behind(uint64_t word, float h) {
-  if constexpr (GROUP_WORD) return apply(span_of(word), h);
-  return apply(part_a(word), h, part_b(word));
+// The state behind the words v[N - 1] .. v[0]: known if one of them drops what was
+// before and all nearer ones are written, else NaN.
+template <bool GROUP_WORDS, int N> __host__ __device__ __forceinline__ float fold(const uint64_t (&v)[N]) {
+  float h = float_of(QUIET_NAN);
+#pragma unroll
+  for (int i = N - 1; i >= 0; --i)
+    h = GROUP_WORDS ? apply(span_of(v[i]), h) : apply(part_a(v[i]), h, part_b(v[i]));
+  return h;
+}
+
+// The map of the tiles of the words v[N - 1] .. v[0].  NOTHING is the word of no rows.
+constexpr uint64_t NOTHING = 0x3f800000ull << 32;
+template <int N> __host__ __device__ __forceinline__ Span span_over(const uint64_t (&v)[N]) {
+  Span s = no_rows();
+#pragma unroll
+  for (int i = N - 1; i >= 0; --i) s = then(s, part_a(v[i]), part_b(v[i]));
+  return normal(s);
 }
 
 }  // namespace gdp
