@@ -3,6 +3,9 @@
 Argument marshalling only: torch supplies device memory and the current
 stream; every step of the computation runs in the library's HIP kernels.  If
 the library is missing this module raises on import -- there is no fallback.
+The entries of the recurrence and of the norm also need the extension
+_records.so, built for this Python and torch; without it they raise when
+called, and the others work.
 """
 import ctypes
 import os
@@ -11,9 +14,12 @@ import torch
 
 try:
     from ._records import records as _records  # (after torch, whose libraries it needs)
-except ImportError as e:
-    raise ImportError(f"the binding's extension is not built ({e}); run __graft_entry__.build() "
-                      "(gated_deltaproduct_recurrence_amd/build.py)") from e
+except ImportError as _e:
+    _why = str(_e)
+
+    def _records(*_):
+        raise ImportError(f"the binding's extension is not built for this Python and torch ({_why}); run "
+                          "__graft_entry__.build() (gated_deltaproduct_recurrence_amd/build.py)")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # GDP_LIBRARY names another build of the library (the host-sanitized check

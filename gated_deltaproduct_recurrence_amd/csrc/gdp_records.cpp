@@ -9,6 +9,7 @@
 
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <cstring>
 #include <exception>
@@ -108,6 +109,27 @@ PyMethodDef methods[] = {{"records", (PyCFunction)(void *)records, METH_FASTCALL
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_records", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
+// "3.10" of "3.10.12 (main, ...)", "2.10.0" of "2.10.0+rocm7.0"
+std::string python_of(const std::string &v) { return v.substr(0, v.find('.', v.find('.') + 1)); }
+std::string torch_of(const std::string &v) { return v.substr(0, v.find('+')); }
+
 }  // namespace
 
-PyMODINIT_FUNC PyInit__records(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__records(void) {
+  // the file's name does not say what it was built for
+  if (python_of(Py_GetVersion()) != python_of(PY_VERSION)) {
+    PyErr_Format(PyExc_ImportError, "built for Python %s", PY_VERSION);
+    return nullptr;
+  }
+  PyObject *torch = PyImport_ImportModule("torch");
+  PyObject *version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+  const char *text = version ? PyUnicode_AsUTF8(version) : nullptr;
+  const bool same = text && torch_of(text) == torch_of(TORCH_VERSION);
+  Py_XDECREF(version);
+  Py_XDECREF(torch);
+  if (!same) {
+    if (!PyErr_Occurred()) PyErr_Format(PyExc_ImportError, "built for torch %s", TORCH_VERSION);
+    return nullptr;
+  }
+  return PyModule_Create(&module);
+}
