@@ -12,15 +12,6 @@ import os
 
 import torch
 
-try:
-    from ._records import records as _records  # (after torch, whose libraries it needs)
-except ImportError as _e:
-    _why = str(_e)
-
-    def _records(*_):
-        raise ImportError(f"the binding's extension is not built for this Python and torch ({_why}); run "
-                          "__graft_entry__.build() (gated_deltaproduct_recurrence_amd/build.py)")
-
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # GDP_LIBRARY names another build of the library (the host-sanitized check
 # build of the CPU sanitizer run); by default the in-tree libgdp.so
@@ -126,6 +117,25 @@ def _load(path=LIB_PATH):
 
 
 LIB = _load()
+
+
+def _load_records():
+    """records() of the extension; where that is missing or built for something else, one that says so."""
+    try:
+        from . import _records as ext  # (after torch, whose libraries it needs)
+        if ext.record_bytes != ctypes.sizeof(gdp_tensor):
+            raise ImportError(f"it fills records of {ext.record_bytes} bytes, gdp_tensor has {ctypes.sizeof(gdp_tensor)}")
+        return ext.records
+    except (ImportError, AttributeError) as e:
+        why = str(e)
+
+    def records(*_):
+        raise ImportError(f"the binding's extension is not built for this library, Python and torch ({why}); run "
+                          "__graft_entry__.build() (gated_deltaproduct_recurrence_amd/build.py)")
+    return records
+
+
+_records = _load_records()
 
 _DT = {torch.float32: GDP_F32, torch.bfloat16: GDP_BF16, torch.int32: GDP_I32, torch.int64: GDP_I64,
        torch.float16: GDP_F16}

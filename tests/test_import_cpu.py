@@ -35,6 +35,8 @@ print("done")
 
 @pytest.mark.parametrize("prepare,why", [
     ("sys.modules['gated_deltaproduct_recurrence_amd._records'] = None", "_records"),
+    ("import types; m = types.ModuleType('_records'); m.record_bytes, m.records = 72, lambda *a: a\n"
+     "sys.modules['gated_deltaproduct_recurrence_amd._records'] = m", "72 bytes"),
     ("torch.__version__ = '1.2.3+other'", "built for torch"),
 ])
 def test_the_older_entries_need_no_extension(prepare, why):

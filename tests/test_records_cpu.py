@@ -1,5 +1,6 @@
 """The binding's extension: gdp_tensor records of torch tensors (host tensors here), against the ctypes
 marshalling, and its refusals."""
+import ctypes
 import os
 
 import pytest
@@ -62,3 +63,11 @@ def test_refusals():
 
 def test_source_exists():
     assert os.path.isfile(build.RECORDS_SOURCE)
+
+
+def test_record_size():
+    """An extension that was built against another gdp_tensor is not used (tests/test_import_cpu.py)."""
+    from gated_deltaproduct_recurrence_amd import _records
+    assert _records.record_bytes == ctypes.sizeof(binding.gdp_tensor)
+    one, two = records(-1, torch.zeros(2), torch.zeros(2))[:2]
+    assert two - one == _records.record_bytes
