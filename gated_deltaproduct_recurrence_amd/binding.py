@@ -602,6 +602,7 @@ def group_norm_backward(x, d_y, weight=None, bias=None, gate=None, activation=No
     dx = _empty(x)
     dz = _empty(x) if gate is not None else None
     dw, db = (None if p is None else _empty(p, dtype=torch.float32) for p in (weight, bias))
+    sums = weight is not None or bias is not None
     gdp_group_norm_backward(x, weight, bias, gate, activation, subtract_mean, eps, d_y, dx, dw, db, dz,
-                            _workspace(x, gdp_group_norm_backward_workspace_bytes(T, G, V)))
+                            _workspace(x, gdp_group_norm_backward_workspace_bytes(T, G, V)) if sums else None)
     return {"dx": dx, "dweight": dw, "dbias": db, "dgate": dz}

@@ -423,7 +423,8 @@ int gdp_group_norm_backward(const gdp_tensor *x, const gdp_tensor *weight, const
     if (grads[i]->dtype != GDP_F32) return fail(GDP_EUNSUPPORTED, "%s must be float32", name);
     if (!contiguous(grads[i])) return fail(GDP_EINVAL, "%s must be contiguous", name);
   }
-  const size_t need = gdp_group_norm_backward_workspace_bytes(T, G, V);
+  const bool sums = present(weight) || present(bias);
+  const size_t need = sums ? gdp_group_norm_backward_workspace_bytes(T, G, V) : 0;
   if ((rc = check_workspace(workspace, workspace_bytes, need))) return rc;
   const Range ins[] = {range_of(x, "x"), range_of(weight, "weight"), range_of(bias, "bias"), range_of(gate, "gate"),
                        range_of(d_y, "d_y")};

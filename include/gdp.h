@@ -453,8 +453,8 @@ enum gdp_activation { GDP_ACT_NONE = 0, GDP_ACT_SILU = 1, GDP_ACT_SIGMOID = 2 };
 int gdp_group_norm(const gdp_tensor *x, const gdp_tensor *weight, const gdp_tensor *bias, const gdp_tensor *gate,
                    int32_t activation, int32_t subtract_mean, float eps, const gdp_tensor *y, void *stream);
 
-/* Host-only.  Workspace bytes gdp_group_norm_backward needs: partial sums of the
- * weight and bias gradients.  0 for invalid sizes. */
+/* Host-only.  Workspace bytes gdp_group_norm_backward needs where a weight or a bias
+ * is given: partial sums of their gradients.  0 for invalid sizes. */
 size_t gdp_group_norm_backward_workspace_bytes(int64_t T, int64_t G, int64_t V);
 
 /* Device.  Gradients of gdp_group_norm (the same x, weight, bias, gate, activation,
@@ -463,7 +463,8 @@ size_t gdp_group_norm_backward_workspace_bytes(int64_t T, int64_t G, int64_t V);
  *   dweight, dbias          f32, contiguous, the shape of weight and bias; required iff
  *                           weight, respectively bias, is given: summed over the tokens
  *                           (and the groups that share them) in a fixed order
- *   workspace    at least gdp_group_norm_backward_workspace_bytes(...), 256-byte aligned
+ *   workspace    at least gdp_group_norm_backward_workspace_bytes(...), 256-byte aligned;
+ *                not used without weight and bias
  * The statistics are formed again from x.  No gradient may overlap an input or another
  * gradient (GDP_EALIAS).  Everything on `stream`, no allocation: capturable. */
 int gdp_group_norm_backward(const gdp_tensor *x, const gdp_tensor *weight, const gdp_tensor *bias,
