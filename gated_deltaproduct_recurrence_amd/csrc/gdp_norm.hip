@@ -158,7 +158,7 @@ __device__ __forceinline__ float normalise(float (&xhat)[E][VEC], const Values<T
 }
 
 // The team's place: its group and first token.
-struct Place { int q, g; int64_t t, t_block, step; };
+struct Place { int q, g; int64_t t, t_block, step; };  // step >= T where a team has one pair
 __device__ __forceinline__ Place place_of(const NormArgs &a, int teams, int team) {
   Place p;
   p.q = (int)blockIdx.x * teams + team;
@@ -376,15 +376,18 @@ Plan plan_of(int64_t V, int vec) {
 int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
 
 // Workgroups: one pair per team while that gives at most `most` / 2, then down to
-// `per_team` pairs per team, at most `most`; in multiples that keep a team's group.
+// `per_team` pairs per team, at most `most`.  Teams that take more than one pair come
+// in multiples that keep a team's group; no more workgroups than there are pairs for,
+// however few tokens an odd number of groups has.
 int64_t grid_of(const Plan &p, int64_t T, int G, int64_t per_team, int64_t most) {
   const int64_t want = (T * G + p.teams - 1) / p.teams, unit = G / gcd(G, p.teams);
   int64_t n = want;
   if (want > most / 2) {
     n = want / per_team;
     n = n < most / 2 ? most / 2 : (n > most ? most : n);
+    n = (n + unit - 1) / unit * unit;
   }
-  return (n + unit - 1) / unit * unit;
+  return n < want ? n : want;
 }
 constexpr int64_t FORWARD_GRID = 1024, BACKWARD_GRID = 768;
 
@@ -482,7 +485,9 @@ hipError_t launch_norm_backward(const NormArgs &a, int xt, hipStream_t stream) {
     }
     if (!a.dw && !a.db) return hipSuccess;
     const bool shared = a.w_sh == 0, fold = shared && p.lpg <= 64 && p.teams > 1;
-    const int64_t rows = fold ? blocks : blocks * p.teams;
+    // the teams that had a pair: all, or (one pair each) the first T G
+    const int64_t teams = blocks * p.teams < a.T * a.G ? blocks * p.teams : a.T * a.G;
+    const int64_t rows = fold ? blocks : teams;
     const dim3 grid((unsigned)((a.V + 15) / 16), shared ? 1u : (unsigned)a.G, 2);
     hipLaunchKernelGGL(gdp_norm_weight_kernel, grid, dim3(1024), 0, stream, a, (int)(shared ? rows : rows / a.G),
                        shared ? 1 : a.G);

@@ -24,3 +24,16 @@ def test_no_parameters_need_no_workspace(b):
         a = change(b, norm_args(b), **absent)
         a["ws"], a["wsb"] = None, 0
         refused(b, norm_backward, a, b.GDP_EWORKSPACE, "needed")
+
+
+def test_the_workspace_follows_the_input(b):
+    """At most one row of sums (weight and bias, float32) per group of a token, or per team of a workgroup."""
+    need = b.gdp_group_norm_backward_workspace_bytes
+    assert need(1, 65535, 8) < 5 << 20 and need(1, 4097, 128) < 5 << 20
+    rng = random.Random(7)
+    sizes = [(1, 1, 1), (1, 65535, 1), (1, 65535, 16384), (3, 4099, 100), (5, 4097, 16384)]
+    for _ in range(3000):
+        V = rng.choice([rng.randint(1, 16384), 1 << rng.randint(0, 14)])
+        sizes.append((int(2 ** rng.uniform(0, 17)), int(2 ** rng.uniform(0, 15.99)), V))
+    for T, G, V in sizes:
+        assert 0 < need(T, G, V) <= 8 * V * (T * G + 256) + 255, (T, G, V)
