@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstring>
 
@@ -327,7 +328,8 @@ int norm_args(const gdp_tensor *x, const gdp_tensor *weight, const gdp_tensor *b
                 (long long)G, (long long)V);
   if (activation != GDP_ACT_NONE && activation != GDP_ACT_SILU && activation != GDP_ACT_SIGMOID)
     return fail(GDP_EINVAL, "unknown activation %d", activation);
-  if (!(eps > 0.f) || std::isinf(eps)) return fail(GDP_EINVAL, "eps must be positive and finite");
+  // (the kernels' 1 / sqrt takes a subnormal variance for 0)
+  if (!(eps >= FLT_MIN) || std::isinf(eps)) return fail(GDP_EINVAL, "eps must be at least 2^-126, and finite");
   const int64_t s3[3] = {T, G, V}, s2[2] = {G, V}, s1[1] = {V};
   int rc;
   if ((rc = check_shape(x, "x", 3, s3))) return rc;

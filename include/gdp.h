@@ -444,7 +444,7 @@ enum gdp_activation { GDP_ACT_NONE = 0, GDP_ACT_SILU = 1, GDP_ACT_SIGMOID = 2 };
  *   bias         as weight, or data == NULL for zeros; with a weight its shape and dtype
  *   gate         [T, G, V]  x's dtype, may be strided, or data == NULL
  *   activation   a gdp_activation
- *   eps          > 0
+ *   eps          at least 2^-126, finite
  *   y            [T, G, V]  x's dtype, may be strided
  * Statistics and products are float32 (the squares of x - mean must stay finite
  * there); y is rounded once.  y may not overlap an input

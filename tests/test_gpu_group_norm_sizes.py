@@ -27,3 +27,15 @@ def test_no_parameters_and_no_workspace(gdp, T, G, V):  # noqa: F811
     gdp.gdp_group_norm_backward(x.cuda(), None, None, z.cuda(), "silu", False, 1e-5, dy.cuda(), dx, None, None, dz, None)
     close(dx, want["dx"], want["dx_bound"], "dx", F32)
     close(dz, want["dgate"], want["dgate_bound"], "dgate", F32)
+
+
+def test_the_smallest_eps(gdp):  # noqa: F811
+    """Groups without variance give the bias, at the smallest eps; groups of tiny values what the formula gives."""
+    eps = 2.0 ** -126
+    x, w, b, z, dy = make(9, 4, 64, F32, weight="channel", bias=True, gated=False, seed=9)
+    flat = torch.full_like(x, 0.5)
+    y = gdp.group_norm(flat.cuda(), weight=w.cuda(), bias=b.cuda(), eps=eps)
+    assert torch.equal(y.cpu(), b.expand(9, 4, 64))
+    d = gdp.group_norm_backward(flat.cuda(), dy.cuda(), weight=w.cuda(), bias=b.cuda(), eps=eps)
+    assert all(torch.isfinite(t).all() for t in d.values() if t is not None) and not d["dweight"].any()
+    check_norm(gdp, 1e-15 * x, w, b, None, dy, "silu", True, eps=eps)

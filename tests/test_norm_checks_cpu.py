@@ -1,10 +1,10 @@
-"""The workspace of the group norm's gradients: asked for where there are sums to form, and in proportion to the
-input (host-side, no GPU; pointers are fake and never dereferenced)."""
+"""Host-side checks of the group norm: eps, and the workspace of the gradients, asked for where there are sums to
+form and in proportion to the input (no GPU; pointers are fake and never dereferenced)."""
 import random
 
 import pytest
 
-from tests.test_layer_abi_cpu import change, norm_args, norm_backward, refused
+from tests.test_layer_abi_cpu import change, norm, norm_args, norm_backward, refused
 
 
 @pytest.fixture(scope="module")
@@ -37,3 +37,14 @@ def test_the_workspace_follows_the_input(b):
         sizes.append((int(2 ** rng.uniform(0, 17)), int(2 ** rng.uniform(0, 15.99)), V))
     for T, G, V in sizes:
         assert 0 < need(T, G, V) <= 8 * V * (T * G + 256) + 255, (T, G, V)
+
+
+@pytest.mark.parametrize("call", [norm, norm_backward])
+def test_eps_below_the_normal_numbers_is_refused(b, call):
+    """1 / sqrt serves no subnormal variance; the smallest normal eps is let through, to the overlap."""
+    for eps, code, text in ((2.0 ** -127, b.GDP_EINVAL, "eps"), (1e-40, b.GDP_EINVAL, "eps"),
+                            (2.0 ** -126, b.GDP_EALIAS, "overlaps input x")):
+        a = norm_args(b)
+        a["eps"] = eps
+        a["y"].data = a["dx"].data = a["x"].data
+        refused(b, call, a, code, text)
