@@ -291,7 +291,7 @@ size_t gdp_workspace_bytes(int64_t T, int64_t N, int32_t n, int32_t Hqk, int32_t
 int gdp_build_descriptors(const gdp_tensor *cu_seqlens, int32_t n, int64_t T, const gdp_descriptors *out,
                           void *stream) {
   if (!present(cu_seqlens) || !out) return fail(GDP_EINVAL, "build_descriptors: cu_seqlens and out are required");
-  if (cu_seqlens->ndim != 1 || cu_seqlens->shape[0] < 1 || cu_seqlens->stride[0] != 1)
+  if (cu_seqlens->ndim != 1 || cu_seqlens->shape[0] < 1 || !contiguous(cu_seqlens))
     return fail(GDP_EINVAL, "cu_seqlens must be a contiguous [N+1] vector");
   if (cu_seqlens->dtype != GDP_I32 && cu_seqlens->dtype != GDP_I64)
     return fail(GDP_EINVAL, "cu_seqlens must be int32 or int64");
@@ -340,7 +340,7 @@ static int prefill_impl(const gdp_tensor *q, const gdp_tensor *k, const gdp_tens
   if (v->ndim != 3) return fail(GDP_EINVAL, "v must be [T*n, Hv, V]");
   const int64_t T = q->shape[0], Hqk = q->shape[1], K = q->shape[2];
   const int64_t Hv = v->shape[1], V = v->shape[2], Hk = k->shape[1];
-  if (cu_seqlens->ndim != 1 || cu_seqlens->shape[0] < 1 || cu_seqlens->stride[0] != 1)
+  if (cu_seqlens->ndim != 1 || cu_seqlens->shape[0] < 1 || !contiguous(cu_seqlens))
     return fail(GDP_EINVAL, "cu_seqlens must be a contiguous [N+1] vector");
   if (cu_seqlens->dtype != GDP_I32 && cu_seqlens->dtype != GDP_I64)
     return fail(GDP_EINVAL, "cu_seqlens must be int32 or int64");

@@ -45,14 +45,15 @@ inline int elem_size(int32_t dt) {
   }
 }
 
-// Checks ndim, the exact shape and that the innermost stride is 1.
+// Checks ndim, the exact shape and that the innermost stride is 1 (of one element it
+// does not matter, and torch keeps any there).
 inline int check_shape(const gdp_tensor *t, const char *name, int ndim, const int64_t *shape) {
   if (t->ndim != ndim) return fail(GDP_EINVAL, "%s: expected %d dims, got %d", name, ndim, t->ndim);
   for (int d = 0; d < ndim; ++d)
     if (shape[d] >= 0 && t->shape[d] != shape[d])
       return fail(GDP_EINVAL, "%s: dim %d is %lld, expected %lld", name, d, (long long)t->shape[d],
                   (long long)shape[d]);
-  if (ndim > 0 && t->stride[ndim - 1] != 1)
+  if (ndim > 0 && t->shape[ndim - 1] != 1 && t->stride[ndim - 1] != 1)
     return fail(GDP_EINVAL, "%s: innermost dimension must be contiguous", name);
   return GDP_OK;
 }

@@ -47,7 +47,7 @@ int check_states(const gdp_tensor *t, const char *name, int64_t R, int64_t C) {
 }
 
 int check_cu(const gdp_tensor *cu) {
-  if (cu->ndim != 1 || cu->shape[0] < 1 || cu->stride[0] != 1)
+  if (cu->ndim != 1 || cu->shape[0] < 1 || !contiguous(cu))
     return fail(GDP_EINVAL, "cu_seqlens must be a contiguous [N+1] vector");
   if (!is_index(cu->dtype)) return fail(GDP_EINVAL, "cu_seqlens must be int32 or int64");
   return GDP_OK;

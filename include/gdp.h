@@ -54,7 +54,7 @@ enum gdp_status {
 
 /* A strided view of device memory.  data == NULL means "absent" (None).
  * shape/stride hold ndim valid entries; strides are in ELEMENTS.  The
- * innermost dimension must be contiguous (stride 1). */
+ * innermost dimension must be contiguous (stride 1, or a size of 1). */
 typedef struct gdp_tensor {
   void *data;
   int32_t dtype;
