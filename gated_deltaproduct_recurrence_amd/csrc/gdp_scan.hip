@@ -45,7 +45,7 @@
 //
 // What bounds it, measured on MI355X (a 1 GiB copy reaches 5.0 TB/s).  32768 x 2048
 // bfloat16 with float32 gates: 112 us, 4.8 TB/s of the operands' bytes; 131104 x 4096
-// of bfloat16 in 68 sequences, complement form: 700 us, 4.6 TB/s; forward and gradients
+// of bfloat16 in 68 sequences, complement form: 704 us, 4.6 TB/s; forward and gradients
 // of 8 x 4096 x 2048: 122 + 205 us, 4.4 and 4.6 TB/s.  The words add 7% to the bytes
 // read and 6% to those written.  Of a workgroup's 11.5 us on the second shape, 4 us are
 // its loads, 3 us the decays and maps (the vector units are issuing 60% of the time),
@@ -448,9 +448,10 @@ __global__ void __launch_bounds__(THREADS, 4) gdp_scan_kernel(ScanArgs a, int ti
 // behind, cut at the sequences' last rows (where d_final_state enters), and is
 // handed on between tiles the same way.  The states are formed again from the
 // checkpoint at the tile's first row.  Tiles of 64 rows: a lane holds the decays, the
-// factors of dg, d_o and (complement form) 1 - a of its rows, 116 registers for 8 rows
-// of a pair; at 80 registers, for three workgroups per CU, it spills (491 us instead
-// of 328 for a training step).
+// factors of dg, d_o and (complement form) 1 - a of its rows, 107 to 128 registers for
+// 8 rows of a pair (78 to 97 without 1 - a; the float32 complement form for few channel
+// blocks spills one); at 80 registers, for three workgroups per CU, the complement form
+// spills (491 us instead of 328 for a training step).
 template <typename XT, typename GT, bool COMPL, bool GROUPS>
 __global__ void __launch_bounds__(THREADS, 4) gdp_scan_backward_kernel(ScanArgs a, int tiles, int blocks) {
   constexpr int R = SCAN_ROWS / WAVES;
@@ -694,8 +695,8 @@ Grid grid_of(const ScanArgs &a, int rows, bool empties) {
 // Channel blocks up to which the states are handed on through groups of tiles.  The
 // workgroups that run at once then work on more tiles of each block, and how far the
 // known states come per look bounds the rate, not the memory: 131072 rows of 64, 256
-// and 512 channels take 41, 82 and 130 us through groups and 149, 167 and 177 without;
-// 1024 channels 227 and 221, and 131104 rows of 4096 channels 784 and 703.
+// and 512 channels take 39, 74 and 120 us through groups and 139, 155 and 167 without;
+// 1024 channels 220 and 216, and 131104 rows of 4096 channels 761 and 704.
 constexpr int NARROW = 4;
 
 hipError_t fill_words(const ScanArgs &a, const Grid &g, hipStream_t stream) {

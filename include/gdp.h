@@ -367,7 +367,8 @@ size_t gdp_gated_scan_workspace_bytes(int64_t T, int64_t N, int64_t D);
  *   output_final_state     write final_state when nonzero
  *   state_cache  [S, D]    f32 contiguous, or NULL; when given, the final state of
  *                          sequence i is written at slot state_indices[i]; an index
- *                          outside [0, S) writes nothing
+ *                          outside [0, S) writes nothing, two sequences naming one slot
+ *                          race (caller error)
  *   state_indices [N]      int32 or int64; required with state_cache
  *   return_checkpoints     write checkpoints when nonzero
  *   o            [T, D]    x's dtype, rows may be strided; the rows no sequence
