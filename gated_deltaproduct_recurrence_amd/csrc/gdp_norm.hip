@@ -40,46 +40,6 @@ namespace {
 
 constexpr int MAX_VALUES = 16;  // values a lane holds of one group
 
-// Sum over the lanes of an aligned team of LPG <= 64 lanes, in every lane: DPP
-// moves within 16 lanes, then the row swaps.
-template <int CTRL> __device__ __forceinline__ float dpp_add(float x) {
-  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
-}
-__device__ __forceinline__ float team_sum(float x, int lpg) {
-  if (lpg > 1) x = dpp_add<0xb1>(x);   // quad_perm 1,0,3,2
-  if (lpg > 2) x = dpp_add<0x4e>(x);   // quad_perm 2,3,0,1
-  if (lpg > 4) x = dpp_add<0x141>(x);  // row_half_mirror
-  if (lpg > 8) x = dpp_add<0x140>(x);  // row_mirror
-  if (lpg > 16) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-  if (lpg > 32) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
-  }
-  return x;
-}
-
-// ... of a team of whole waves (LPG > 64): the waves' sums through LDS.  `turn`
-// alternates the slots, so one barrier per sum is enough.
-template <int WIDE> struct Team {
-  int lpg, lane, first_wave;  // lanes per team, lane within it, its first wave in the workgroup
-  float (*slots)[16];         // [2][16]
-  int turn = 0;
-  __device__ float sum(float x) {
-    x = team_sum(x, WIDE ? 64 : lpg);
-    if constexpr (WIDE) {
-      if ((lane & 63) == 0) slots[turn][first_wave + (lane >> 6)] = x;
-      __syncthreads();
-      x = 0.f;
-      for (int v = 0; v < lpg >> 6; ++v) x += slots[turn][first_wave + v];
-      turn ^= 1;
-    }
-    return x;
-  }
-};
-
 // s = sigmoid(v): the hardware's exponential and reciprocal, each good to one step;
 // the product before them is rounded, which adds |v| 2^-24 relative to exp(-v)
 __device__ __forceinline__ float sigmoid(float v) {
