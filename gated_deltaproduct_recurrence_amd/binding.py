@@ -3,9 +3,9 @@
 Argument marshalling only: torch supplies device memory and the current
 stream; every step of the computation runs in the library's HIP kernels.  If
 the library is missing this module raises on import -- there is no fallback.
-The entries of the recurrence and of the norm also need the extension
-_records.so, built for this Python and torch; without it they raise when
-called, and the others work.
+The entries of the layers (gated scan, group norm, short convolution,
+selective scan, residual norm) also need the extension _records.so, built for
+this Python and torch; without it they raise when called, and the others work.
 """
 import ctypes
 import os
@@ -21,6 +21,7 @@ GDP_F32, GDP_BF16, GDP_I32, GDP_I64, GDP_F16 = 0, 1, 2, 3, 4
 GDP_OK, GDP_EINVAL, GDP_EUNSUPPORTED, GDP_EALIAS, GDP_EWORKSPACE, GDP_EHIP = 0, -1, -2, -3, -4, -5
 GDP_DBG_CU, GDP_DBG_SLOT, GDP_DBG_DUP = 1, 2, 4
 GDP_SCAN_CHECKPOINT_ROWS = 64
+GDP_SELECT_CHECKPOINT_ROWS = 16
 ACTIVATIONS = {None: 0, "none": 0, "silu": 1, "sigmoid": 2}  # gdp_activation
 STATUS_NAMES = {GDP_EINVAL: "GDP_EINVAL", GDP_EUNSUPPORTED: "GDP_EUNSUPPORTED", GDP_EALIAS: "GDP_EALIAS",
                 GDP_EWORKSPACE: "GDP_EWORKSPACE", GDP_EHIP: "GDP_EHIP"}
@@ -31,7 +32,12 @@ EXPORTED = ("gdp_descriptor_capacity", "gdp_build_descriptors", "gdp_workspace_b
             "gdp_debug_status", "gdp_last_error", "gdp_version", "gdp_chunk_prefill_noalloc",
             "gdp_gated_scan_workspace_bytes", "gdp_gated_scan", "gdp_gated_scan_decode",
             "gdp_gated_scan_backward_workspace_bytes", "gdp_gated_scan_backward", "gdp_group_norm",
-            "gdp_group_norm_backward_workspace_bytes", "gdp_group_norm_backward")
+            "gdp_group_norm_backward_workspace_bytes", "gdp_group_norm_backward",
+            "gdp_short_conv", "gdp_short_conv_decode", "gdp_short_conv_backward_workspace_bytes",
+            "gdp_short_conv_backward", "gdp_selective_scan_workspace_bytes", "gdp_selective_scan",
+            "gdp_selective_scan_decode", "gdp_selective_scan_backward_workspace_bytes",
+            "gdp_selective_scan_backward", "gdp_residual_norm", "gdp_residual_norm_backward_workspace_bytes",
+            "gdp_residual_norm_backward")
 
 
 class gdp_tensor(ctypes.Structure):
@@ -93,7 +99,7 @@ def _load(path=LIB_PATH):
                                                ctypes.c_void_p]
     lib.gdp_debug_status.restype = ctypes.c_int
     lib.gdp_debug_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int32, ctypes.c_void_p]
-    # the recurrence's and the norm's tensors cross as addresses of gdp_tensor records (_records)
+    # the layers' tensors cross as addresses of gdp_tensor records (_records)
     P, i32, i64, size = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     for name in ("gdp_gated_scan_workspace_bytes", "gdp_gated_scan_backward_workspace_bytes",
                  "gdp_group_norm_backward_workspace_bytes"):
@@ -109,6 +115,31 @@ def _load(path=LIB_PATH):
     lib.gdp_group_norm.argtypes = [P, P, P, P, i32, i32, ctypes.c_float, P, P]
     lib.gdp_group_norm_backward.restype = ctypes.c_int
     lib.gdp_group_norm_backward.argtypes = [P, P, P, P, i32, i32, ctypes.c_float, P, P, P, P, P, P, size, P]
+    lib.gdp_short_conv.restype = ctypes.c_int
+    lib.gdp_short_conv.argtypes = [P, P, P, i32, P, P, i32, P, P, P, P, P]
+    lib.gdp_short_conv_decode.restype = ctypes.c_int
+    lib.gdp_short_conv_decode.argtypes = [P, P, P, i32, P, P, P, P]
+    lib.gdp_short_conv_backward_workspace_bytes.restype = size
+    lib.gdp_short_conv_backward_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    lib.gdp_short_conv_backward.restype = ctypes.c_int
+    lib.gdp_short_conv_backward.argtypes = [P, P, P, i32, P, P, P, P, P, P, P, P, P, size, P]
+    lib.gdp_selective_scan_workspace_bytes.restype = size
+    lib.gdp_selective_scan_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    lib.gdp_selective_scan.restype = ctypes.c_int
+    lib.gdp_selective_scan.argtypes = [P, P, P, P, P, P, P, P, i32, P, P, i32, P, P, i32, P, P, P, P, size, P]
+    lib.gdp_selective_scan_decode.restype = ctypes.c_int
+    lib.gdp_selective_scan_decode.argtypes = [P, P, P, P, P, P, P, P, i32, P, P, P, P]
+    lib.gdp_selective_scan_backward_workspace_bytes.restype = size
+    lib.gdp_selective_scan_backward_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i32]
+    lib.gdp_selective_scan_backward.restype = ctypes.c_int
+    lib.gdp_selective_scan_backward.argtypes = [P, P, P, P, P, P, P, P, i32, *[P] * 15, size, P]
+    lib.gdp_residual_norm.restype = ctypes.c_int
+    lib.gdp_residual_norm.argtypes = [P, P, P, P, P, i32, i32, i32, ctypes.c_float, ctypes.c_float, P, P, P]
+    lib.gdp_residual_norm_backward_workspace_bytes.restype = size
+    lib.gdp_residual_norm_backward_workspace_bytes.argtypes = [i64, i64]
+    lib.gdp_residual_norm_backward.restype = ctypes.c_int
+    lib.gdp_residual_norm_backward.argtypes = [P, P, P, P, P, i32, i32, i32, ctypes.c_float, ctypes.c_float,
+                                               *[P] * 8, size, P]
     lib.gdp_last_error.restype = ctypes.c_char_p
     lib.gdp_last_error.argtypes = []
     lib.gdp_version.restype = ctypes.c_char_p
@@ -440,6 +471,96 @@ def gdp_group_norm_backward(x, weight, bias, gate, activation, subtract_mean, ep
           bool(subtract_mean), float(eps), *r[4:9], *_workspace_args(workspace, dev))
 
 
+def gdp_short_conv(x, weight, bias, activation, cu_seqlens, initial_state, output_final_state, state_cache,
+                   state_indices, y, final_state, stream=None):
+    """Direct call of the C entry point (caller-allocated outputs); `activation` is a key of ACTIVATIONS."""
+    dev = x.get_device()
+    r = _records(dev, x, weight, bias, cu_seqlens, initial_state, state_cache, state_indices, y, final_state)
+    _call(dev, stream, LIB.gdp_short_conv, r[0], r[1], r[2], _activation(activation), r[3], r[4],
+          bool(output_final_state), r[5], r[6], r[7], r[8])
+
+
+def gdp_short_conv_decode(x, weight, bias, activation, state_cache, state_indices, y, stream=None):
+    """Direct call of the C entry point; y is caller-allocated, state_cache is updated in place."""
+    dev = x.get_device()
+    r = _records(dev, x, weight, bias, state_cache, state_indices, y)
+    _call(dev, stream, LIB.gdp_short_conv_decode, r[0], r[1], r[2], _activation(activation), r[3], r[4], r[5])
+
+
+def gdp_short_conv_backward_workspace_bytes(T, N, D, W):
+    return int(LIB.gdp_short_conv_backward_workspace_bytes(T, N, D, W))
+
+
+def gdp_short_conv_backward(x, weight, bias, activation, cu_seqlens, initial_state, d_y, d_final_state, dx, dweight,
+                            dbias, d_initial_state, workspace, stream=None):
+    """Direct call of the C entry point (caller-allocated gradients and workspace)."""
+    dev = x.get_device()
+    r = _records(dev, x, weight, bias, cu_seqlens, initial_state, d_y, d_final_state, dx, dweight, dbias,
+                 d_initial_state)
+    _call(dev, stream, LIB.gdp_short_conv_backward, r[0], r[1], r[2], _activation(activation), *r[3:11],
+          *_workspace_args(workspace, dev))
+
+
+def gdp_selective_scan_workspace_bytes(T, N, D, G, S):
+    return int(LIB.gdp_selective_scan_workspace_bytes(T, N, D, G, S))
+
+
+def gdp_selective_scan(u, dt, A, B, C, skip, gate, dt_bias, dt_softplus, cu_seqlens, initial_state,
+                       output_final_state, state_cache, state_indices, return_checkpoints, o, final_state,
+                       checkpoints, workspace, stream=None):
+    """Direct call of the C entry point (caller-allocated outputs and workspace)."""
+    dev = u.get_device()
+    r = _records(dev, u, dt, A, B, C, skip, gate, dt_bias, cu_seqlens, initial_state, state_cache, state_indices, o,
+                 final_state, checkpoints)
+    _call(dev, stream, LIB.gdp_selective_scan, *r[:8], bool(dt_softplus), r[8], r[9], bool(output_final_state),
+          r[10], r[11], bool(return_checkpoints), r[12], r[13], r[14], *_workspace_args(workspace, dev))
+
+
+def gdp_selective_scan_decode(u, dt, A, B, C, skip, gate, dt_bias, dt_softplus, state_cache, state_indices, o,
+                              stream=None):
+    """Direct call of the C entry point; o is caller-allocated, state_cache is updated in place."""
+    dev = u.get_device()
+    r = _records(dev, u, dt, A, B, C, skip, gate, dt_bias, state_cache, state_indices, o)
+    _call(dev, stream, LIB.gdp_selective_scan_decode, *r[:8], bool(dt_softplus), r[8], r[9], r[10])
+
+
+def gdp_selective_scan_backward_workspace_bytes(T, N, D, G, S, with_checkpoints):
+    return int(LIB.gdp_selective_scan_backward_workspace_bytes(T, N, D, G, S, int(bool(with_checkpoints))))
+
+
+def gdp_selective_scan_backward(u, dt, A, B, C, skip, gate, dt_bias, dt_softplus, cu_seqlens, initial_state,
+                                checkpoints, d_o, d_final_state, du, ddt, dA, dB, dC, dskip, dgate, ddt_bias,
+                                d_initial_state, workspace, stream=None):
+    """Direct call of the C entry point (caller-allocated gradients and workspace)."""
+    dev = u.get_device()
+    r = _records(dev, u, dt, A, B, C, skip, gate, dt_bias, cu_seqlens, initial_state, checkpoints, d_o,
+                 d_final_state, du, ddt, dA, dB, dC, dskip, dgate, ddt_bias, d_initial_state)
+    _call(dev, stream, LIB.gdp_selective_scan_backward, *r[:8], bool(dt_softplus), *r[8:22],
+          *_workspace_args(workspace, dev))
+
+
+def gdp_residual_norm(x, y, post_weight, pre_weight, gate, activation, post_norm, pre_norm, residual_scale, eps, r, n,
+                      stream=None):
+    """Direct call of the C entry point (caller-allocated outputs; r may be x, updated in place)."""
+    dev = y.get_device()
+    t = _records(dev, x, y, post_weight, pre_weight, gate, r, n)
+    _call(dev, stream, LIB.gdp_residual_norm, *t[:5], _activation(activation), bool(post_norm), bool(pre_norm),
+          float(residual_scale), float(eps), t[5], t[6])
+
+
+def gdp_residual_norm_backward_workspace_bytes(T, D):
+    return int(LIB.gdp_residual_norm_backward_workspace_bytes(T, D))
+
+
+def gdp_residual_norm_backward(x, y, post_weight, pre_weight, gate, activation, post_norm, pre_norm, residual_scale,
+                               eps, d_r, d_n, dx, dy, dpost_weight, dpre_weight, dgate, workspace, stream=None):
+    """Direct call of the C entry point (caller-allocated gradients and workspace)."""
+    dev = y.get_device()
+    t = _records(dev, x, y, post_weight, pre_weight, gate, d_r, d_n, dx, dy, dpost_weight, dpre_weight, dgate)
+    _call(dev, stream, LIB.gdp_residual_norm_backward, *t[:5], _activation(activation), bool(post_norm),
+          bool(pre_norm), float(residual_scale), float(eps), *t[5:12], *_workspace_args(workspace, dev))
+
+
 def _activation(name):
     if name not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(k for k in ACTIVATIONS if k)} or None, got {name!r}")
@@ -606,3 +727,114 @@ def group_norm_backward(x, d_y, weight=None, bias=None, gate=None, activation=No
     gdp_group_norm_backward(x, weight, bias, gate, activation, subtract_mean, eps, d_y, dx, dw, db, dz,
                             _workspace(x, gdp_group_norm_backward_workspace_bytes(T, G, V)) if sums else None)
     return {"dx": dx, "dweight": dw, "dbias": db, "dgate": dz}
+
+
+def short_conv(x, weight, cu_seqlens, bias=None, activation=None, initial_state=None, output_final_state=False,
+               state_cache=None, state_indices=None, out=None):
+    """Allocating front end of the short causal convolution over packed sequences (x [T, D], weight [D, W], bias
+    [D]; activation None, "silu" or "sigmoid"): y_t = act(bias + sum_j weight[:, j] x_{t-W+1+j}).  States are the
+    W - 1 inputs before (initial_state) and at the end of (final state, state_cache) each sequence, [N, W-1, D] in
+    x's dtype.  Returns (y, final_state or None).  Rows that no sequence covers are left as they are in `out`."""
+    T, D = x.shape
+    N = cu_seqlens.shape[0] - 1
+    y = out if out is not None else _empty(x)
+    fs = _empty(x, (N, weight.shape[1] - 1, D)) if output_final_state else None
+    gdp_short_conv(x, weight, bias, activation, cu_seqlens, initial_state, output_final_state, state_cache,
+                   state_indices, y, fs)
+    return y, fs
+
+
+def short_conv_decode(x, weight, state_cache, state_indices, bias=None, activation=None, out=None):
+    """Allocating front end of the convolution's single-token step: returns y [N, D] in x's dtype; the state cache
+    [S, W-1, D] is updated in place."""
+    y = out if out is not None else _empty(x)
+    gdp_short_conv_decode(x, weight, bias, activation, state_cache, state_indices, y)
+    return y
+
+
+def short_conv_backward(x, weight, cu_seqlens, d_y, bias=None, activation=None, initial_state=None,
+                        d_final_state=None):
+    """Allocating front end of the convolution's gradients: returns a dict of dx (x's dtype), dweight, dbias (None
+    without a bias) and d_initial_state (None without an initial state), these three float32."""
+    T, D = x.shape
+    N, W = cu_seqlens.shape[0] - 1, weight.shape[1]
+    dx, dw = _empty(x), _empty(weight, dtype=torch.float32)
+    db = _empty(bias, dtype=torch.float32) if bias is not None else None
+    ds0 = _empty(initial_state, dtype=torch.float32) if initial_state is not None else None
+    gdp_short_conv_backward(x, weight, bias, activation, cu_seqlens, initial_state, d_y, d_final_state, dx, dw, db,
+                            ds0, _workspace(x, gdp_short_conv_backward_workspace_bytes(T, N, D, W)))
+    return {"dx": dx, "dweight": dw, "dbias": db, "d_initial_state": ds0}
+
+
+def selective_scan(u, dt, A, B, C, cu_seqlens, skip=None, gate=None, dt_bias=None, dt_softplus=False,
+                   initial_state=None, output_final_state=False, state_cache=None, state_indices=None,
+                   return_checkpoints=False, out=None):
+    """Allocating front end of the selective state space scan over packed sequences: with delta = dt + dt_bias (its
+    softplus with dt_softplus), h_t = exp(delta_t A) h_{t-1} + delta_t u_t B_t per channel and state, and
+    o_t = (C_t . h_t + skip u_t) silu(gate_t).  u, gate [T, D], dt [T, D] (float32 or u's dtype), A [D, S] float32,
+    B, C [T, G, S], skip, dt_bias [D] float32, states [N, D, S] float32.  Returns (o, final_state or None) or, with
+    return_checkpoints, (o, final_state or None, checkpoints), which selective_scan_backward takes.  Rows that no
+    sequence covers are left as they are in `out`."""
+    T, D = u.shape
+    N, G, S = cu_seqlens.shape[0] - 1, B.shape[1], A.shape[1]
+    o = out if out is not None else _empty(u)
+    fs = _empty(u, (N, D, S), torch.float32) if output_final_state else None
+    cp = _empty(u, (T // GDP_SELECT_CHECKPOINT_ROWS + N, S, D), torch.float32) if return_checkpoints else None
+    gdp_selective_scan(u, dt, A, B, C, skip, gate, dt_bias, dt_softplus, cu_seqlens, initial_state,
+                       output_final_state, state_cache, state_indices, return_checkpoints, o, fs, cp,
+                       _workspace(u, gdp_selective_scan_workspace_bytes(T, N, D, G, S)))
+    return (o, fs, cp) if return_checkpoints else (o, fs)
+
+
+def selective_scan_decode(u, dt, A, B, C, state_cache, state_indices, skip=None, gate=None, dt_bias=None,
+                          dt_softplus=False, out=None):
+    """Allocating front end of the selective scan's single-token step (u, dt, gate [N, D], B, C [N, G, S]): returns
+    o [N, D] in u's dtype; the state cache [S', D, S] is updated in place."""
+    o = out if out is not None else _empty(u)
+    gdp_selective_scan_decode(u, dt, A, B, C, skip, gate, dt_bias, dt_softplus, state_cache, state_indices, o)
+    return o
+
+
+def selective_scan_backward(u, dt, A, B, C, cu_seqlens, d_o, skip=None, gate=None, dt_bias=None, dt_softplus=False,
+                            initial_state=None, d_final_state=None, checkpoints=None):
+    """Allocating front end of the selective scan's gradients: returns a dict of du, dgate, dB, dC (u's dtype), ddt
+    (dt's dtype), dA, dskip, ddt_bias and d_initial_state (float32), None where the forward call had none.  Without
+    the forward call's `checkpoints` the states are formed again first."""
+    T, D = u.shape
+    N, G, S = cu_seqlens.shape[0] - 1, B.shape[1], A.shape[1]
+    du, ddt, dA, dB, dC = _empty(u), _empty(dt), _empty(A), _empty(B), _empty(C)
+    dskip, dz, dbias, ds0 = (None if t is None else _empty(t) for t in (skip, gate, dt_bias, initial_state))
+    gdp_selective_scan_backward(u, dt, A, B, C, skip, gate, dt_bias, dt_softplus, cu_seqlens, initial_state,
+                                checkpoints, d_o, d_final_state, du, ddt, dA, dB, dC, dskip, dz, dbias, ds0,
+                                _workspace(u, gdp_selective_scan_backward_workspace_bytes(
+                                    T, N, D, G, S, checkpoints is not None)))
+    return {"du": du, "ddt": ddt, "dA": dA, "dB": dB, "dC": dC, "dskip": dskip, "dgate": dz, "ddt_bias": dbias,
+            "d_initial_state": ds0}
+
+
+def residual_norm(x, y, post_weight=None, pre_weight=None, gate=None, activation=None, post_norm=True, pre_norm=True,
+                  residual_scale=1.0, eps=1e-5, out=None):
+    """Allocating front end of the norms around a block: with p = y rstd(y) post_weight (y post_weight without
+    post_norm), returns r = x + residual_scale act(gate) p, the next residual stream in x's dtype, and
+    n = r rstd(r) pre_weight, the next block's input in y's dtype (None without pre_norm).  x, y, gate [T, D],
+    weights [D]; activation None, "silu" or "sigmoid" is the gate's.  out=x updates the residual stream in place."""
+    r = out if out is not None else _empty(x)
+    n = _empty(y) if pre_norm else None
+    gdp_residual_norm(x, y, post_weight, pre_weight, gate, activation, post_norm, pre_norm, residual_scale, eps, r, n)
+    return r, n
+
+
+def residual_norm_backward(x, y, d_r, d_n, post_weight=None, pre_weight=None, gate=None, activation=None,
+                           post_norm=True, pre_norm=True, residual_scale=1.0, eps=1e-5):
+    """Allocating front end of the gradients of residual_norm for d_r (None for zeros) and d_n (None without
+    pre_norm): returns a dict of dx (x's dtype), dy and dgate (y's dtype), dpost_weight and dpre_weight (float32),
+    None where the forward call had none."""
+    T, D = y.shape
+    dx, dy = _empty(x), _empty(y)
+    dz = _empty(y) if gate is not None else None
+    dw, dv = (None if w is None else _empty(w, dtype=torch.float32) for w in (post_weight, pre_weight))
+    sums = post_weight is not None or pre_weight is not None
+    gdp_residual_norm_backward(x, y, post_weight, pre_weight, gate, activation, post_norm, pre_norm, residual_scale,
+                               eps, d_r, d_n, dx, dy, dw, dv, dz,
+                               _workspace(y, gdp_residual_norm_backward_workspace_bytes(T, D)) if sums else None)
+    return {"dx": dx, "dy": dy, "dgate": dz, "dpost_weight": dw, "dpre_weight": dv}

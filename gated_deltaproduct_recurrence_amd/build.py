@@ -14,7 +14,10 @@ SOURCES = [os.path.join(CSRC, "gdp_kernels.hip"), os.path.join(CSRC, "gdp_decode
            os.path.join(CSRC, "gdp_validate.hip"),
            os.path.join(CSRC, "gdp_noalloc.hip"),
            os.path.join(CSRC, "gdp_scan.hip"), os.path.join(CSRC, "gdp_norm.hip"),
-           os.path.join(CSRC, "gdp_layer_api.cpp"),
+           os.path.join(CSRC, "gdp_conv.hip"), os.path.join(CSRC, "gdp_select.hip"),
+           os.path.join(CSRC, "gdp_select_bwd.hip"), os.path.join(CSRC, "gdp_resnorm.hip"),
+           os.path.join(CSRC, "gdp_sums.hip"),
+           os.path.join(CSRC, "gdp_layer_api.cpp"), os.path.join(CSRC, "gdp_block_api.cpp"),
            os.path.join(CSRC, "gdp_api.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # the binding's CPython extension (host code only: torch tensors to gdp_tensor records)

@@ -1,0 +1,114 @@
+// gdp_block_common.h -- device helpers shared by the short convolution, the selective
+// scan and the norms around a block.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdp.h"
+#include "gdp_launch.h"
+#include "gdp_layer_common.h"
+
+namespace gdp {
+
+__device__ __forceinline__ int uniform_of(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// N neighbouring elements at any element's alignment: the memory instructions take
+// every alignment, so rows of odd lengths and views that start anywhere are read
+// and written in whole pieces too.
+template <typename T, int N> struct __attribute__((packed, aligned(sizeof(T)))) Piece { T v[N]; };
+
+// channels ch .. ch + N - 1 of a row of D; those behind its end read as 0 and are not written
+template <typename T, int N> __device__ __forceinline__ Piece<T, N> load_piece(const T *row, int ch, int D) {
+  if (ch + N <= D) return *(const Piece<T, N> *)(row + ch);
+  Piece<T, N> p;
+#pragma unroll
+  for (int c = 0; c < N; ++c) p.v[c] = ch + c < D ? row[ch + c] : (T)0.f;
+  return p;
+}
+template <typename T, int N> __device__ __forceinline__ void store_piece(T *row, int ch, int D, const Piece<T, N> &p) {
+  if (ch + N <= D) {
+    *(Piece<T, N> *)(row + ch) = p;
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+    if (ch + c < D) row[ch + c] = p.v[c];
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_floats(T *row, int ch, int D, const float (&x)[N]) {
+  Piece<T, N> p;
+#pragma unroll
+  for (int c = 0; c < N; ++c) p.v[c] = (T)x[c];
+  store_piece<T, N>(row, ch, D, p);
+}
+// element i of a parameter of type `type` (float32 or T)
+template <typename T> __device__ __forceinline__ float param_at(const void *p, int type, int64_t i) {
+  return type == EL_F32 ? ((const float *)p)[i] : (float)((const T *)p)[i];
+}
+
+// s = sigmoid(v): the hardware's exponential and reciprocal, each good to one step;
+// the product before them is rounded, which adds |v| 2^-24 relative to exp(-v).  The
+// reciprocal of an infinite sum is 0.
+__device__ __forceinline__ float sigmoid_of(float v) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -LOG2E_L));
+}
+__device__ __forceinline__ float act_of(int act, float v) {
+  if (act == GDP_ACT_NONE) return v;
+  const float s = sigmoid_of(v);
+  return act == GDP_ACT_SILU ? v * s : s;
+}
+// act(v) and act'(v)
+__device__ __forceinline__ float act_of(int act, float v, float *slope) {
+  if (act == GDP_ACT_NONE) {
+    *slope = 1.f;
+    return v;
+  }
+  const float s = sigmoid_of(v);
+  if (act == GDP_ACT_SILU) {
+    const float f = v * s;
+    *slope = fmaf(f, 1.f - s, s);  // s (1 + v (1 - s))
+    return f;
+  }
+  *slope = s * (1.f - s);
+  return s;
+}
+
+// A piece of one sequence: rows [begin, end) of sequence `seq`, whose rows are
+// [first, last).  Sequences are cut into chunks of 2^shift rows from their first
+// row on, so no chunk holds rows of two sequences.  Chunk c of sequence i has number
+//     (cu[i] >> shift) + i + c:
+// sequence i + 1 starts at least that many numbers later as sequence i has chunks, so
+// numbers are unique, rise with the rows, and lie below (T >> shift) + N; some name
+// no chunk.  An empty sequence has one chunk, without rows.
+struct Chunk {
+  int begin, end, first, last, seq, index;
+};
+// The chunk of a number, found by a whole wave (all 64 lanes) in steps of 64: false where
+// it names none.  Boundaries that do not rise give chunks that overlap or leave out rows, all
+// within [0, T) and [0, N).
+__device__ __forceinline__ bool find_chunk(Chunk *k, const void *cu, int is64, int T, int N, int shift, int number) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, hi = N, step;
+  do {
+    step = (hi - lo + 63) >> 6;
+    const int i = lo + lane * step;
+    const bool at = i < hi && ((int)bound_at(cu, is64, i, T) >> shift) + i <= number;
+    const int c = __popcll(__ballot(at));
+    if (c == 0) return false;
+    lo = uniform_of(lo + (c - 1) * step);
+    hi = min(hi, lo + step);
+  } while (step > 1);
+  k->seq = lo;
+  k->first = uniform_of((int)bound_at(cu, is64, lo, T));
+  k->last = max(k->first, uniform_of((int)bound_at(cu, is64, lo + 1, T)));
+  k->index = number - ((k->first >> shift) + lo);
+  const int64_t begin = k->first + ((int64_t)k->index << shift);
+  if (k->index < 0 || (k->index > 0 && begin >= k->last)) return false;
+  k->begin = (int)begin;
+  k->end = min((int64_t)k->last, begin + ((int64_t)1 << shift));
+  return true;
+}
+// numbers of chunks of 2^shift rows
+__host__ __device__ inline int64_t chunk_numbers(int64_t T, int64_t N, int shift) { return (T >> shift) + N; }
+
+}  // namespace gdp

@@ -1,0 +1,341 @@
+// gdp_select.hip -- gfx950 kernels of the selective state space scan over packed
+// sequences, per channel with S states,
+//     delta_t = softplus(dt_t + bias)  (or dt_t + bias),
+//     h_t = exp(delta_t A) h_{t-1} + delta_t u_t B_t,
+//     o_t = (C_t . h_t + skip u_t) silu(z_t),
+// and of its single-token step.  B and C are shared by the channels of a group.
+//
+// What bounds it is the vector units: per element and state one exponential and four
+// float32 operations, against 6 to 10 bytes per element.  So a lane holds a channel
+// with all its states in registers, and B_t and C_t, the same for a whole wave, are scalar
+// operands: they cost no vector registers, no LDS and no vector instructions.  A first
+// kernel lays them out for scalar loads (float32, whatever their type and alignment).
+//
+// The time axis: a wave walks one chunk of a sequence (gdp_block_common.h).  Where a call has few
+// channels and long sequences, chunks are short enough to fill the chip, and the
+// states that enter them come from two kernels before: the chunks' own ends (from a state
+// of 0; the decay over a chunk is exp(A sum delta), one sum per channel), and a walk over
+// the chunks of each sequence.  A sequence's last chunk takes no part in the first of them;
+// sequences of one chunk in neither.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdp.h"
+#include "gdp_block.h"
+#include "gdp_block_common.h"
+#include "gdp_select_common.h"
+
+namespace gdp {
+namespace {
+
+constexpr int WAVES = 4, ROWS = 4;  // waves per workgroup, rows in flight
+
+// B and C rows as float32 behind each other, zeros behind the last state
+template <typename T> __global__ void __launch_bounds__(256) gdp_select_stage_kernel(SelectArgs a, float *bc, int P) {
+  const int64_t all = (int64_t)a.T * a.G * 2 * P;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    const int n = (int)(i & (P - 1)), which = (int)(i / P & 1);
+    const int64_t row = i / (2 * P), t = row / a.G, g = row % a.G;
+    const T *p = which ? (const T *)a.C + t * a.C_st + g * a.C_sg : (const T *)a.B + t * a.B_st + g * a.B_sg;
+    bc[i] = n < a.S ? (float)p[n] : 0.f;
+  }
+}
+
+// A wave's chunk and channels
+struct Place { Chunk k; int number, ch, group; bool live; };
+__device__ __forceinline__ bool place_of(Place *p, const SelectArgs &a, const SelectGrid &g, int64_t jobs) {
+  const int64_t id = (int64_t)blockIdx.x * WAVES + uniform_of(threadIdx.x >> 6);
+  if (id >= jobs) return false;
+  p->number = (int)(id / g.blocks);
+  if (!find_chunk(&p->k, a.cu, a.cu_is64, a.T, a.N, g.shift, p->number)) return false;
+  const int b = (int)(id % g.blocks), per = a.D / a.G;
+  p->group = b / g.per_group;
+  const int at = (b % g.per_group) * 64 + (threadIdx.x & 63);
+  p->live = at < per;
+  p->ch = p->group * per + at;
+  return true;
+}
+
+template <typename UT, typename DT> struct Rows {
+  UT u[ROWS], z[ROWS];
+  DT dt[ROWS];
+};
+
+// The states at the ends of the chunks that another chunk follows, from initial_state
+// in a sequence's first chunk and from 0 elsewhere, and the sums of the steps.
+template <typename UT, typename DT, int P>
+__global__ void __launch_bounds__(64 * WAVES) gdp_select_ends_kernel(SelectArgs a, SelectGrid g, SelectSpace s,
+                                                                     int64_t jobs) {
+  Place p;
+  if (!place_of(&p, a, g, jobs) || p.k.end == p.k.last || !p.live) return;
+  const int ch = p.ch;
+  float A2[P], h[P];
+  load_rates<P>(A2, a, ch);
+#pragma unroll
+  for (int n = 0; n < P; ++n)
+    h[n] = a.s0 && p.k.index == 0 && n < a.S ? a.s0[((int64_t)p.k.seq * a.D + ch) * a.S + n] : 0.f;
+  const float bias = a.bias ? a.bias[ch] : 0.f;
+  const UT *u = (const UT *)a.u + ch;
+  const DT *dt = (const DT *)a.dt + ch;
+  Rows<UT, DT> next;
+  // (a chunk that another follows is full: a multiple of ROWS rows)
+  auto fetch = [&](int t) {
+    if (t < p.k.end) {
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        next.u[r] = u[(t + r) * a.u_st];
+        next.dt[r] = dt[(t + r) * a.dt_st];
+      }
+    }
+  };
+  fetch(p.k.begin);
+  float sum = 0.f;
+  for (int t = p.k.begin; t < p.k.end; t += ROWS) {
+    const Rows<UT, DT> now = next;
+    fetch(t + ROWS);
+    float part = 0.f;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const Scalars B = scalars(s.bc + ((int64_t)(t + r) * a.G + p.group) * 2 * P);
+      const float v = (float)now.dt[r] + bias, delta = a.softplus ? softplus_of(v) : v;
+      const float w = delta * (float)now.u[r];
+      part += delta;
+#pragma unroll
+      for (int n = 0; n < P; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(delta * A2[n]), h[n], w * B[n]);
+    }
+    sum += part;
+  }
+  float *out = s.states + (int64_t)p.number * P * a.D + ch;
+#pragma unroll
+  for (int n = 0; n < P; ++n) out[(int64_t)n * a.D] = h[n];
+  s.sums[(int64_t)p.number * a.D + ch] = sum;
+}
+
+// The states entering the chunks, in place of those at their ends: a lane walks the chunks
+// of a sequence for one state of one channel.
+template <int P>
+__global__ void __launch_bounds__(256) gdp_select_enter_kernel(SelectArgs a, SelectGrid g, SelectSpace s) {
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;  // n D + ch
+  if (at >= (int64_t)P * a.D) return;
+  const int n = (int)(at / a.D), ch = (int)(at % a.D);
+  const float A2 = n < a.S ? a.A[(int64_t)ch * a.S + n] * LOG2E_L : 0.f;
+  for (int i = blockIdx.y; i < a.N; i += gridDim.y) {
+    const int64_t first = bound_at(a.cu, a.cu_is64, i, a.T), len = bound_at(a.cu, a.cu_is64, i + 1, a.T) - first;
+    const int64_t chunks = (len + ((int64_t)1 << g.shift) - 1) >> g.shift;
+    if (chunks < 2) continue;
+    const int64_t step = (int64_t)P * a.D, number = (first >> g.shift) + i;
+    float *state = s.states + number * step + at;
+    const float *sum = s.sums + number * a.D + ch;
+    float h = *state;
+    constexpr int AHEAD = 8;
+    int64_t c = 1;
+    for (; c + AHEAD < chunks; c += AHEAD) {
+      float end[AHEAD], d[AHEAD];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        end[j] = state[(c + j) * step];
+        d[j] = sum[(c + j) * a.D];
+      }
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        state[(c + j) * step] = h;
+        h = fmaf(__builtin_amdgcn_exp2f(A2 * d[j]), h, end[j]);
+      }
+    }
+    for (; c < chunks; ++c) {
+      const float end = c + 1 < chunks ? state[c * step] : 0.f, d = c + 1 < chunks ? sum[c * a.D] : 0.f;
+      state[c * step] = h;
+      h = fmaf(__builtin_amdgcn_exp2f(A2 * d), h, end);
+    }
+  }
+}
+
+template <typename UT, typename DT, int P>
+__global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, SelectGrid g, SelectSpace s,
+                                                                int64_t jobs) {
+  Place p;
+  if (!place_of(&p, a, g, jobs) || !p.live) return;
+  const Chunk k = p.k;
+  const int ch = p.ch;
+  float A2[P], h[P];
+  load_rates<P>(A2, a, ch);
+  if (k.index > 0) {
+    const float *enter = s.states + (int64_t)p.number * P * a.D + ch;
+#pragma unroll
+    for (int n = 0; n < P; ++n) h[n] = enter[(int64_t)n * a.D];
+  } else {
+#pragma unroll
+    for (int n = 0; n < P; ++n) h[n] = a.s0 && n < a.S ? a.s0[((int64_t)k.seq * a.D + ch) * a.S + n] : 0.f;
+  }
+  if (k.begin < k.end) {
+    const float bias = a.bias ? a.bias[ch] : 0.f, skip = a.skip ? a.skip[ch] : 0.f;
+    const UT *u = (const UT *)a.u + ch, *z = (const UT *)a.z + ch;
+    const DT *dt = (const DT *)a.dt + ch;
+    UT *o = (UT *)a.o + ch;
+    Rows<UT, DT> next = {};
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r)
+        if (t + r < k.end) {
+          next.u[r] = u[(t + r) * a.u_st];
+          next.dt[r] = dt[(t + r) * a.dt_st];
+          if (a.z) next.z[r] = z[(t + r) * a.z_st];
+        }
+    };
+    auto row = [&](int t, UT ur, DT dtr, UT zr) {
+      const Scalars B = scalars(s.bc + ((int64_t)t * a.G + p.group) * 2 * P), C = B + P;
+      const float uf = (float)ur, v = (float)dtr + bias, delta = a.softplus ? softplus_of(v) : v;
+      const float w = delta * uf;
+      float y[4] = {skip * uf, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < P; ++n) {
+        h[n] = fmaf(__builtin_amdgcn_exp2f(delta * A2[n]), h[n], w * B[n]);
+        y[n & 3] = fmaf(h[n], C[n], y[n & 3]);
+      }
+      float out = (y[0] + y[1]) + (y[2] + y[3]);
+      if (a.z) out *= act_of(GDP_ACT_SILU, (float)zr);
+      if (a.o) o[t * a.o_st] = (UT)out;
+    };
+    fetch(k.begin);
+    for (int t = k.begin; t < k.end; t += ROWS) {
+      if (a.points && ((t - k.begin) & (SELECT_ROWS - 1)) == 0) {
+        const int64_t at = (k.first / SELECT_ROWS) + k.seq + (t - k.first) / SELECT_ROWS;
+        float *point = a.points + at * a.S * a.D + ch;
+#pragma unroll
+        for (int n = 0; n < P; ++n)
+          if (n < a.S) point[(int64_t)n * a.D] = h[n];
+      }
+      const Rows<UT, DT> now = next;
+      fetch(t + ROWS);
+      if (t + ROWS <= k.end) {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) row(t + r, now.u[r], now.dt[r], now.z[r]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < ROWS - 1; ++r)
+          if (t + r < k.end) row(t + r, now.u[r], now.dt[r], now.z[r]);
+      }
+    }
+  }
+  if (k.end != k.last) return;
+  if (a.final_state) {
+#pragma unroll
+    for (int n = 0; n < P; ++n)
+      if (n < a.S) a.final_state[((int64_t)k.seq * a.D + ch) * a.S + n] = h[n];
+  }
+  if (a.cache) {
+    const int64_t slot = index_at(a.slots, a.slots_is64, k.seq);
+    if (slot >= 0 && slot < a.num_slots) {
+#pragma unroll
+      for (int n = 0; n < P; ++n)
+        if (n < a.S) a.cache[(slot * a.D + ch) * a.S + n] = h[n];
+    }
+  }
+}
+
+// One token: a stream over the states that are named, four states per lane.
+template <typename UT, typename DT, int P>
+__global__ void __launch_bounds__(256) gdp_select_decode_kernel(SelectArgs a) {
+  constexpr int LANES = P / 4;  // of one channel
+  const int64_t i = blockIdx.x;
+  const int ch = (int)blockIdx.y * (256 / LANES) + threadIdx.x / LANES, n0 = (threadIdx.x % LANES) * 4;
+  if (ch >= a.D) return;
+  const int64_t slot = index_at(a.slots, a.slots_is64, i);
+  UT *o = (UT *)a.o + i * a.o_st + ch;
+  if (slot < 0 || slot >= a.num_slots) {
+    if (n0 == 0) *o = (UT)0.f;
+    return;
+  }
+  const int group = ch / (a.D / a.G);
+  float *state = a.cache + (slot * a.D + ch) * a.S;
+  const float *A = a.A + (int64_t)ch * a.S;
+  const Piece<float, 4> h = load_piece<float, 4>(state, n0, a.S), Av = load_piece<float, 4>(A, n0, a.S);
+  const Piece<UT, 4> B = load_piece<UT, 4>((const UT *)a.B + i * a.B_st + group * a.B_sg, n0, a.S),
+                     C = load_piece<UT, 4>((const UT *)a.C + i * a.C_st + group * a.C_sg, n0, a.S);
+  const float u = (float)((const UT *)a.u)[i * a.u_st + ch];
+  const float v = (float)((const DT *)a.dt)[i * a.dt_st + ch] + (a.bias ? a.bias[ch] : 0.f);
+  const float delta = a.softplus ? softplus_of(v) : v, w = delta * u;
+  Piece<float, 4> next;
+  float y = 0.f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    next.v[c] = fmaf(__builtin_amdgcn_exp2f(delta * (Av.v[c] * LOG2E_L)), h.v[c], w * (float)B.v[c]);
+    if (n0 + c < a.S) y = fmaf(next.v[c], (float)C.v[c], y);
+  }
+  store_piece<float, 4>(state, n0, a.S, next);
+  y = team_sum(y, LANES);
+  if (n0 == 0) {
+    y += a.skip ? a.skip[ch] * u : 0.f;
+    if (a.z) y *= act_of(GDP_ACT_SILU, (float)((const UT *)a.z)[i * a.z_st + ch]);
+    *o = (UT)y;
+  }
+}
+
+}  // namespace
+
+// A launch holds less than 2^32 threads: per block of 64 channels a wave for 32 rows and
+// for a sequence; B and C's layout is a loop.  The decode step: 256 threads per entry.
+bool select_served(int64_t T, int64_t N, int64_t D, int64_t G, int64_t S) {
+  if (T > BLOCK_MAX_ROWS || N > BLOCK_MAX_SEQS || D > BLOCK_MAX_CHANNELS) return false;
+  const int64_t blocks = G * ((D / G + 63) / 64);
+  return ((T >> 5) + N + 1) * blocks * 8 < ((int64_t)1 << 32) / 64 - WAVES &&
+         N * ((D + 31) / 32) < ((int64_t)1 << 32) / 256 && D <= 65535 * (int64_t)32;
+}
+
+size_t select_bytes(int64_t T, int64_t N, int64_t D, int64_t G, int64_t S) {
+  return select_space(nullptr, T, D, G, S, forward_grid(T, N, D, G).numbers).bytes;
+}
+
+hipError_t launch_select_stage(const SelectArgs &a, int ut, float *bc, hipStream_t stream) {
+  const int P = padded_states(a.S);
+  const int64_t want = ((int64_t)a.T * a.G * 2 * P + 255) / 256;
+  const dim3 grid((unsigned)(want < 4096 ? want : 4096));
+  if (want == 0) return hipSuccess;
+  if (ut == EL_F32)
+    hipLaunchKernelGGL(gdp_select_stage_kernel<float>, grid, dim3(256), 0, stream, a, bc, P);
+  else if (ut == EL_BF16)
+    hipLaunchKernelGGL(gdp_select_stage_kernel<bf16>, grid, dim3(256), 0, stream, a, bc, P);
+  else
+    hipLaunchKernelGGL(gdp_select_stage_kernel<_Float16>, grid, dim3(256), 0, stream, a, bc, P);
+  return hipGetLastError();
+}
+
+hipError_t launch_select(const SelectArgs &a, int ut, int dt, hipStream_t stream) {
+  const SelectGrid g = forward_grid(a.T, a.N, a.D, a.G);
+  const int64_t jobs = g.numbers * g.blocks;
+  if (jobs == 0 || a.N == 0) return hipSuccess;
+  const SelectSpace s = select_space(a.ws, a.T, a.D, a.G, a.S, g.numbers);
+  if (hipError_t e = launch_select_stage(a, ut, s.bc, stream)) return e;
+  return select_types(ut, dt, [&](auto u, auto d) {
+    using UT = decltype(u);
+    using DT = decltype(d);
+    return by_states(a.S, [&](auto n) {
+      constexpr int P = decltype(n)::value;
+      const dim3 grid((unsigned)((jobs + WAVES - 1) / WAVES)), threads(64 * WAVES);
+      if (a.T > (int64_t)1 << g.shift) {  // else no sequence has two chunks
+        hipLaunchKernelGGL((gdp_select_ends_kernel<UT, DT, P>), grid, threads, 0, stream, a, g, s, jobs);
+        if (hipError_t e = hipGetLastError()) return e;
+        const dim3 lanes((unsigned)(((int64_t)P * a.D + 255) / 256), (unsigned)(a.N < 256 ? a.N : 256));
+        hipLaunchKernelGGL(gdp_select_enter_kernel<P>, lanes, dim3(256), 0, stream, a, g, s);
+        if (hipError_t e = hipGetLastError()) return e;
+      }
+      hipLaunchKernelGGL((gdp_select_kernel<UT, DT, P>), grid, threads, 0, stream, a, g, s, jobs);
+      return hipGetLastError();
+    });
+  });
+}
+
+hipError_t launch_select_decode(const SelectArgs &a, int ut, int dt, hipStream_t stream) {
+  if (a.N == 0) return hipSuccess;
+  return select_types(ut, dt, [&](auto u, auto d) {
+    return by_states(a.S, [&](auto n) {
+      constexpr int P = decltype(n)::value, channels = 256 / (P / 4);
+      hipLaunchKernelGGL((gdp_select_decode_kernel<decltype(u), decltype(d), P>),
+                         dim3((unsigned)a.N, (unsigned)((a.D + channels - 1) / channels)), dim3(256), 0, stream, a);
+      return hipGetLastError();
+    });
+  });
+}
+
+}  // namespace gdp

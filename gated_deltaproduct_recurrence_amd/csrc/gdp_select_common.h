@@ -1,0 +1,104 @@
+// gdp_select_common.h -- device helpers of the selective scan's kernels
+// (gdp_select.hip, gdp_select_bwd.hip) and the layout of its workspace.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdp_block.h"
+#include "gdp_block_common.h"
+
+namespace gdp {
+
+// states of a channel as the kernels hold them: zeros behind the last one
+inline int padded_states(int64_t S) { return S <= 4 ? 4 : (S <= 8 ? 8 : (S <= 16 ? 16 : 32)); }
+
+// 64 channels of one group per wave
+struct SelectGrid {
+  int blocks, per_group, shift;  // channel blocks, those of one group, log2 of a chunk's rows
+  int64_t numbers;               // of chunks
+};
+inline SelectGrid select_grid(int64_t T, int64_t N, int64_t D, int64_t G, int64_t want, int least, int most) {
+  SelectGrid g;
+  g.per_group = (int)((D / G + 63) / 64);
+  g.blocks = (int)(G * g.per_group);
+  g.shift = most;
+  while (g.shift > least && (T >> g.shift) * g.blocks < want) --g.shift;
+  g.numbers = chunk_numbers(T, N, g.shift);
+  return g;
+}
+
+inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// The workspace's first part: B and C as float32, [T, G, 2, padded S] (the kernels read
+// them as scalars); then the chunks' states [numbers, padded S, D] and sums of steps
+// [numbers, D].
+struct SelectSpace {
+  float *bc, *states, *sums;
+  size_t bytes;
+};
+inline SelectSpace select_space(void *ws, int64_t T, int64_t D, int64_t G, int64_t S, int64_t numbers) {
+  const int64_t P = padded_states(S);
+  SelectSpace s;
+  char *p = (char *)ws;
+  size_t at = 0;
+  s.bc = (float *)p;
+  at += round256((size_t)T * G * 2 * P * 4);
+  s.states = (float *)(p + at);
+  at += round256((size_t)numbers * P * D * 4);
+  s.sums = (float *)(p + at);
+  at += round256((size_t)numbers * D * 4);
+  s.bytes = at;
+  return s;
+}
+
+typedef const float __attribute__((address_space(4))) *Scalars;  // read by scalar loads
+__device__ __forceinline__ Scalars scalars(const float *p) { return (Scalars)(uintptr_t)p; }
+
+// log(1 + e) for e in [0, 1]: 2 atanh(e / (2 + e)), whose odd series in q = e / (2 + e)
+// <= 1/3 is cut behind q^15 (the first term left out is below 2^-25 of the sum).
+__device__ __forceinline__ float log1p_of(float e) {
+  const float q = e * __builtin_amdgcn_rcpf(2.f + e), q2 = q * q;
+  float p = 1.f / 15.f;
+  p = fmaf(p, q2, 1.f / 13.f);
+  p = fmaf(p, q2, 1.f / 11.f);
+  p = fmaf(p, q2, 1.f / 9.f);
+  p = fmaf(p, q2, 1.f / 7.f);
+  p = fmaf(p, q2, 1.f / 5.f);
+  p = fmaf(p, q2, 1.f / 3.f);
+  p = fmaf(p, q2, 1.f);
+  return 2.f * q * p;
+}
+// softplus(v) = max(v, 0) + log(1 + exp(-|v|)); good to 4 steps where it is above 2^-126
+__device__ __forceinline__ float softplus_of(float v) {
+  return fmaxf(v, 0.f) + log1p_of(__builtin_amdgcn_exp2f(-fabsf(v) * LOG2E_L));
+}
+
+// A[ch] as base-2 exponents; zeros behind the last state
+template <int P> __device__ __forceinline__ void load_rates(float (&A2)[P], const SelectArgs &a, int ch) {
+#pragma unroll
+  for (int n = 0; n < P; ++n) A2[n] = n < a.S ? a.A[(int64_t)ch * a.S + n] * LOG2E_L : 0.f;
+}
+
+template <typename F> hipError_t select_types(int ut, int dt, F f) {
+  if (ut == EL_F32) return f((float)0, (float)0);
+  if (ut == EL_BF16) return dt == EL_F32 ? f((bf16)0, (float)0) : f((bf16)0, (bf16)0);
+  return dt == EL_F32 ? f((_Float16)0, (float)0) : f((_Float16)0, (_Float16)0);
+}
+template <int P> struct States { static constexpr int value = P; };
+template <typename F> hipError_t by_states(int64_t S, F f) {
+  switch (padded_states(S)) {
+    case 4: return f(States<4>());
+    case 8: return f(States<8>());
+    case 16: return f(States<16>());
+    default: return f(States<32>());
+  }
+}
+
+// the forward pass's chunks
+inline SelectGrid forward_grid(int64_t T, int64_t N, int64_t D, int64_t G) {
+  return select_grid(T, N, D, G, 4096, 5, 11);
+}
+// B and C into the workspace
+hipError_t launch_select_stage(const SelectArgs &a, int u_type, float *bc, hipStream_t stream);
+
+}  // namespace gdp

@@ -474,13 +474,212 @@ int gdp_group_norm_backward(const gdp_tensor *x, const gdp_tensor *weight, const
                             const gdp_tensor *dbias, const gdp_tensor *dgate, void *workspace,
                             size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * What stands around a recurrence in a layer: the short convolution before it, a
+ * selective state space scan in its place, and the norms before and after the
+ * block.  The conventions above hold here too.
+ * ------------------------------------------------------------------------ */
+
+/* Device.  Short causal convolution over packed sequences, channel by channel:
+ *     v_t = bias + sum_{j < W} weight[d, j] x_{t-W+1+j},   y_t = act(v_t),
+ * the W - 1 rows before a sequence's first being its initial state (or zeros).
+ *   x            [T, D]    f32, bf16 or f16; rows may be strided
+ *   weight       [D, W]    f32 or x's dtype, contiguous; 2 <= W <= 8 (GDP_EUNSUPPORTED
+ *                          otherwise)
+ *   bias         [D]       weight's dtype, contiguous, or data == NULL for zeros
+ *   activation   a gdp_activation
+ *   cu_seqlens   [N+1]     int32 or int64, contiguous
+ *   initial_state [N, W-1, D]  x's dtype, contiguous: the inputs before each sequence,
+ *                          oldest first; or data == NULL for zeros
+ *   output_final_state     write final_state when nonzero
+ *   state_cache  [S, W-1, D]  x's dtype, contiguous, or NULL; when given, the final state
+ *                          of sequence i is written at slot state_indices[i]; an index
+ *                          outside [0, S) writes nothing, two sequences naming one slot
+ *                          race (caller error)
+ *   state_indices [N]      int32 or int64; required with state_cache
+ *   y            [T, D]    x's dtype, rows may be strided; rows no sequence covers are left
+ *                          as they are
+ *   final_state  [N, W-1, D]  x's dtype, contiguous; required iff output_final_state: the
+ *                          last W - 1 inputs (of a shorter sequence, its initial state's
+ *                          last ones before them)
+ * Products and sums are float32, y is rounded once, states are copied.  No output may
+ * overlap an input or another output (GDP_EALIAS).  One launch on `stream`; capturable. */
+int gdp_short_conv(const gdp_tensor *x, const gdp_tensor *weight, const gdp_tensor *bias, int32_t activation,
+                   const gdp_tensor *cu_seqlens, const gdp_tensor *initial_state, int32_t output_final_state,
+                   const gdp_tensor *state_cache, const gdp_tensor *state_indices, const gdp_tensor *y,
+                   const gdp_tensor *final_state, void *stream);
+
+/* Device.  One token of the convolution per entry, on the state cache in place: for
+ * slot = state_indices[i] in [0, S), y[i] from the slot's W - 1 inputs and x[i], which
+ * then takes the place of the newest, the others moving up; the other entries (padding,
+ * -1) get a zero output row and touch no state.
+ *   x, y [N, D], weight, bias, activation as for gdp_short_conv; state_cache [S, W-1, D],
+ *   state_indices [N].  Two entries naming one slot race (caller error).  One launch on
+ *   `stream`; capturable. */
+int gdp_short_conv_decode(const gdp_tensor *x, const gdp_tensor *weight, const gdp_tensor *bias, int32_t activation,
+                          const gdp_tensor *state_cache, const gdp_tensor *state_indices, const gdp_tensor *y,
+                          void *stream);
+
+/* Host-only.  Workspace bytes gdp_short_conv_backward needs: partial sums of the weights'
+ * gradients.  0 for invalid sizes. */
+size_t gdp_short_conv_backward_workspace_bytes(int64_t T, int64_t N, int64_t D, int64_t W);
+
+/* Device.  Gradients of gdp_short_conv for d_y [T, D] of x's dtype and d_final_state
+ * [N, W-1, D] f32 (or data == NULL for zeros):
+ *   dx           [T, D]       x's dtype, rows may be strided; rows no sequence covers are
+ *                             written as zeros
+ *   dweight      [D, W], dbias [D] (iff a bias is given)  f32, contiguous, summed over the
+ *                             tokens in a fixed order
+ *   d_initial_state [N, W-1, D]  f32, contiguous, or data == NULL
+ *   workspace    at least gdp_short_conv_backward_workspace_bytes(...), 256-byte aligned
+ * v_t is formed again from x.  No gradient may overlap an input or another gradient
+ * (GDP_EALIAS).  Calls that share a workspace must be ordered.  Everything on `stream`, no
+ * allocation: capturable. */
+int gdp_short_conv_backward(const gdp_tensor *x, const gdp_tensor *weight, const gdp_tensor *bias, int32_t activation,
+                            const gdp_tensor *cu_seqlens, const gdp_tensor *initial_state, const gdp_tensor *d_y,
+                            const gdp_tensor *d_final_state, const gdp_tensor *dx, const gdp_tensor *dweight,
+                            const gdp_tensor *dbias, const gdp_tensor *d_initial_state, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* Rows of a sequence per checkpoint of the selective scan. */
+#define GDP_SELECT_CHECKPOINT_ROWS 16
+
+/* Host-only.  Workspace bytes gdp_selective_scan needs: B and C as float32, and the states
+ * at the ends of pieces of long sequences.  0 for invalid sizes. */
+size_t gdp_selective_scan_workspace_bytes(int64_t T, int64_t N, int64_t D, int64_t G, int64_t S);
+
+/* Device.  Selective state space scan over packed sequences, S states h per channel d:
+ *     delta_t = softplus(dt_t + dt_bias)  or, without dt_softplus,  dt_t + dt_bias,
+ *     h_t = exp(delta_t A) h_{t-1} + delta_t u_t B_t,
+ *     o_t = (C_t . h_t + skip u_t) silu(gate_t),
+ * from h = initial_state (or 0) in every sequence; without a gate the last factor is 1.
+ *   u            [T, D]    f32, bf16 or f16; rows may be strided
+ *   dt           [T, D]    f32 or u's dtype; rows may be strided
+ *   A            [D, S]    f32, contiguous, negative (delta_t A > 0 is served while the
+ *                          products of decays over 2048 rows stay finite in float32; what
+ *                          such a product below 2^-126 leaves of a state may be taken
+ *                          for 0); 1 <= S <= 32 (GDP_EUNSUPPORTED otherwise)
+ *   B, C         [T, G, S] u's dtype, tokens and groups may be strided; channel d reads
+ *                          group d / (D / G)
+ *   skip, dt_bias [D]      f32, contiguous, or data == NULL for zeros
+ *   gate         [T, D]    u's dtype, rows may be strided, or data == NULL
+ *   cu_seqlens   [N+1]     int32 or int64, contiguous
+ *   initial_state [N, D, S]  f32 contiguous, or data == NULL for zeros
+ *   output_final_state, state_cache [S', D, S] f32, state_indices [N]  as for gdp_gated_scan
+ *   return_checkpoints     write checkpoints when nonzero
+ *   o            [T, D]    u's dtype, rows may be strided; rows no sequence covers are left
+ *                          as they are
+ *   final_state  [N, D, S] f32 contiguous; required iff output_final_state; of an empty
+ *                          sequence its initial state
+ *   checkpoints  [T / 16 + N, S, D]  f32 contiguous: row cu_seqlens[i] / 16 + i + k holds
+ *                          the states entering row 16 k of sequence i, the other rows are
+ *                          unspecified; what gdp_selective_scan_backward reads
+ *   workspace    at least gdp_selective_scan_workspace_bytes(...), 256-byte aligned
+ * States are float32, o is rounded once.  A non-finite input stays within its sequence,
+ * and but for B and C within its channel.  No output may overlap an input or another output
+ * (GDP_EALIAS).  Calls that share a workspace must be ordered.  Two runs on the same inputs
+ * give the same bits.  Two to four launches on `stream`, no allocation: capturable. */
+int gdp_selective_scan(const gdp_tensor *u, const gdp_tensor *dt, const gdp_tensor *A, const gdp_tensor *B,
+                       const gdp_tensor *C, const gdp_tensor *skip, const gdp_tensor *gate, const gdp_tensor *dt_bias,
+                       int32_t dt_softplus, const gdp_tensor *cu_seqlens, const gdp_tensor *initial_state,
+                       int32_t output_final_state, const gdp_tensor *state_cache, const gdp_tensor *state_indices,
+                       int32_t return_checkpoints, const gdp_tensor *o, const gdp_tensor *final_state,
+                       const gdp_tensor *checkpoints, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Device.  One token of the selective scan per entry, on the state cache in place; entries
+ * whose slot lies outside [0, S') (padding, -1) get a zero output row and touch no state.
+ *   u, dt, gate, o [N, D], B, C [N, G, S] and the parameters as for gdp_selective_scan;
+ *   state_cache [S', D, S] f32 contiguous, state_indices [N] int32 or int64.  Two entries
+ *   naming one slot race (caller error).  One launch on `stream`; capturable. */
+int gdp_selective_scan_decode(const gdp_tensor *u, const gdp_tensor *dt, const gdp_tensor *A, const gdp_tensor *B,
+                              const gdp_tensor *C, const gdp_tensor *skip, const gdp_tensor *gate,
+                              const gdp_tensor *dt_bias, int32_t dt_softplus, const gdp_tensor *state_cache,
+                              const gdp_tensor *state_indices, const gdp_tensor *o, void *stream);
+
+/* Host-only.  Workspace bytes gdp_selective_scan_backward needs; without the forward call's
+ * checkpoints, room for them too.  0 for invalid sizes. */
+size_t gdp_selective_scan_backward_workspace_bytes(int64_t T, int64_t N, int64_t D, int64_t G, int64_t S,
+                                                   int32_t with_checkpoints);
+
+/* Device.  Gradients of gdp_selective_scan for d_o [T, D] of u's dtype and d_final_state
+ * [N, D, S] f32 (or data == NULL for zeros):
+ *   u .. initial_state   the forward call's
+ *   checkpoints  those of the forward call, or data == NULL: the states are then formed
+ *                again first
+ *   du, dgate    [T, D]    u's dtype, rows may be strided (dgate iff a gate is given)
+ *   ddt          [T, D]    dt's dtype, rows may be strided
+ *   dA           [D, S]    f32, contiguous
+ *   dB, dC       [T, G, S] u's dtype, contiguous: sums over the group's channels
+ *   dskip, ddt_bias [D]    f32, contiguous; iff skip, respectively dt_bias, is given
+ *   d_initial_state [N, D, S]  f32, contiguous, or data == NULL
+ *   workspace    at least gdp_selective_scan_backward_workspace_bytes(...), 256-byte aligned
+ * Rows no sequence covers are written as zeros; sums over tokens and channels are float32, in
+ * a fixed order.  No gradient may overlap an input or another gradient (GDP_EALIAS).
+ * Calls that share a workspace must be ordered.  Everything on `stream`, no allocation:
+ * capturable. */
+int gdp_selective_scan_backward(const gdp_tensor *u, const gdp_tensor *dt, const gdp_tensor *A, const gdp_tensor *B,
+                                const gdp_tensor *C, const gdp_tensor *skip, const gdp_tensor *gate,
+                                const gdp_tensor *dt_bias, int32_t dt_softplus, const gdp_tensor *cu_seqlens,
+                                const gdp_tensor *initial_state, const gdp_tensor *checkpoints, const gdp_tensor *d_o,
+                                const gdp_tensor *d_final_state, const gdp_tensor *du, const gdp_tensor *ddt,
+                                const gdp_tensor *dA, const gdp_tensor *dB, const gdp_tensor *dC,
+                                const gdp_tensor *dskip, const gdp_tensor *dgate, const gdp_tensor *ddt_bias,
+                                const gdp_tensor *d_initial_state, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/* Device.  The norms after a block and before the next one, with the block's gate, the
+ * residual scale and the residual sum between them.  Per token, over all D channels:
+ *     p = y rstd(y) post_weight,  or  y post_weight  without post_norm,
+ *     r = x + residual_scale f(gate) p,      n = r rstd(r) pre_weight,
+ * rstd(v) = 1 / sqrt(mean(v^2) + eps), f the gate's activation (1 without a gate).
+ *   x            [T, D]  residual stream, f32 or y's dtype; rows may be strided
+ *   y            [T, D]  block's output, f32, bf16 or f16; rows may be strided
+ *   post_weight, pre_weight [D]  f32 or y's dtype (one dtype for both), contiguous, or
+ *                data == NULL for ones; pre_weight only with pre_norm
+ *   gate         [T, D]  y's dtype, rows may be strided, or data == NULL
+ *   gate_activation  a gdp_activation; GDP_ACT_NONE without a gate
+ *   eps          at least 2^-126, finite
+ *   r            [T, D]  x's dtype, rows may be strided; it may be x itself (same address,
+ *                dtype and strides), which is then updated in place
+ *   n            [T, D]  y's dtype, rows may be strided; required iff pre_norm
+ * Sums and products are float32 (the squares of y and r must stay finite there); r and n
+ * are rounded once, n from the r before its rounding.  Otherwise no output may overlap
+ * an input or another output (GDP_EALIAS).  D <= 16384 (GDP_EUNSUPPORTED otherwise).  One
+ * launch on `stream`; capturable. */
+int gdp_residual_norm(const gdp_tensor *x, const gdp_tensor *y, const gdp_tensor *post_weight,
+                      const gdp_tensor *pre_weight, const gdp_tensor *gate, int32_t gate_activation, int32_t post_norm,
+                      int32_t pre_norm, float residual_scale, float eps, const gdp_tensor *r, const gdp_tensor *n,
+                      void *stream);
+
+/* Host-only.  Workspace bytes gdp_residual_norm_backward needs where a weight is given:
+ * partial sums of the weights' gradients.  0 for invalid sizes. */
+size_t gdp_residual_norm_backward_workspace_bytes(int64_t T, int64_t D);
+
+/* Device.  Gradients of gdp_residual_norm (the same inputs) for d_r [T, D] of x's dtype (or
+ * data == NULL for zeros, with pre_norm) and d_n [T, D] of y's dtype (iff pre_norm):
+ *   dx           [T, D]  x's dtype; dy, dgate (iff a gate is given) [T, D]  y's dtype; rows
+ *                may be strided
+ *   dpost_weight, dpre_weight [D]  f32, contiguous; iff the weight is given: summed over the
+ *                tokens in a fixed order
+ *   workspace    at least gdp_residual_norm_backward_workspace_bytes(...), 256-byte aligned;
+ *                not used without weights
+ * r is formed again from x, y and gate (a call that updated x in place has lost it).  No
+ * gradient may overlap an input or another gradient (GDP_EALIAS).  Calls that share a
+ * workspace must be ordered.  Everything on `stream`, no allocation: capturable. */
+int gdp_residual_norm_backward(const gdp_tensor *x, const gdp_tensor *y, const gdp_tensor *post_weight,
+                               const gdp_tensor *pre_weight, const gdp_tensor *gate, int32_t gate_activation,
+                               int32_t post_norm, int32_t pre_norm, float residual_scale, float eps,
+                               const gdp_tensor *d_r, const gdp_tensor *d_n, const gdp_tensor *dx,
+                               const gdp_tensor *dy, const gdp_tensor *dpost_weight, const gdp_tensor *dpre_weight,
+                               const gdp_tensor *dgate, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Debug validation of the data-dependent arguments.  These are not checked by
  * default, because checking them needs a read of device data.  A bad value stays
  * in bounds (every kernel clamps sequence ranges to [0, T] and skips slots
  * outside the cache), but the results are then undefined.  With the environment
  * variable GDP_DEBUG_VALIDATE=1, gdp_chunk_prefill (and the entries built on it),
- * gdp_recurrent_decode, gdp_gated_scan, gdp_gated_scan_decode and
- * gdp_gated_scan_backward first launch a check on their stream.  The check ORs
+ * gdp_recurrent_decode, the gated scan's, the short convolution's and the selective
+ * scan's entries first launch a check on their stream.  The check ORs
  * these bits into a word kept per device:
  *   GDP_DBG_CU    cu_seqlens decreases somewhere, or an entry lies outside [0, T]
  *                 (Megatron Core page, chunk_gated_delta_product_varlen: the
