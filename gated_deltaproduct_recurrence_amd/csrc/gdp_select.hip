@@ -57,9 +57,26 @@ __device__ __forceinline__ bool place_of(Place *p, const SelectArgs &a, const Se
   return true;
 }
 
-template <typename UT, typename DT> struct Rows {
-  UT u[ROWS], z[ROWS];
-  DT dt[ROWS];
+// M neighbouring rows of a lane's channel: raw, then as steps, weighted inputs and gates
+template <typename UT, typename DT, int M> struct Rows {
+  UT u[M], z[M];
+  DT dt[M];
+  __device__ __forceinline__ void load(const SelectArgs &a, int64_t t, int ch, bool gate) {
+#pragma unroll
+    for (int r = 0; r < M; ++r) {
+      u[r] = ((const UT *)a.u)[(t + r) * a.u_st + ch];
+      dt[r] = ((const DT *)a.dt)[(t + r) * a.dt_st + ch];
+      if (gate) z[r] = ((const UT *)a.z)[(t + r) * a.z_st + ch];
+    }
+  }
+  __device__ __forceinline__ void steps(float (&delta)[M], float bias, int softplus) const {
+#pragma unroll
+    for (int r = 0; r < M; ++r) delta[r] = (float)dt[r] + bias;
+    if (softplus) {
+#pragma unroll
+      for (int r = 0; r < M; ++r) delta[r] = softplus_of(delta[r]);
+    }
+  }
 };
 
 // The states at the ends of the chunks that another chunk follows, from initial_state
@@ -76,33 +93,24 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_ends_kernel(SelectArgs 
   for (int n = 0; n < P; ++n)
     h[n] = a.s0 && p.k.index == 0 && n < a.S ? a.s0[((int64_t)p.k.seq * a.D + ch) * a.S + n] : 0.f;
   const float bias = a.bias ? a.bias[ch] : 0.f;
-  const UT *u = (const UT *)a.u + ch;
-  const DT *dt = (const DT *)a.dt + ch;
-  Rows<UT, DT> next;
-  // (a chunk that another follows is full: a multiple of ROWS rows)
-  auto fetch = [&](int t) {
-    if (t < p.k.end) {
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        next.u[r] = u[(t + r) * a.u_st];
-        next.dt[r] = dt[(t + r) * a.dt_st];
-      }
-    }
-  };
-  fetch(p.k.begin);
+  Rows<UT, DT, ROWS> next = {};
+  next.load(a, p.k.begin, ch, false);
   float sum = 0.f;
-  for (int t = p.k.begin; t < p.k.end; t += ROWS) {
-    const Rows<UT, DT> now = next;
-    fetch(t + ROWS);
-    float part = 0.f;
+  const float *bc = s.bc + ((int64_t)p.k.begin * a.G + p.group) * 2 * P;
+  const int64_t bc_st = (int64_t)a.G * 2 * P;
+  // (a chunk that another follows is full: a multiple of ROWS rows)
+  for (int t = p.k.begin; t < p.k.end; t += ROWS, bc += ROWS * bc_st) {
+    const Rows<UT, DT, ROWS> now = next;
+    if (t + ROWS < p.k.end) next.load(a, t + ROWS, ch, false);
+    float delta[ROWS], part = 0.f;
+    now.steps(delta, bias, a.softplus);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      const Scalars B = scalars(s.bc + ((int64_t)(t + r) * a.G + p.group) * 2 * P);
-      const float v = (float)now.dt[r] + bias, delta = a.softplus ? softplus_of(v) : v;
-      const float w = delta * (float)now.u[r];
-      part += delta;
+      const Scalars B = scalars(bc + r * bc_st);
+      const float w = delta[r] * (float)now.u[r];
+      part += delta[r];
 #pragma unroll
-      for (int n = 0; n < P; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(delta * A2[n]), h[n], w * B[n]);
+      for (int n = 0; n < P; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(delta[r] * A2[n]), h[n], w * B[n]);
     }
     sum += part;
   }
@@ -170,52 +178,62 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
   }
   if (k.begin < k.end) {
     const float bias = a.bias ? a.bias[ch] : 0.f, skip = a.skip ? a.skip[ch] : 0.f;
-    const UT *u = (const UT *)a.u + ch, *z = (const UT *)a.z + ch;
-    const DT *dt = (const DT *)a.dt + ch;
-    UT *o = (UT *)a.o + ch;
-    Rows<UT, DT> next = {};
-    auto fetch = [&](int t) {
+    const bool gate = a.z != nullptr;
+    const float *bc = s.bc + ((int64_t)k.begin * a.G + p.group) * 2 * P;
+    const int64_t bc_st = (int64_t)a.G * 2 * P;
+    UT *o = (UT *)a.o + k.begin * a.o_st + ch;
+    // M rows of the recurrence
+    auto run = [&](auto &x) {
+      constexpr int M = sizeof(x.u) / sizeof(UT);
+      float delta[M], y[M];
+      x.steps(delta, bias, a.softplus);
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r)
-        if (t + r < k.end) {
-          next.u[r] = u[(t + r) * a.u_st];
-          next.dt[r] = dt[(t + r) * a.dt_st];
-          if (a.z) next.z[r] = z[(t + r) * a.z_st];
+      for (int r = 0; r < M; ++r) {
+        const Scalars B = scalars(bc), C = B + P;
+        bc += bc_st;
+        const float u = (float)x.u[r], w = delta[r] * u;
+        float s[2] = {skip * u, 0.f};
+#pragma unroll
+        for (int n = 0; n < P; ++n) {
+          h[n] = fmaf(__builtin_amdgcn_exp2f(delta[r] * A2[n]), h[n], w * B[n]);
+          s[n & 1] = fmaf(h[n], C[n], s[n & 1]);
         }
+        y[r] = s[0] + s[1];
+      }
+      if (gate) {
+#pragma unroll
+        for (int r = 0; r < M; ++r) y[r] *= act_of(GDP_ACT_SILU, (float)x.z[r]);
+      }
+      if (a.o) {
+#pragma unroll
+        for (int r = 0; r < M; ++r) {
+          *o = (UT)y[r];
+          o += a.o_st;
+        }
+      }
     };
-    auto row = [&](int t, UT ur, DT dtr, UT zr) {
-      const Scalars B = scalars(s.bc + ((int64_t)t * a.G + p.group) * 2 * P), C = B + P;
-      const float uf = (float)ur, v = (float)dtr + bias, delta = a.softplus ? softplus_of(v) : v;
-      const float w = delta * uf;
-      float y[4] = {skip * uf, 0.f, 0.f, 0.f};
+    Rows<UT, DT, ROWS> next = {};
+    const int whole = k.begin + ((k.end - k.begin) & ~(ROWS - 1));
+    if (k.begin < whole) next.load(a, k.begin, ch, gate);
+    auto point = [&](int t) {  // before row t, the first of 16
+      const int64_t at = (k.first / SELECT_ROWS) + k.seq + (t - k.first) / SELECT_ROWS;
+      float *out = a.points + at * a.S * a.D + ch;
 #pragma unroll
-      for (int n = 0; n < P; ++n) {
-        h[n] = fmaf(__builtin_amdgcn_exp2f(delta * A2[n]), h[n], w * B[n]);
-        y[n & 3] = fmaf(h[n], C[n], y[n & 3]);
-      }
-      float out = (y[0] + y[1]) + (y[2] + y[3]);
-      if (a.z) out *= act_of(GDP_ACT_SILU, (float)zr);
-      if (a.o) o[t * a.o_st] = (UT)out;
+      for (int n = 0; n < P; ++n)
+        if (n < a.S) out[(int64_t)n * a.D] = h[n];
     };
-    fetch(k.begin);
-    for (int t = k.begin; t < k.end; t += ROWS) {
-      if (a.points && ((t - k.begin) & (SELECT_ROWS - 1)) == 0) {
-        const int64_t at = (k.first / SELECT_ROWS) + k.seq + (t - k.first) / SELECT_ROWS;
-        float *point = a.points + at * a.S * a.D + ch;
-#pragma unroll
-        for (int n = 0; n < P; ++n)
-          if (n < a.S) point[(int64_t)n * a.D] = h[n];
-      }
-      const Rows<UT, DT> now = next;
-      fetch(t + ROWS);
-      if (t + ROWS <= k.end) {
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) row(t + r, now.u[r], now.dt[r], now.z[r]);
-      } else {
-#pragma unroll
-        for (int r = 0; r < ROWS - 1; ++r)
-          if (t + r < k.end) row(t + r, now.u[r], now.dt[r], now.z[r]);
-      }
+    int t = k.begin;
+    for (; t < whole; t += ROWS) {
+      if (a.points && ((t - k.begin) & (SELECT_ROWS - 1)) == 0) point(t);
+      const Rows<UT, DT, ROWS> now = next;
+      if (t + ROWS < whole) next.load(a, t + ROWS, ch, gate);
+      run(now);
+    }
+    if (a.points && t < k.end && ((t - k.begin) & (SELECT_ROWS - 1)) == 0) point(t);
+    for (; t < k.end; ++t) {
+      Rows<UT, DT, 1> one = {};
+      one.load(a, t, ch, gate);
+      run(one);
     }
   }
   if (k.end != k.last) return;

@@ -61,7 +61,12 @@ BackwardSpace backward_space(void *ws, int64_t T, int64_t N, int64_t D, int64_t 
 }
 static_assert(SELECT_ROWS == 16, "checkpoint numbers are chunk numbers of 2^4 rows");
 
-SelectGrid backward_grid(int64_t T, int64_t N, int64_t D, int64_t G) { return select_grid(T, N, D, G, 1024, 6, 11); }
+SelectGrid backward_grid(int64_t T, int64_t N, int64_t D, int64_t G) { return select_grid(T, N, D, G, 2048, 6, 11); }
+
+template <typename UT, typename DT, int M> struct Back {
+  UT d_o[M], z[M];
+  DT dt[M];
+};
 
 // The gradients of the states entering the chunks that follow another, of what the chunk's
 // own rows (and in a sequence's last chunk d_final_state) contribute, and the sums of
@@ -81,39 +86,58 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_starts_kernel(SelectArg
   for (int n = 0; n < P; ++n)
     e[n] = k.end == k.last && a.dfinal && n < a.S ? a.dfinal[((int64_t)k.seq * a.D + ch) * a.S + n] : 0.f;
   const float bias = a.bias ? a.bias[ch] : 0.f;
-  const UT *z = (const UT *)a.z + ch, *d_o = (const UT *)a.d_o + ch;
-  const DT *dt = (const DT *)a.dt + ch;
-  struct {
-    UT z[ROWS], d_o[ROWS];
-    DT dt[ROWS];
-  } next = {}, now;
-  auto fetch = [&](int t) {  // rows t, t - 1, ..
+  const bool gate = a.z != nullptr;
+  // rows t, t - 1, ..
+  auto load = [&](auto &x, int t) {
+    constexpr int M = sizeof(x.d_o) / sizeof(UT);
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r)
-      if (t - r >= k.begin) {
-        next.d_o[r] = d_o[(t - r) * a.do_st];
-        next.dt[r] = dt[(t - r) * a.dt_st];
-        if (a.z) next.z[r] = z[(t - r) * a.z_st];
-      }
+    for (int r = 0; r < M; ++r) {
+      x.d_o[r] = ((const UT *)a.d_o)[(t - r) * a.do_st + ch];
+      x.dt[r] = ((const DT *)a.dt)[(t - r) * a.dt_st + ch];
+      if (gate) x.z[r] = ((const UT *)a.z)[(t - r) * a.z_st + ch];
+    }
   };
-  fetch(k.end - 1);
+  const float *bc = s.bc + ((int64_t)(k.end - 1) * a.G + group) * 2 * P + P;  // C of the row
+  const int64_t bc_st = (int64_t)a.G * 2 * P;
   float sum = 0.f;
-  for (int t = k.end - 1; t >= k.begin; t -= ROWS) {
-    now = next;
-    fetch(t - ROWS);
-    float part = 0.f;
+  auto run = [&](const auto &x) {
+    constexpr int M = sizeof(x.d_o) / sizeof(UT);
+    float delta[M], gy[M], part = 0.f;
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      if (t - r < k.begin) continue;
-      const Scalars C = scalars(s.bc + ((int64_t)(t - r) * a.G + group) * 2 * P + P);
-      const float v = (float)now.dt[r] + bias, delta = a.softplus ? softplus_of(v) : v;
-      float gy = (float)now.d_o[r];
-      if (a.z) gy *= act_of(GDP_ACT_SILU, (float)now.z[r]);
-      part += delta;
+    for (int r = 0; r < M; ++r) {
+      delta[r] = (float)x.dt[r] + bias;
+      gy[r] = (float)x.d_o[r];
+    }
+    if (a.softplus) {
 #pragma unroll
-      for (int n = 0; n < P; ++n) e[n] = __builtin_amdgcn_exp2f(delta * A2[n]) * fmaf(C[n], gy, e[n]);
+      for (int r = 0; r < M; ++r) delta[r] = softplus_of(delta[r]);
+    }
+    if (gate) {
+#pragma unroll
+      for (int r = 0; r < M; ++r) gy[r] *= act_of(GDP_ACT_SILU, (float)x.z[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < M; ++r) {
+      const Scalars C = scalars(bc);
+      bc -= bc_st;
+      part += delta[r];
+#pragma unroll
+      for (int n = 0; n < P; ++n) e[n] = __builtin_amdgcn_exp2f(delta[r] * A2[n]) * fmaf(C[n], gy[r], e[n]);
     }
     sum += part;
+  };
+  int t = k.end - 1;
+  Back<UT, DT, ROWS> next = {};
+  if (t - ROWS + 1 >= k.begin) load(next, t);
+  for (; t - ROWS + 1 >= k.begin; t -= ROWS) {
+    const Back<UT, DT, ROWS> now = next;
+    if (t - 2 * ROWS + 1 >= k.begin) load(next, t - ROWS);
+    run(now);
+  }
+  for (; t >= k.begin; --t) {
+    Back<UT, DT, 1> one = {};
+    load(one, t);
+    run(one);
   }
   float *out = s.states + (int64_t)number * P * a.D + ch;
 #pragma unroll
@@ -177,19 +201,20 @@ template <int CTRL> __device__ __forceinline__ float add_within(float x, float y
   return keep + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(give), CTRL, 0xf, 0xf, true));
 }
 
-// LDS: five values per row and channel, then the waves' sums over their states
-struct Tile {
+// LDS: five values per row and channel, B and C, then the waves' sums over their states
+template <int P> struct alignas(16) Tile {
+  float bc[R][2][P];
   float delta[R][64], u[R][64], gy[R][64];
   float zs[R][64];  // d_o silu'(z)
   float ds[R][64];  // softplus'
 };
-struct Part { float through[HALF][64], carried[HALF][64], y[HALF][64]; };
+struct Part { float through[R][64], carried[R][64], y[R][64]; };
 
 template <typename UT, typename DT, int P>
-__global__ void __launch_bounds__(64 * (P / OWN)) gdp_select_backward_kernel(SelectArgs a, SelectGrid g,
-                                                                             BackwardSpace b) {
-  constexpr int W = P / OWN;
-  __shared__ Tile tile;
+__global__ void __launch_bounds__(64 * (P / OWN)) __attribute__((amdgpu_waves_per_eu(P > 4 ? 2 : 1)))
+gdp_select_backward_kernel(SelectArgs a, SelectGrid g, BackwardSpace b) {
+  constexpr int W = P / OWN, MINE = R / W;  // waves, rows of a block that a wave loads and finishes: w, w + W, ..
+  __shared__ Tile<P> tile;
   __shared__ Part parts[W];
   const int w = uniform_of(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int number = (int)(blockIdx.x / (unsigned)g.blocks), blk = (int)(blockIdx.x % (unsigned)g.blocks);
@@ -198,6 +223,12 @@ __global__ void __launch_bounds__(64 * (P / OWN)) gdp_select_backward_kernel(Sel
   const int ch = group * per + (live ? at : per - 1);  // lanes without a channel hold the last one's, as zeros
   Chunk k;
   const bool some = find_chunk(&k, a.cu, a.cu_is64, a.T, a.N, g.shift, number);
+  // the wave's places in LDS, as vector registers (as scalars every row's address is a
+  // scalar of its own, and they spill)
+  int mine = w;
+  asm("" : "+v"(mine));
+  const float *my_bc = &tile.bc[0][0][mine * OWN];
+  Part *my_part = (Part *)&parts[mine].through[0][lane];
   float A[OWN], A2[OWN], e[OWN], dA[OWN] = {}, dskip = 0.f, dbias = 0.f;
   const float skip = a.skip ? a.skip[ch] : 0.f;
 #pragma unroll
@@ -208,6 +239,7 @@ __global__ void __launch_bounds__(64 * (P / OWN)) gdp_select_backward_kernel(Sel
   }
   if (some) {
     const float bias = a.bias ? a.bias[ch] : 0.f;
+    const bool gate = a.z != nullptr;
     if (k.end < k.last) {
       const float *behind = b.s.states + ((int64_t)number * P + w * OWN) * a.D + ch;
 #pragma unroll
@@ -217,42 +249,77 @@ __global__ void __launch_bounds__(64 * (P / OWN)) gdp_select_backward_kernel(Sel
       for (int n = 0; n < OWN; ++n)
         if (live && w * OWN + n < a.S) e[n] = a.dfinal[((int64_t)k.seq * a.D + ch) * a.S + w * OWN + n];
     }
-    for (int t0 = k.begin + ((k.end - k.begin - 1) & ~(R - 1)); t0 >= k.begin && k.end > k.begin; t0 -= R) {
+    // a block's inputs, loaded a block ahead where a wave holds few rows of them
+    constexpr bool AHEAD = MINE <= 4;
+    UT u_[MINE] = {}, z_[MINE] = {}, do_[MINE] = {};
+    DT dt_[MINE] = {};
+    float point[OWN] = {}, bc_[2] = {};
+    auto fetch = [&](int t0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {  // 2 P floats per row: two per lane of the workgroup
+        const int q = threadIdx.x + i * 64 * W, r = q / (2 * P);
+        if (t0 + r < k.end) bc_[i] = b.s.bc[((int64_t)(t0 + r) * a.G + group) * 2 * P + q % (2 * P)];
+      }
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) {
+        const int64_t t = t0 + w + i * W;
+        if (t < k.end) {
+          u_[i] = ((const UT *)a.u)[t * a.u_st + ch];
+          dt_[i] = ((const DT *)a.dt)[t * a.dt_st + ch];
+          do_[i] = ((const UT *)a.d_o)[t * a.do_st + ch];
+          if (gate) z_[i] = ((const UT *)a.z)[t * a.z_st + ch];
+        }
+      }
+      const int64_t row = (k.first / R) + k.seq + (t0 - k.first) / R;
+      const float *p = a.points + (row * a.S + w * OWN) * a.D + ch;
+#pragma unroll
+      for (int n = 0; n < OWN; ++n)
+        if (w * OWN + n < a.S) point[n] = p[(int64_t)n * a.D];
+    };
+    int t0 = k.begin + ((k.end - k.begin - 1) & ~(R - 1));
+    if (AHEAD && k.begin < k.end) fetch(t0);
+    for (; t0 >= k.begin && k.begin < k.end; t0 -= R) {
       const int rows = min(R, k.end - t0);
+      if (!AHEAD) fetch(t0);
       // the rows' steps, inputs and output gradients, and the slopes for what follows
-      for (int r = w; r < R; r += W) {
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) {
+        const int r = w + i * W;
         float delta = 0.f, u = 0.f, gy = 0.f, zs = 0.f, ds = 0.f;
-        if (r < rows && live) {
-          const int64_t t = t0 + r;
-          const float v = (float)((const DT *)a.dt)[t * a.dt_st + ch] + bias;
-          u = (float)((const UT *)a.u)[t * a.u_st + ch];
-          gy = (float)((const UT *)a.d_o)[t * a.do_st + ch];
+        if (r < rows) {
+          const float v = (float)dt_[i] + bias;
+          u = live ? (float)u_[i] : 0.f;
+          gy = live ? (float)do_[i] : 0.f;
           delta = a.softplus ? softplus_of(v) : v;
           ds = a.softplus ? sigmoid_of(v) : 1.f;
-          if (a.z) {
-            const float f = act_of(GDP_ACT_SILU, (float)((const UT *)a.z)[t * a.z_st + ch], &zs);
+          if (gate) {
+            const float f = act_of(GDP_ACT_SILU, (float)z_[i], &zs);
             zs *= gy;
             gy *= f;
           }
         }
-        tile.delta[r][lane] = delta;
+        tile.delta[r][lane] = live ? delta : 0.f;
         tile.u[r][lane] = u;
-        tile.gy[r][lane] = gy;
+        tile.gy[r][lane] = live ? gy : 0.f;
         tile.zs[r][lane] = zs;
         tile.ds[r][lane] = ds;
       }
-      float h[R][OWN], d[R][OWN], last[OWN];  // states before the rows, decays; the state behind the block
-      {
-        const int64_t point = (k.first / R) + k.seq + (t0 - k.first) / R;
-        const float *p = a.points + (point * a.S + w * OWN) * a.D + ch;
 #pragma unroll
-        for (int n = 0; n < OWN; ++n) last[n] = live && w * OWN + n < a.S ? p[(int64_t)n * a.D] : 0.f;
-      }
-      const float *bc = b.s.bc + ((int64_t)t0 * a.G + group) * 2 * P + w * OWN;
-      const int64_t bc_st = (int64_t)a.G * 2 * P;
+      for (int i = 0; i < 2; ++i) (&tile.bc[0][0][0])[threadIdx.x + i * 64 * W] = bc_[i];
+      float h[R][OWN], d[R][OWN], last[OWN];  // states before the rows, decays; the state behind the block
+#pragma unroll
+      for (int n = 0; n < OWN; ++n) last[n] = live ? point[n] : 0.f;
       __syncthreads();
+      if (AHEAD && t0 > k.begin) fetch(t0 - R);
+      // (B and C as vector operands out of LDS: as scalars they made every wait one for all
+      // loads in flight, and the training step of 4 x 2048 x 2048 took 692 us, not 584)
+      auto four = [&](float (&x)[OWN], int r, int which) {
+        const float4 v = *(const float4 *)(my_bc + (r * 2 + which) * P);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+      };
       auto forward = [&](int r) {
-        const Scalars B = scalars(bc + r * bc_st);
+        float B[OWN];
+        four(B, r, 0);
         const float delta = tile.delta[r][lane], x = delta * tile.u[r][lane];
 #pragma unroll
         for (int n = 0; n < OWN; ++n) {
@@ -260,10 +327,13 @@ __global__ void __launch_bounds__(64 * (P / OWN)) gdp_select_backward_kernel(Sel
           d[r][n] = __builtin_amdgcn_exp2f(delta * A2[n]);
           last[n] = fmaf(d[r][n], last[n], x * B[n]);
         }
+        if (r % 2 == 1) __builtin_amdgcn_sched_barrier(0);  // or more rows' operands are read ahead than fit
       };
-      float through[HALF], carried[HALF], y[HALF], share[2 * HALF];
+      float share[2 * HALF];
       auto backward = [&](int r) {
-        const Scalars B = scalars(bc + r * bc_st), C = B + P;
+        float B[OWN], C[OWN];
+        four(B, r, 0);
+        four(C, r, 1);
         const int i = r & (HALF - 1);
         const float delta = tile.delta[r][lane], x = delta * tile.u[r][lane], gy = tile.gy[r][lane];
         float q[2 * OWN], s1 = 0.f, s2 = 0.f, s3 = 0.f;
@@ -280,67 +350,39 @@ __global__ void __launch_bounds__(64 * (P / OWN)) gdp_select_backward_kernel(Sel
           s2 = fmaf(c, A[n], s2);
           dA[n] = fmaf(c, delta, dA[n]);
         }
-        through[i] = s1;
-        carried[i] = s2;
-        y[i] = s3;
+        my_part->through[r][0] = s1;
+        my_part->carried[r][0] = s2;
+        my_part->y[r][0] = s3;
         // 16 lanes each of (q0, q2, q1, q3), and of (q4, q6, q5, q7)
         share[2 * i] = add_quarters(add_halves(q[0], q[1]), add_halves(q[2], q[3]));
         share[2 * i + 1] = add_quarters(add_halves(q[4], q[5]), add_halves(q[6], q[7]));
+        if (r % 2 == 0) __builtin_amdgcn_sched_barrier(0);
       };
-      // rows [first, first + HALF) of the block are done: their outputs
-      auto finish = [&](int first) {
-        {
-          const bool b3 = lane & 8, b2 = lane & 4, b1 = lane & 2, b0 = lane & 1;
-          float s[HALF], s4[HALF / 2], s2[HALF / 4];
+      // the sums over lanes of rows [first, first + HALF)
+      auto store_shares = [&](int first) {
+        const bool b3 = lane & 8, b2 = lane & 4, b1 = lane & 2, b0 = lane & 1;
+        float s[HALF], s4[HALF / 2], s2[HALF / 4];
 #pragma unroll
-          for (int i = 0; i < HALF; ++i) s[i] = add_within<0x140>(share[2 * i], share[2 * i + 1], b3);  // row_mirror
+        for (int i = 0; i < HALF; ++i) s[i] = add_within<0x140>(share[2 * i], share[2 * i + 1], b3);  // row_mirror
 #pragma unroll
-          for (int i = 0; i < HALF / 2; ++i) s4[i] = add_within<0x141>(s[2 * i], s[2 * i + 1], b2);  // row_half_mirror
+        for (int i = 0; i < HALF / 2; ++i) s4[i] = add_within<0x141>(s[2 * i], s[2 * i + 1], b2);  // row_half_mirror
 #pragma unroll
-          for (int i = 0; i < HALF / 4; ++i) s2[i] = add_within<0x4e>(s4[2 * i], s4[2 * i + 1], b1);  // quad 2, 3, 0, 1
-          const float one = add_within<0xb1>(s2[0], s2[1], b0);                                       // quad 1, 0, 3, 2
-          const int row = (b2 ? 1 : 0) + (b1 ? 2 : 0) + (b0 ? 4 : 0), part = lane >> 4;
-          const int n = part == 1 ? 2 : (part == 2 ? 1 : part);
-          if (first + row < rows)
-            b.shares[(((int64_t)blk * a.T + t0 + first + row) * 2 + (b3 ? 1 : 0)) * P + w * OWN + n] = one;
-        }
-        __syncthreads();  // the sums before are read
-#pragma unroll
-        for (int i = 0; i < HALF; ++i) {
-          parts[w].through[i][lane] = through[i];
-          parts[w].carried[i][lane] = carried[i];
-          if (a.z) parts[w].y[i][lane] = y[i];
-        }
-        __syncthreads();
-        for (int i = w; i < HALF && first + i < rows; i += W) {
-          float s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-          for (int v = 0; v < W; ++v) {
-            s1 += parts[v].through[i][lane];
-            s2 += parts[v].carried[i][lane];
-            if (a.z) s3 += parts[v].y[i][lane];
-          }
-          const int r = first + i;
-          const int64_t t = t0 + r;
-          const float u = tile.u[r][lane], gy = tile.gy[r][lane];
-          const float ddt = fmaf(u, s1, s2) * tile.ds[r][lane];
-          dskip = fmaf(gy, u, dskip);
-          dbias += ddt;
-          if (!live) continue;
-          ((UT *)a.du)[t * a.du_st + ch] = (UT)fmaf(tile.delta[r][lane], s1, skip * gy);
-          ((DT *)a.ddt)[t * a.ddt_st + ch] = (DT)ddt;
-          if (a.z) ((UT *)a.dz)[t * a.dz_st + ch] = (UT)(tile.zs[r][lane] * fmaf(skip, u, s3));
-        }
+        for (int i = 0; i < HALF / 4; ++i) s2[i] = add_within<0x4e>(s4[2 * i], s4[2 * i + 1], b1);  // quad 2, 3, 0, 1
+        const float one = add_within<0xb1>(s2[0], s2[1], b0);                                       // quad 1, 0, 3, 2
+        const int row = (b2 ? 1 : 0) + (b1 ? 2 : 0) + (b0 ? 4 : 0), part = lane >> 4;
+        const int n = part == 1 ? 2 : (part == 2 ? 1 : part);
+        if (first + row < rows)
+          b.shares[(((int64_t)blk * a.T + t0 + first + row) * 2 + (b3 ? 1 : 0)) * P + w * OWN + n] = one;
       };
       if (rows == R) {
 #pragma unroll
         for (int r = 0; r < R; ++r) forward(r);
 #pragma unroll
         for (int r = R - 1; r >= HALF; --r) backward(r);
-        finish(HALF);
+        store_shares(HALF);
 #pragma unroll
         for (int r = HALF - 1; r >= 0; --r) backward(r);
-        finish(0);
+        store_shares(0);
       } else {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -352,19 +394,41 @@ __global__ void __launch_bounds__(64 * (P / OWN)) gdp_select_backward_kernel(Sel
           }
         }
 #pragma unroll
-        for (int i = 0; i < HALF; ++i) through[i] = carried[i] = y[i] = share[2 * i] = share[2 * i + 1] = 0.f;
+        for (int i = 0; i < 2 * HALF; ++i) share[i] = 0.f;
         if (rows > HALF) {
 #pragma unroll
           for (int r = R - 2; r >= HALF; --r)
             if (r < rows) backward(r);
-          finish(HALF);
+          store_shares(HALF);
         }
 #pragma unroll
         for (int r = HALF - 1; r >= 0; --r)
           if (r < rows) backward(r);
-        finish(0);
+        store_shares(0);
       }
-      __syncthreads();  // the tile is read
+      __syncthreads();
+      // a wave's rows; it alone writes them in the tile again
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) {
+        const int r = w + i * W;
+        if (r >= rows) continue;
+        float s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+        for (int v = 0; v < W; ++v) {
+          s1 += parts[v].through[r][lane];
+          s2 += parts[v].carried[r][lane];
+          s3 += parts[v].y[r][lane];
+        }
+        const int64_t t = t0 + r;
+        const float u = tile.u[r][lane], gy = tile.gy[r][lane];
+        const float ddt = fmaf(u, s1, s2) * tile.ds[r][lane];
+        dskip = fmaf(gy, u, dskip);
+        dbias += ddt;
+        if (!live) continue;
+        ((UT *)a.du)[t * a.du_st + ch] = (UT)fmaf(tile.delta[r][lane], s1, skip * gy);
+        ((DT *)a.ddt)[t * a.ddt_st + ch] = (DT)ddt;
+        if (gate) ((UT *)a.dz)[t * a.dz_st + ch] = (UT)(tile.zs[r][lane] * fmaf(skip, u, s3));
+      }
     }
     if (k.index == 0 && a.ds0 && live) {
 #pragma unroll
