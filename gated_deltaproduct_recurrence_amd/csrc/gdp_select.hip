@@ -7,9 +7,9 @@
 //
 // What bounds it is the vector units: per element and state one exponential and four
 // float32 operations, against 6 to 10 bytes per element.  So a lane holds a channel
-// with all its states in registers, and B_t and C_t, the same for a whole wave, are scalar
-// operands: they cost no vector registers, no LDS and no vector instructions.  A first
-// kernel lays them out for scalar loads (float32, whatever their type and alignment).
+// with all its states in registers, and B_t and C_t, the same for a whole wave, come to it
+// from the wave's own LDS, four states per read.  A first kernel lays them out for
+// that (float32, zeros behind the last state, whatever their type and alignment).
 //
 // The time axis: a wave walks one chunk of a sequence (gdp_block_common.h).  Where a call has few
 // channels and long sequences, chunks are short enough to fill the chip, and the
@@ -53,7 +53,7 @@ __device__ __forceinline__ bool place_of(Place *p, const SelectArgs &a, const Se
   p->group = b / g.per_group;
   const int at = (b % g.per_group) * 64 + (threadIdx.x & 63);
   p->live = at < per;
-  p->ch = p->group * per + at;
+  p->ch = p->group * per + min(at, per - 1);  // lanes without a channel work on the last one's, and write nothing
   return true;
 }
 
@@ -84,8 +84,9 @@ template <typename UT, typename DT, int M> struct Rows {
 template <typename UT, typename DT, int P>
 __global__ void __launch_bounds__(64 * WAVES) gdp_select_ends_kernel(SelectArgs a, SelectGrid g, SelectSpace s,
                                                                      int64_t jobs) {
+  __shared__ __attribute__((aligned(16))) float lds[WAVES][ROWS * P];
   Place p;
-  if (!place_of(&p, a, g, jobs) || p.k.end == p.k.last || !p.live) return;
+  if (!place_of(&p, a, g, jobs) || p.k.end == p.k.last) return;
   const int ch = p.ch;
   float A2[P], h[P];
   load_rates<P>(A2, a, ch);
@@ -93,27 +94,41 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_ends_kernel(SelectArgs 
   for (int n = 0; n < P; ++n)
     h[n] = a.s0 && p.k.index == 0 && n < a.S ? a.s0[((int64_t)p.k.seq * a.D + ch) * a.S + n] : 0.f;
   const float bias = a.bias ? a.bias[ch] : 0.f;
-  Rows<UT, DT, ROWS> next = {};
-  next.load(a, p.k.begin, ch, false);
-  float sum = 0.f;
+  float *mine = lds[threadIdx.x >> 6];
   const float *bc = s.bc + ((int64_t)p.k.begin * a.G + p.group) * 2 * P;
   const int64_t bc_st = (int64_t)a.G * 2 * P;
+  Rows<UT, DT, ROWS> next = {};
+  Shared<ROWS, P> next_b;
+  next.load(a, p.k.begin, ch, false);
+  next_b.load(bc, bc_st);
+  float sum = 0.f;
   // (a chunk that another follows is full: a multiple of ROWS rows)
-  for (int t = p.k.begin; t < p.k.end; t += ROWS, bc += ROWS * bc_st) {
+  for (int t = p.k.begin; t < p.k.end; t += ROWS) {
     const Rows<UT, DT, ROWS> now = next;
-    if (t + ROWS < p.k.end) next.load(a, t + ROWS, ch, false);
+    next_b.lay(mine);
+    bc += ROWS * bc_st;
+    if (t + ROWS < p.k.end) {
+      next.load(a, t + ROWS, ch, false);
+      next_b.load(bc, bc_st);
+    }
     float delta[ROWS], part = 0.f;
     now.steps(delta, bias, a.softplus);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      const Scalars B = scalars(bc + r * bc_st);
       const float w = delta[r] * (float)now.u[r];
       part += delta[r];
 #pragma unroll
-      for (int n = 0; n < P; ++n) h[n] = fmaf(__builtin_amdgcn_exp2f(delta[r] * A2[n]), h[n], w * B[n]);
+      for (int n = 0; n < P; n += 4) {
+        const float4 B = *(const float4 *)(mine + r * P + n);
+        h[n] = fmaf(__builtin_amdgcn_exp2f(delta[r] * A2[n]), h[n], w * B.x);
+        h[n + 1] = fmaf(__builtin_amdgcn_exp2f(delta[r] * A2[n + 1]), h[n + 1], w * B.y);
+        h[n + 2] = fmaf(__builtin_amdgcn_exp2f(delta[r] * A2[n + 2]), h[n + 2], w * B.z);
+        h[n + 3] = fmaf(__builtin_amdgcn_exp2f(delta[r] * A2[n + 3]), h[n + 3], w * B.w);
+      }
     }
     sum += part;
   }
+  if (!p.live) return;
   float *out = s.states + (int64_t)p.number * P * a.D + ch;
 #pragma unroll
   for (int n = 0; n < P; ++n) out[(int64_t)n * a.D] = h[n];
@@ -162,8 +177,9 @@ __global__ void __launch_bounds__(256) gdp_select_enter_kernel(SelectArgs a, Sel
 template <typename UT, typename DT, int P>
 __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, SelectGrid g, SelectSpace s,
                                                                 int64_t jobs) {
+  __shared__ __attribute__((aligned(16))) float lds[WAVES][ROWS * 2 * P];
   Place p;
-  if (!place_of(&p, a, g, jobs) || !p.live) return;
+  if (!place_of(&p, a, g, jobs)) return;
   const Chunk k = p.k;
   const int ch = p.ch;
   float A2[P], h[P];
@@ -179,24 +195,28 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
   if (k.begin < k.end) {
     const float bias = a.bias ? a.bias[ch] : 0.f, skip = a.skip ? a.skip[ch] : 0.f;
     const bool gate = a.z != nullptr;
+    float *mine = lds[threadIdx.x >> 6];
     const float *bc = s.bc + ((int64_t)k.begin * a.G + p.group) * 2 * P;
     const int64_t bc_st = (int64_t)a.G * 2 * P;
     UT *o = (UT *)a.o + k.begin * a.o_st + ch;
     // M rows of the recurrence
-    auto run = [&](auto &x) {
+    auto run = [&](const auto &x) {
       constexpr int M = sizeof(x.u) / sizeof(UT);
       float delta[M], y[M];
       x.steps(delta, bias, a.softplus);
 #pragma unroll
       for (int r = 0; r < M; ++r) {
-        const Scalars B = scalars(bc), C = B + P;
-        bc += bc_st;
         const float u = (float)x.u[r], w = delta[r] * u;
         float s[2] = {skip * u, 0.f};
 #pragma unroll
-        for (int n = 0; n < P; ++n) {
-          h[n] = fmaf(__builtin_amdgcn_exp2f(delta[r] * A2[n]), h[n], w * B[n]);
-          s[n & 1] = fmaf(h[n], C[n], s[n & 1]);
+        for (int n = 0; n < P; n += 4) {
+          const float4 Bv = *(const float4 *)(mine + r * 2 * P + n), Cv = *(const float4 *)(mine + (r * 2 + 1) * P + n);
+          const float B[4] = {Bv.x, Bv.y, Bv.z, Bv.w}, C[4] = {Cv.x, Cv.y, Cv.z, Cv.w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            h[n + c] = fmaf(__builtin_amdgcn_exp2f(delta[r] * A2[n + c]), h[n + c], w * B[c]);
+            s[c & 1] = fmaf(h[n + c], C[c], s[c & 1]);
+          }
         }
         y[r] = s[0] + s[1];
       }
@@ -204,39 +224,50 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
 #pragma unroll
         for (int r = 0; r < M; ++r) y[r] *= act_of(GDP_ACT_SILU, (float)x.z[r]);
       }
-      if (a.o) {
+      if (a.o && p.live) {
 #pragma unroll
-        for (int r = 0; r < M; ++r) {
-          *o = (UT)y[r];
-          o += a.o_st;
-        }
+        for (int r = 0; r < M; ++r) o[r * a.o_st] = (UT)y[r];
       }
+      o += M * a.o_st;
     };
     Rows<UT, DT, ROWS> next = {};
+    Shared<ROWS, 2 * P> next_bc;
     const int whole = k.begin + ((k.end - k.begin) & ~(ROWS - 1));
-    if (k.begin < whole) next.load(a, k.begin, ch, gate);
+    if (k.begin < whole) {
+      next.load(a, k.begin, ch, gate);
+      next_bc.load(bc, bc_st);
+    }
     auto point = [&](int t) {  // before row t, the first of 16
       const int64_t at = (k.first / SELECT_ROWS) + k.seq + (t - k.first) / SELECT_ROWS;
       float *out = a.points + at * a.S * a.D + ch;
 #pragma unroll
       for (int n = 0; n < P; ++n)
-        if (n < a.S) out[(int64_t)n * a.D] = h[n];
+        if (n < a.S && p.live) out[(int64_t)n * a.D] = h[n];
     };
     int t = k.begin;
     for (; t < whole; t += ROWS) {
       if (a.points && ((t - k.begin) & (SELECT_ROWS - 1)) == 0) point(t);
       const Rows<UT, DT, ROWS> now = next;
-      if (t + ROWS < whole) next.load(a, t + ROWS, ch, gate);
+      next_bc.lay(mine);
+      bc += ROWS * bc_st;
+      if (t + ROWS < whole) {
+        next.load(a, t + ROWS, ch, gate);
+        next_bc.load(bc, bc_st);
+      }
       run(now);
     }
     if (a.points && t < k.end && ((t - k.begin) & (SELECT_ROWS - 1)) == 0) point(t);
     for (; t < k.end; ++t) {
       Rows<UT, DT, 1> one = {};
+      Shared<1, 2 * P> one_bc;
       one.load(a, t, ch, gate);
+      one_bc.load(bc, bc_st);
+      one_bc.lay(mine);
+      bc += bc_st;
       run(one);
     }
   }
-  if (k.end != k.last) return;
+  if (k.end != k.last || !p.live) return;
   if (a.final_state) {
 #pragma unroll
     for (int n = 0; n < P; ++n)

@@ -77,9 +77,11 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_starts_kernel(SelectArg
   const int64_t id = (int64_t)blockIdx.x * WAVES + uniform_of(threadIdx.x >> 6);
   if (id >= jobs) return;
   const int number = (int)(id / g.blocks), b = (int)(id % g.blocks), per = a.D / a.G, group = b / g.per_group;
-  const int at = (b % g.per_group) * 64 + (threadIdx.x & 63), ch = group * per + at;
+  const int at = (b % g.per_group) * 64 + (threadIdx.x & 63), ch = group * per + min(at, per - 1);
+  __shared__ __attribute__((aligned(16))) float lds[WAVES][ROWS * P];
+  float *mine = lds[threadIdx.x >> 6];
   Chunk k;
-  if (!find_chunk(&k, a.cu, a.cu_is64, a.T, a.N, g.shift, number) || k.index == 0 || at >= per) return;
+  if (!find_chunk(&k, a.cu, a.cu_is64, a.T, a.N, g.shift, number) || k.index == 0) return;
   float A2[P], e[P];
   load_rates<P>(A2, a, ch);
 #pragma unroll
@@ -118,27 +120,45 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_starts_kernel(SelectArg
     }
 #pragma unroll
     for (int r = 0; r < M; ++r) {
-      const Scalars C = scalars(bc);
-      bc -= bc_st;
       part += delta[r];
 #pragma unroll
-      for (int n = 0; n < P; ++n) e[n] = __builtin_amdgcn_exp2f(delta[r] * A2[n]) * fmaf(C[n], gy[r], e[n]);
+      for (int n = 0; n < P; n += 4) {
+        const float4 v = *(const float4 *)(mine + r * P + n);
+        const float C[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          e[n + c] = __builtin_amdgcn_exp2f(delta[r] * A2[n + c]) * fmaf(C[c], gy[r], e[n + c]);
+      }
     }
     sum += part;
   };
   int t = k.end - 1;
   Back<UT, DT, ROWS> next = {};
-  if (t - ROWS + 1 >= k.begin) load(next, t);
+  Shared<ROWS, P> next_c;
+  if (t - ROWS + 1 >= k.begin) {
+    load(next, t);
+    next_c.load(bc, -bc_st);
+  }
   for (; t - ROWS + 1 >= k.begin; t -= ROWS) {
     const Back<UT, DT, ROWS> now = next;
-    if (t - 2 * ROWS + 1 >= k.begin) load(next, t - ROWS);
+    next_c.lay(mine);
+    bc -= ROWS * bc_st;
+    if (t - 2 * ROWS + 1 >= k.begin) {
+      load(next, t - ROWS);
+      next_c.load(bc, -bc_st);
+    }
     run(now);
   }
   for (; t >= k.begin; --t) {
     Back<UT, DT, 1> one = {};
+    Shared<1, P> one_c;
     load(one, t);
+    one_c.load(bc, -bc_st);
+    one_c.lay(mine);
+    bc -= bc_st;
     run(one);
   }
+  if (at >= per) return;
   float *out = s.states + (int64_t)number * P * a.D + ch;
 #pragma unroll
   for (int n = 0; n < P; ++n) out[(int64_t)n * a.D] = e[n];
@@ -311,8 +331,7 @@ gdp_select_backward_kernel(SelectArgs a, SelectGrid g, BackwardSpace b) {
       for (int n = 0; n < OWN; ++n) last[n] = live ? point[n] : 0.f;
       __syncthreads();
       if (AHEAD && t0 > k.begin) fetch(t0 - R);
-      // (B and C as vector operands out of LDS: as scalars they made every wait one for all
-      // loads in flight, and the training step of 4 x 2048 x 2048 took 692 us, not 584)
+      // (B and C out of LDS: as scalars the training step of 4 x 2048 x 2048 took 692 us, not 584)
       auto four = [&](float (&x)[OWN], int r, int which) {
         const float4 v = *(const float4 *)(my_bc + (r * 2 + which) * P);
         x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;

@@ -29,8 +29,7 @@ inline SelectGrid select_grid(int64_t T, int64_t N, int64_t D, int64_t G, int64_
 
 inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// The workspace's first part: B and C as float32, [T, G, 2, padded S] (the kernels read
-// them as scalars); then the chunks' states [numbers, padded S, D] and sums of steps
+// The workspace's first part: B and C as float32, [T, G, 2, padded S]; then the chunks' states [numbers, padded S, D] and sums of steps
 // [numbers, D].
 struct SelectSpace {
   float *bc, *states, *sums;
@@ -51,26 +50,45 @@ inline SelectSpace select_space(void *ws, int64_t T, int64_t D, int64_t G, int64
   return s;
 }
 
-typedef const float __attribute__((address_space(4))) *Scalars;  // read by scalar loads
-__device__ __forceinline__ Scalars scalars(const float *p) { return (Scalars)(uintptr_t)p; }
+// N floats of each of M rows (`stride` apart), held by a wave until it lays them into its
+// own LDS, [M, N], where every lane reads all of them.  (As scalar loads they miss the
+// scalar cache row by row, 600 cycles each, and every wait is one for all of them.)
+template <int M, int N> struct Shared {
+  static constexpr int EACH = (M * N + 63) / 64;
+  float v[EACH];
+  __device__ __forceinline__ void load(const float *p, int64_t stride) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const int at = min(lane + i * 64, M * N - 1);
+      v[i] = p[at / N * stride + at % N];
+    }
+  }
+  __device__ __forceinline__ void lay(float *lds) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+      if (M * N % 64 == 0 || lane + i * 64 < M * N) lds[lane + i * 64] = v[i];
+  }
+};
 
-// log(1 + e) for e in [0, 1]: 2 atanh(e / (2 + e)), whose odd series in q = e / (2 + e)
-// <= 1/3 is cut behind q^15 (the first term left out is below 2^-25 of the sum).
+// log(1 + e) for e in [0, 1]: 2 atanh(q), q = e / (2 + e) <= 1/3, as q times a polynomial
+// in q^2.  Its coefficients make the largest relative error of the exact polynomial over
+// [0, 1/9] as small as five of them can, 2^-27.9; evaluated in float32, log(1 + e) is good to
+// 4 units of 2^-24.
 __device__ __forceinline__ float log1p_of(float e) {
   const float q = e * __builtin_amdgcn_rcpf(2.f + e), q2 = q * q;
-  float p = 1.f / 15.f;
-  p = fmaf(p, q2, 1.f / 13.f);
-  p = fmaf(p, q2, 1.f / 11.f);
-  p = fmaf(p, q2, 1.f / 9.f);
-  p = fmaf(p, q2, 1.f / 7.f);
-  p = fmaf(p, q2, 1.f / 5.f);
-  p = fmaf(p, q2, 1.f / 3.f);
-  p = fmaf(p, q2, 1.f);
-  return 2.f * q * p;
+  float p = 0.2817833524993873f;
+  p = fmaf(p, q2, 0.27960602677791624f);
+  p = fmaf(p, q2, 0.4002491028745423f);
+  p = fmaf(p, q2, 0.6666631468186291f);
+  p = fmaf(p, q2, 2.f);
+  return q * p;
 }
-// softplus(v) = max(v, 0) + log(1 + exp(-|v|)); good to 4 steps where it is above 2^-126
+// softplus(v) = max(v, 0) + log(1 + exp(-|v|)).  (The median of three, as max() first
+// brings its operand into canonical form.)
 __device__ __forceinline__ float softplus_of(float v) {
-  return fmaxf(v, 0.f) + log1p_of(__builtin_amdgcn_exp2f(-fabsf(v) * LOG2E_L));
+  return __builtin_amdgcn_fmed3f(v, 0.f, __builtin_inff()) + log1p_of(__builtin_amdgcn_exp2f(-fabsf(v) * LOG2E_L));
 }
 
 // A[ch] as base-2 exponents; zeros behind the last state

@@ -10,9 +10,9 @@ sigmoid and the activations count as in oracle/layers.py.
 
   softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|): e is off by (2 |v| + 4) U
       relative, which log(1 + e) carries on with a factor of at most 1; e / (2 + e)
-      adds 4 U (a sum, a reciprocal good to one step, a product), the odd polynomial
-      of eight rounded steps 3 U and its cut end 1/2 U, the last products 2 U:
-      (2 |v| + 14) U of log(1 + e), and U of the sum;
+      adds 4 U (a sum, a reciprocal good to one step, a product), the polynomial in
+      its square 3 U and what its rounded coefficients leave 1/2 U, the last product U:
+      (2 |v| + 14) U of log(1 + e) at most, and U of the sum;
   exp(delta A): the product delta A log2(e) is rounded twice and its constant once
       (3 U of |delta A|), the exponential good to one step (2 U, one to spare); a
       value below 2^-126 may come out as 0;
