@@ -17,29 +17,51 @@ __device__ __forceinline__ int uniform_of(int x) { return __builtin_amdgcn_readf
 // and written in whole pieces too.
 template <typename T, int N> struct __attribute__((packed, aligned(sizeof(T)))) Piece { T v[N]; };
 
-// channels ch .. ch + N - 1 of a row of D; those behind its end read as 0 and are not written
-template <typename T, int N> __device__ __forceinline__ Piece<T, N> load_piece(const T *row, int ch, int D) {
-  if (ch + N <= D) return *(const Piece<T, N> *)(row + ch);
+// channels ch .. ch + N - 1 of a row of D; those behind its end read as 0 and are not
+// written.  STREAMED: past the caches (gdp_layer_common.h).
+template <typename T, int N, bool STREAMED = false>
+__device__ __forceinline__ Piece<T, N> load_piece(const T *row, int ch, int D) {
+  if (ch + N <= D) {
+    if constexpr (STREAMED) {
+      typedef T vec __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+      const vec v = __builtin_nontemporal_load((const vec *)(row + ch));
+      Piece<T, N> p;
+#pragma unroll
+      for (int c = 0; c < N; ++c) p.v[c] = v[c];
+      return p;
+    } else {
+      return *(const Piece<T, N> *)(row + ch);
+    }
+  }
   Piece<T, N> p;
 #pragma unroll
   for (int c = 0; c < N; ++c) p.v[c] = ch + c < D ? row[ch + c] : (T)0.f;
   return p;
 }
-template <typename T, int N> __device__ __forceinline__ void store_piece(T *row, int ch, int D, const Piece<T, N> &p) {
+template <typename T, int N, bool STREAMED = false>
+__device__ __forceinline__ void store_piece(T *row, int ch, int D, const Piece<T, N> &p) {
   if (ch + N <= D) {
-    *(Piece<T, N> *)(row + ch) = p;
+    if constexpr (STREAMED) {
+      typedef T vec __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+      vec v;
+#pragma unroll
+      for (int c = 0; c < N; ++c) v[c] = p.v[c];
+      __builtin_nontemporal_store(v, (vec *)(row + ch));
+    } else {
+      *(Piece<T, N> *)(row + ch) = p;
+    }
     return;
   }
 #pragma unroll
   for (int c = 0; c < N; ++c)
     if (ch + c < D) row[ch + c] = p.v[c];
 }
-template <typename T, int N>
+template <typename T, int N, bool STREAMED = false>
 __device__ __forceinline__ void store_floats(T *row, int ch, int D, const float (&x)[N]) {
   Piece<T, N> p;
 #pragma unroll
   for (int c = 0; c < N; ++c) p.v[c] = (T)x[c];
-  store_piece<T, N>(row, ch, D, p);
+  store_piece<T, N, STREAMED>(row, ch, D, p);
 }
 // element i of a parameter of type `type` (float32 or T)
 template <typename T> __device__ __forceinline__ float param_at(const void *p, int type, int64_t i) {

@@ -52,7 +52,7 @@ template <typename T, int N> __device__ __forceinline__ void to_floats(float (&x
   for (int c = 0; c < N; ++c) x[c] = (float)p.v[c];
 }
 
-template <typename T, int W, int VEC>
+template <typename T, int W, int VEC, bool STREAMED>
 __global__ void __launch_bounds__(64 * WAVES) gdp_conv_kernel(ConvArgs a, int shift, int blocks, int jobs) {
   const int id = (int)blockIdx.x * WAVES + uniform_of(threadIdx.x >> 6);
   if (id >= jobs) return;
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_conv_kernel(ConvArgs a, int sh
     auto fetch = [&](int t) {
 #pragma unroll
       for (int r = 0; r < ROWS; ++r)
-        if (t + r < k.end) next[r] = load_piece<T, VEC>(row + (int64_t)(t + r - k.begin) * a.x_st, ch, a.D);
+        if (t + r < k.end) next[r] = load_piece<T, VEC, STREAMED>(row + (int64_t)(t + r - k.begin) * a.x_st, ch, a.D);
     };
     fetch(k.begin);
     load_taps<T, W, VEC>(w, b, a, ch);
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_conv_kernel(ConvArgs a, int sh
 #pragma unroll
             for (int c = 0; c < VEC; ++c) y[c] = act_of(a.act, y[c]);
           }
-          store_floats<T, VEC>(out, ch, a.D, y);
+          store_floats<T, VEC, STREAMED>(out, ch, a.D, y);
           out += a.y_st;
         }
       }
@@ -309,9 +309,12 @@ hipError_t launch_conv(const ConvArgs &a, int xt, hipStream_t stream) {
     const int shift = shift_of(a.T, blocks, WANT);
     const int64_t jobs = chunk_numbers(a.T, a.N, shift) * blocks;
     if (jobs == 0 || a.N == 0) return hipSuccess;
+    const bool streamed = (int64_t)a.T * a.D * 2 * (int64_t)sizeof(T) > STREAM_BYTES;
     return by_taps(a.W, [&](auto w) {
-      hipLaunchKernelGGL((gdp_conv_kernel<T, decltype(w)::value, VEC>), dim3((unsigned)((jobs + WAVES - 1) / WAVES)),
-                         dim3(64 * WAVES), 0, stream, a, shift, (int)blocks, (int)jobs);
+      auto *kernel = streamed ? gdp_conv_kernel<T, decltype(w)::value, VEC, true>
+                              : gdp_conv_kernel<T, decltype(w)::value, VEC, false>;
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((jobs + WAVES - 1) / WAVES)), dim3(64 * WAVES), 0, stream, a, shift,
+                         (int)blocks, (int)jobs);
       return hipGetLastError();
     });
   });

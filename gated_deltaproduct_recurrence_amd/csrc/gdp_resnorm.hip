@@ -32,23 +32,23 @@ constexpr int MAX_VALUES = 16;  // values a lane holds of one token
 
 template <typename T, int VEC, int E> struct Row {
   Piece<T, VEC> p[E];
-  __device__ __forceinline__ void load(const T *row, int lane, int lpg, int D) {
+  template <bool STREAMED> __device__ __forceinline__ void load(const T *row, int lane, int lpg, int D) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int ch = (e * lpg + lane) * VEC;
       p[e] = {};
-      if (ch < D) p[e] = load_piece<T, VEC>(row, ch, D);
+      if (ch < D) p[e] = load_piece<T, VEC, STREAMED>(row, ch, D);
     }
   }
   __device__ __forceinline__ float at(int e, int c) const { return (float)p[e].v[c]; }
 };
 
-template <typename T, int VEC, int E>
+template <bool STREAMED, typename T, int VEC, int E>
 __device__ __forceinline__ void store_row(T *row, const float (&x)[E][VEC], int lane, int lpg, int D) {
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int ch = (e * lpg + lane) * VEC;
-    if (ch < D) store_floats<T, VEC>(row, ch, D, x[e]);
+    if (ch < D) store_floats<T, VEC, STREAMED>(row, ch, D, x[e]);
   }
 }
 
@@ -74,7 +74,7 @@ __device__ __forceinline__ float rstd_of(const float (&v)[E][VEC], Team<WIDE> &t
 }
 
 // T: y, the gate and n; X: the residual stream
-template <typename T, typename X, int VEC, int E, int WIDE>
+template <typename T, typename X, int VEC, int E, int WIDE, bool STREAMED>
 __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_resnorm_kernel(ResNormArgs a, int lpg) {
   __shared__ float slots[WIDE ? 2 : 1][16];
   const int tid = threadIdx.x, teams = (int)blockDim.x / lpg;
@@ -88,9 +88,9 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_resnorm_kern
   Row<X, VEC, E> xv{}, xn{};
   auto fetch = [&](int64_t t) {
     if (t < a.T) {
-      yn.load((const T *)a.y + t * a.y_st, team.lane, lpg, a.D);
-      xn.load((const X *)a.x + t * a.x_st, team.lane, lpg, a.D);
-      if (a.z) zn.load((const T *)a.z + t * a.z_st, team.lane, lpg, a.D);
+      yn.template load<STREAMED>((const T *)a.y + t * a.y_st, team.lane, lpg, a.D);
+      xn.template load<STREAMED>((const X *)a.x + t * a.x_st, team.lane, lpg, a.D);
+      if (a.z) zn.template load<STREAMED>((const T *)a.z + t * a.z_st, team.lane, lpg, a.D);
     }
   };
   int64_t t = (int64_t)blockIdx.x * teams + tid / lpg;
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_resnorm_kern
         if (a.z) p *= act_of(a.act, zv.at(e, c));
         v[e][c] = xv.at(e, c) + p;
       }
-    if (t < a.T) store_row<X, VEC, E>((X *)a.r + t * a.r_st, v, team.lane, lpg, a.D);
+    if (t < a.T) store_row<STREAMED, X, VEC, E>((X *)a.r + t * a.r_st, v, team.lane, lpg, a.D);
     if (a.pre) {
       // lanes behind the row's end hold zeros: x and y are 0 there
       const float rr = rstd_of<VEC, E, WIDE>(v, team, inv_d, a.eps);
@@ -123,14 +123,14 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_resnorm_kern
       for (int e = 0; e < E; ++e)
 #pragma unroll
         for (int c = 0; c < VEC; ++c) v[e][c] *= rr * wb[e][c];
-      if (t < a.T) store_row<T, VEC, E>((T *)a.n + t * a.n_st, v, team.lane, lpg, a.D);
+      if (t < a.T) store_row<STREAMED, T, VEC, E>((T *)a.n + t * a.n_st, v, team.lane, lpg, a.D);
     }
   }
 }
 
 // The gradients; partial sums of the weights' gradients to the workspace, one row
 // [2, D] per workgroup (the teams' sums added in LDS).
-template <typename T, typename X, int VEC, int E, int WIDE>
+template <typename T, typename X, int VEC, int E, int WIDE, bool STREAMED>
 __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_resnorm_backward_kernel(ResNormArgs a, int lpg) {
   __shared__ float slots[WIDE ? 2 : 1][16];
   __shared__ float part[WIDE ? 1 : 256 * MAX_VALUES];
@@ -145,13 +145,13 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_resnorm_back
   Row<X, VEC, E> xv{}, rv{}, xn{}, rn{};
   auto fetch = [&](int64_t t) {
     if (t < a.T) {
-      yn.load((const T *)a.y + t * a.y_st, team.lane, lpg, a.D);
+      yn.template load<STREAMED>((const T *)a.y + t * a.y_st, team.lane, lpg, a.D);
       if (a.pre) {  // r is needed for its norm alone
-        xn.load((const X *)a.x + t * a.x_st, team.lane, lpg, a.D);
-        nn.load((const T *)a.dn + t * a.dn_st, team.lane, lpg, a.D);
+        xn.template load<STREAMED>((const X *)a.x + t * a.x_st, team.lane, lpg, a.D);
+        nn.template load<STREAMED>((const T *)a.dn + t * a.dn_st, team.lane, lpg, a.D);
       }
-      if (a.z) zn.load((const T *)a.z + t * a.z_st, team.lane, lpg, a.D);
-      if (a.dr) rn.load((const X *)a.dr + t * a.dr_st, team.lane, lpg, a.D);
+      if (a.z) zn.template load<STREAMED>((const T *)a.z + t * a.z_st, team.lane, lpg, a.D);
+      if (a.dr) rn.template load<STREAMED>((const X *)a.dr + t * a.dr_st, team.lane, lpg, a.D);
     }
   };
   int64_t t = (int64_t)blockIdx.x * teams + tid / lpg;
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_resnorm_back
 #pragma unroll
         for (int c = 0; c < VEC; ++c) e_[e][c] = rv.at(e, c);
     }
-    if (t < a.T) store_row<X, VEC, E>((X *)a.dx + t * a.dx_st, e_, team.lane, lpg, a.D);
+    if (t < a.T) store_row<STREAMED, X, VEC, E>((X *)a.dx + t * a.dx_st, e_, team.lane, lpg, a.D);
     // dp in e_, then v; dz in its own
     if (a.z) {
       float dz[E][VEC];
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_resnorm_back
           dz[e][c] = d * yhat[e][c] * wa[e][c] * slope;
           e_[e][c] = d * f;
         }
-      if (t < a.T) store_row<T, VEC, E>((T *)a.dz + t * a.dz_st, dz, team.lane, lpg, a.D);
+      if (t < a.T) store_row<STREAMED, T, VEC, E>((T *)a.dz + t * a.dz_st, dz, team.lane, lpg, a.D);
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e)
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_resnorm_back
 #pragma unroll
         for (int c = 0; c < VEC; ++c) e_[e][c] = ry * fmaf(-yhat[e][c], s, e_[e][c]);
     }
-    if (t < a.T) store_row<T, VEC, E>((T *)a.dy + t * a.dy_st, e_, team.lane, lpg, a.D);
+    if (t < a.T) store_row<STREAMED, T, VEC, E>((T *)a.dy + t * a.dy_st, e_, team.lane, lpg, a.D);
   }
   if (!a.dw_post && !a.dw_pre) return;
   const bool fold = !WIDE && teams > 1;
@@ -336,10 +336,12 @@ hipError_t launch_resnorm(const ResNormArgs &a, int yt, int xt, hipStream_t stre
     using T = decltype(y);
     using X = decltype(x);
     const Plan p = plan_of(a.D, vec_of<T>());
+    const bool streamed = a.T * a.D * (int64_t)(2 * sizeof(X) + (1 + (a.z != nullptr) + a.pre) * sizeof(T)) > STREAM_BYTES;
     return by_plan<T>(p, [&](auto s) {
       using S = decltype(s);
-      hipLaunchKernelGGL((gdp_resnorm_kernel<T, X, S::vec, S::pieces, S::wide>),
-                         dim3((unsigned)grid_of(p, a.T, FORWARD_GRID)), dim3(p.threads), 0, stream, a, p.lpg);
+      auto *kernel = streamed ? gdp_resnorm_kernel<T, X, S::vec, S::pieces, S::wide, true>
+                              : gdp_resnorm_kernel<T, X, S::vec, S::pieces, S::wide, false>;
+      hipLaunchKernelGGL(kernel, dim3((unsigned)grid_of(p, a.T, FORWARD_GRID)), dim3(p.threads), 0, stream, a, p.lpg);
       return hipGetLastError();
     });
   });
@@ -350,12 +352,15 @@ hipError_t launch_resnorm_backward(const ResNormArgs &a, int yt, int xt, hipStre
     using T = decltype(y);
     using X = decltype(x);
     const Plan p = plan_of(a.D, vec_of<T>());
+    const bool streamed =
+        a.T * a.D * (int64_t)(3 * sizeof(X) + (2 + 2 * (a.z != nullptr) + a.pre) * sizeof(T)) > STREAM_BYTES;
     const int64_t blocks = grid_of(p, a.T, BACKWARD_GRID);
     if (blocks) {
       const hipError_t e = by_plan<T>(p, [&](auto s) {
         using S = decltype(s);
-        hipLaunchKernelGGL((gdp_resnorm_backward_kernel<T, X, S::vec, S::pieces, S::wide>), dim3((unsigned)blocks),
-                           dim3(p.threads), 0, stream, a, p.lpg);
+        auto *kernel = streamed ? gdp_resnorm_backward_kernel<T, X, S::vec, S::pieces, S::wide, true>
+                                : gdp_resnorm_backward_kernel<T, X, S::vec, S::pieces, S::wide, false>;
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(p.threads), 0, stream, a, p.lpg);
         return hipGetLastError();
       });
       if (e != hipSuccess) return e;

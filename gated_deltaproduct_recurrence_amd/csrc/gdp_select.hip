@@ -29,12 +29,52 @@
 namespace gdp {
 namespace {
 
-constexpr int WAVES = 4, ROWS = 4;  // waves per workgroup, rows in flight
+constexpr int WAVES = 4, ROWS = 4;  // waves per workgroup (or one), rows in flight
 
-// B and C rows as float32 behind each other, zeros behind the last state
-template <typename T> __global__ void __launch_bounds__(256) gdp_select_stage_kernel(SelectArgs a, float *bc, int P) {
-  const int64_t all = (int64_t)a.T * a.G * 2 * P;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+// B and C rows as float32 behind each other, zeros behind the last state; the last
+// workgroup sorts the chunk numbers by their chunks' lengths, in 64 classes, longest first
+// (those that name no chunk last).  Within a class they stand as their counters
+// give them, which changes no result.
+template <typename T>
+__global__ void __launch_bounds__(256) gdp_select_stage_kernel(SelectArgs a, float *bc, int P, int shift, int numbers,
+                                                               int *order) {
+  if (order && blockIdx.x == gridDim.x - 1) {
+    __shared__ int count[64], start[64];
+    constexpr int EACH = (int)(MOST_ORDERED / 256);
+    int cls[EACH];
+    if (threadIdx.x < 64) count[threadIdx.x] = 0;
+    __syncthreads();
+    for (int j = 0; j < EACH; ++j) {
+      const int number = j * 256 + threadIdx.x;
+      cls[j] = -1;
+      if (number >= numbers) continue;
+      int lo = 0, hi = a.N;  // the last sequence whose numbers begin at or before it
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (((int)bound_at(a.cu, a.cu_is64, mid, a.T) >> shift) + mid <= number) lo = mid;
+        else hi = mid;
+      }
+      const int first = (int)bound_at(a.cu, a.cu_is64, lo, a.T), last = (int)bound_at(a.cu, a.cu_is64, lo + 1, a.T);
+      const int64_t at = (int64_t)(number - (first >> shift) - lo) << shift, left = at < 0 ? 0 : last - first - at;
+      const int64_t rows = left < 0 ? 0 : (left < (int64_t)1 << shift ? left : (int64_t)1 << shift);
+      cls[j] = 63 - (int)(rows * 63 >> shift);
+      atomicAdd(&count[cls[j]], 1);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      int sum = 0;
+      for (int c = 0; c < 64; ++c) {
+        start[c] = sum;
+        sum += count[c];
+      }
+    }
+    __syncthreads();
+    for (int j = 0; j < EACH; ++j)
+      if (cls[j] >= 0) order[atomicAdd(&start[cls[j]], 1)] = j * 256 + threadIdx.x;
+    return;
+  }
+  const int64_t all = (int64_t)a.T * a.G * 2 * P, step = (int64_t)(gridDim.x - (order ? 1 : 0)) * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
     const int n = (int)(i & (P - 1)), which = (int)(i / P & 1);
     const int64_t row = i / (2 * P), t = row / a.G, g = row % a.G;
     const T *p = which ? (const T *)a.C + t * a.C_st + g * a.C_sg : (const T *)a.B + t * a.B_st + g * a.B_sg;
@@ -44,10 +84,12 @@ template <typename T> __global__ void __launch_bounds__(256) gdp_select_stage_ke
 
 // A wave's chunk and channels
 struct Place { Chunk k; int number, ch, group; bool live; };
-__device__ __forceinline__ bool place_of(Place *p, const SelectArgs &a, const SelectGrid &g, int64_t jobs) {
-  const int64_t id = (int64_t)blockIdx.x * WAVES + uniform_of(threadIdx.x >> 6);
+__device__ __forceinline__ bool place_of(Place *p, const SelectArgs &a, const SelectGrid &g, const int *order,
+                                         int64_t jobs) {
+  const int64_t id = (int64_t)blockIdx.x * (blockDim.x >> 6) + uniform_of(threadIdx.x >> 6);
   if (id >= jobs) return false;
   p->number = (int)(id / g.blocks);
+  if (order) p->number = uniform_of(order[p->number]);
   if (!find_chunk(&p->k, a.cu, a.cu_is64, a.T, a.N, g.shift, p->number)) return false;
   const int b = (int)(id % g.blocks), per = a.D / a.G;
   p->group = b / g.per_group;
@@ -86,7 +128,7 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_ends_kernel(SelectArgs 
                                                                      int64_t jobs) {
   __shared__ __attribute__((aligned(16))) float lds[WAVES][ROWS * P];
   Place p;
-  if (!place_of(&p, a, g, jobs) || p.k.end == p.k.last) return;
+  if (!place_of(&p, a, g, s.order, jobs) || p.k.end == p.k.last) return;
   const int ch = p.ch;
   float A2[P], h[P];
   load_rates<P>(A2, a, ch);
@@ -179,7 +221,7 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
                                                                 int64_t jobs) {
   __shared__ __attribute__((aligned(16))) float lds[WAVES][ROWS * 2 * P];
   Place p;
-  if (!place_of(&p, a, g, jobs)) return;
+  if (!place_of(&p, a, g, s.order, jobs)) return;
   const Chunk k = p.k;
   const int ch = p.ch;
   float A2[P], h[P];
@@ -336,17 +378,15 @@ size_t select_bytes(int64_t T, int64_t N, int64_t D, int64_t G, int64_t S) {
   return select_space(nullptr, T, D, G, S, forward_grid(T, N, D, G).numbers).bytes;
 }
 
-hipError_t launch_select_stage(const SelectArgs &a, int ut, float *bc, hipStream_t stream) {
+hipError_t launch_select_stage(const SelectArgs &a, int ut, const SelectGrid &g, const SelectSpace &s,
+                               hipStream_t stream) {
   const int P = padded_states(a.S);
-  const int64_t want = ((int64_t)a.T * a.G * 2 * P + 255) / 256;
-  const dim3 grid((unsigned)(want < 4096 ? want : 4096));
+  int64_t want = ((int64_t)a.T * a.G * 2 * P + 255) / 256;
+  want = (want < 4096 ? want : 4096) + (s.order ? 1 : 0);
   if (want == 0) return hipSuccess;
-  if (ut == EL_F32)
-    hipLaunchKernelGGL(gdp_select_stage_kernel<float>, grid, dim3(256), 0, stream, a, bc, P);
-  else if (ut == EL_BF16)
-    hipLaunchKernelGGL(gdp_select_stage_kernel<bf16>, grid, dim3(256), 0, stream, a, bc, P);
-  else
-    hipLaunchKernelGGL(gdp_select_stage_kernel<_Float16>, grid, dim3(256), 0, stream, a, bc, P);
+  auto *kernel = ut == EL_F32 ? gdp_select_stage_kernel<float>
+                              : (ut == EL_BF16 ? gdp_select_stage_kernel<bf16> : gdp_select_stage_kernel<_Float16>);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)want), dim3(256), 0, stream, a, s.bc, P, g.shift, (int)g.numbers, s.order);
   return hipGetLastError();
 }
 
@@ -354,14 +394,19 @@ hipError_t launch_select(const SelectArgs &a, int ut, int dt, hipStream_t stream
   const SelectGrid g = forward_grid(a.T, a.N, a.D, a.G);
   const int64_t jobs = g.numbers * g.blocks;
   if (jobs == 0 || a.N == 0) return hipSuccess;
-  const SelectSpace s = select_space(a.ws, a.T, a.D, a.G, a.S, g.numbers);
-  if (hipError_t e = launch_select_stage(a, ut, s.bc, stream)) return e;
+  SelectSpace s = select_space(a.ws, a.T, a.D, a.G, a.S, g.numbers);
+  // one wave per workgroup while that leaves compute units without one: 812 rows of 512
+  // channels take 40 us so and 44 with four, 32768 of 2048 take 495 and 462
+  const int waves = jobs <= 1024 ? 1 : WAVES;
+  // (the chunks of one sequence stand in order, and few waves all run at once)
+  if (a.N == 1 || waves == 1) s.order = nullptr;
+  if (hipError_t e = launch_select_stage(a, ut, g, s, stream)) return e;
   return select_types(ut, dt, [&](auto u, auto d) {
     using UT = decltype(u);
     using DT = decltype(d);
     return by_states(a.S, [&](auto n) {
       constexpr int P = decltype(n)::value;
-      const dim3 grid((unsigned)((jobs + WAVES - 1) / WAVES)), threads(64 * WAVES);
+      const dim3 grid((unsigned)((jobs + waves - 1) / waves)), threads(64 * waves);
       if (a.T > (int64_t)1 << g.shift) {  // else no sequence has two chunks
         hipLaunchKernelGGL((gdp_select_ends_kernel<UT, DT, P>), grid, threads, 0, stream, a, g, s, jobs);
         if (hipError_t e = hipGetLastError()) return e;

@@ -514,7 +514,9 @@ hipError_t launch_select_backward(const SelectArgs &given, int ut, int dt, hipSt
   const BackwardSpace b = backward_space(a.ws, a.T, a.N, a.D, a.G, a.S, g, a.points != nullptr);
   hipError_t e;
   if (a.points) {
-    e = launch_select_stage(a, ut, b.s.bc, stream);
+    SelectSpace stage = b.s;
+    stage.order = nullptr;
+    e = launch_select_stage(a, ut, g, stage, stream);
   } else {  // the checkpoints again, into the workspace (which begins as the forward pass's)
     a.points = b.points;
     e = launch_select(a, ut, dt, stream);

@@ -29,10 +29,15 @@ inline SelectGrid select_grid(int64_t T, int64_t N, int64_t D, int64_t G, int64_
 
 inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Chunk numbers, long chunks first, where that many fit: the numbers' order in which the
+// waves take them.  Few waves of uneven chunks leave compute units idle at the end otherwise.
+constexpr int64_t MOST_ORDERED = 1024;
+
 // The workspace's first part: B and C as float32, [T, G, 2, padded S]; then the chunks' states [numbers, padded S, D] and sums of steps
 // [numbers, D].
 struct SelectSpace {
   float *bc, *states, *sums;
+  int *order;  // [numbers], or null
   size_t bytes;
 };
 inline SelectSpace select_space(void *ws, int64_t T, int64_t D, int64_t G, int64_t S, int64_t numbers) {
@@ -46,6 +51,11 @@ inline SelectSpace select_space(void *ws, int64_t T, int64_t D, int64_t G, int64
   at += round256((size_t)numbers * P * D * 4);
   s.sums = (float *)(p + at);
   at += round256((size_t)numbers * D * 4);
+  s.order = nullptr;
+  if (numbers <= MOST_ORDERED) {
+    s.order = (int *)(p + at);
+    at += round256((size_t)numbers * 4);
+  }
   s.bytes = at;
   return s;
 }
@@ -112,11 +122,18 @@ template <typename F> hipError_t by_states(int64_t S, F f) {
   }
 }
 
-// the forward pass's chunks
+// The forward pass's chunks: short enough for 4096 waves; but where the sequences are as
+// many as fill the chip by themselves, as long as twice their mean length, so that most
+// are one chunk and take part in neither of the first two kernels.
 inline SelectGrid forward_grid(int64_t T, int64_t N, int64_t D, int64_t G) {
-  return select_grid(T, N, D, G, 4096, 5, 11);
+  SelectGrid g = select_grid(T, N, D, G, 4096, 5, 11);
+  if (N * g.blocks >= 2048)
+    while (g.shift < 11 && ((int64_t)1 << g.shift) * N < 2 * T) ++g.shift;
+  g.numbers = chunk_numbers(T, N, g.shift);
+  return g;
 }
-// B and C into the workspace
-hipError_t launch_select_stage(const SelectArgs &a, int u_type, float *bc, hipStream_t stream);
+// B and C into the workspace, and the chunks' order
+hipError_t launch_select_stage(const SelectArgs &a, int u_type, const SelectGrid &g, const SelectSpace &s,
+                               hipStream_t stream);
 
 }  // namespace gdp
