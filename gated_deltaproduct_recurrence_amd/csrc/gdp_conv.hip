@@ -23,7 +23,8 @@
 namespace gdp {
 namespace {
 
-constexpr int WAVES = 4, ROWS = 4;
+constexpr int WAVES = 4, FORWARD_ROWS = 2, BACKWARD_ROWS = 2;  // rows: of a group, loaded a group ahead
+template <bool B> struct Flag { static constexpr bool value = B; };
 
 // Row t >= first - (W - 1) of a chunk's sequence: those before its first lie in the initial state.
 template <typename T, int W, int VEC>
@@ -36,15 +37,26 @@ __device__ __forceinline__ Piece<T, VEC> row_before(const ConvArgs &a, const Chu
   return p;
 }
 
+template <typename P, int W, int VEC> __device__ __forceinline__ void load_rows(float (&w)[W][VEC], const P *p, int ch, int D) {
+  if (ch + VEC <= D) {  // the channels' taps lie behind each other
+    const Piece<P, VEC * W> all = *(const Piece<P, VEC * W> *)(p + (int64_t)ch * W);
+#pragma unroll
+    for (int c = 0; c < VEC; ++c)
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][c] = (float)all.v[c * W + j];
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < VEC; ++c)
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][c] = ch + c < D ? (float)p[(int64_t)(ch + c) * W + j] : 0.f;
+}
 template <typename T, int W, int VEC>
 __device__ __forceinline__ void load_taps(float (&w)[W][VEC], float (&b)[VEC], const ConvArgs &a, int ch) {
+  if (a.w_type == EL_F32) load_rows<float, W, VEC>(w, (const float *)a.w, ch, a.D);
+  else load_rows<T, W, VEC>(w, (const T *)a.w, ch, a.D);
 #pragma unroll
-  for (int c = 0; c < VEC; ++c) {
-    const int d = min(ch + c, a.D - 1);
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[j][c] = param_at<T>(a.w, a.w_type, (int64_t)d * W + j);
-    b[c] = a.b ? param_at<T>(a.b, a.w_type, d) : 0.f;
-  }
+  for (int c = 0; c < VEC; ++c) b[c] = a.b && ch + c < a.D ? param_at<T>(a.b, a.w_type, ch + c) : 0.f;
 }
 
 template <typename T, int N> __device__ __forceinline__ void to_floats(float (&x)[N], const Piece<T, N> &p) {
@@ -60,43 +72,56 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_conv_kernel(ConvArgs a, int sh
   if (!find_chunk(&k, a.cu, a.cu_is64, a.T, a.N, shift, id / blocks)) return;
   const int ch = (id % blocks) * 64 * VEC + (threadIdx.x & 63) * VEC;
   if (ch >= a.D) return;
+  constexpr int ROWS = FORWARD_ROWS;
   if (k.begin < k.end) {
     float w[W][VEC], b[VEC], x[W - 1 + ROWS][VEC];
     Piece<T, VEC> next[ROWS] = {};
     const T *row = (const T *)a.x + (int64_t)k.begin * a.x_st;
     auto fetch = [&](int t) {
+      const T *p = row + (int64_t)(t - k.begin) * a.x_st;
+      if (t + ROWS <= k.end) {
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r)
-        if (t + r < k.end) next[r] = load_piece<T, VEC, STREAMED>(row + (int64_t)(t + r - k.begin) * a.x_st, ch, a.D);
+        for (int r = 0; r < ROWS; ++r) next[r] = load_piece<T, VEC, STREAMED>(p + r * a.x_st, ch, a.D);
+      } else {
+#pragma unroll
+        for (int r = 0; r < ROWS - 1; ++r)
+          if (t + r < k.end) next[r] = load_piece<T, VEC, STREAMED>(p + r * a.x_st, ch, a.D);
+      }
     };
     fetch(k.begin);
     load_taps<T, W, VEC>(w, b, a, ch);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) to_floats(x[j], row_before<T, W, VEC>(a, k, (int64_t)k.begin - (W - 1) + j, ch));
     T *out = (T *)a.y + (int64_t)k.begin * a.y_st;
+    // `count` rows of the group in x, all of them (without a branch per row) or fewer
+    auto group = [&](auto all, int count) {
+      float y[ROWS][VEC];
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int c = 0; c < VEC; ++c) {
+          float v = b[c];
+#pragma unroll
+          for (int j = 0; j < W; ++j) v = fmaf(w[j][c], x[r + j][c], v);
+          y[r][c] = v;
+        }
+      if (a.act != GDP_ACT_NONE) {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+          for (int c = 0; c < VEC; ++c) y[r][c] = act_of(a.act, y[r][c]);
+      }
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r)
+        if (decltype(all)::value || r < count) store_floats<T, VEC, STREAMED>(out + r * a.y_st, ch, a.D, y[r]);
+      out += ROWS * a.y_st;
+    };
     for (int t = k.begin; t < k.end; t += ROWS) {
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) to_floats(x[W - 1 + r], next[r]);
       fetch(t + ROWS);
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        if (t + r < k.end) {
-          float y[VEC];
-#pragma unroll
-          for (int c = 0; c < VEC; ++c) {
-            float v = b[c];
-#pragma unroll
-            for (int j = 0; j < W; ++j) v = fmaf(w[j][c], x[r + j][c], v);
-            y[c] = v;
-          }
-          if (a.act != GDP_ACT_NONE) {
-#pragma unroll
-            for (int c = 0; c < VEC; ++c) y[c] = act_of(a.act, y[c]);
-          }
-          store_floats<T, VEC, STREAMED>(out, ch, a.D, y);
-          out += a.y_st;
-        }
-      }
+      if (t + ROWS <= k.end) group(Flag<true>(), ROWS);
+      else group(Flag<false>(), k.end - t);
 #pragma unroll
       for (int j = 0; j < W - 1; ++j)
 #pragma unroll
@@ -150,7 +175,7 @@ __global__ void __launch_bounds__(256) gdp_conv_decode_kernel(ConvArgs a) {
 // end have dv = 0), and row t's dx is whole when row t + W - 1 is done.  Chunk 0
 // also forms the rows of the initial state's gradient, which lie before it.  Sums
 // of dw and db over the chunk go to the workspace: row `number` of [numbers, W + 2, D].
-template <typename T, int W, int VEC>
+template <typename T, int W, int VEC, bool STREAMED>
 __global__ void __launch_bounds__(64 * WAVES) gdp_conv_backward_kernel(ConvArgs a, int shift, int blocks, int numbers,
                                                                        int jobs) {
   const int id = (int)blockIdx.x * WAVES + uniform_of(threadIdx.x >> 6);
@@ -169,17 +194,28 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_conv_backward_kernel(ConvArgs 
     return;
   }
   float dw[W][VEC] = {}, db[VEC] = {};
+  constexpr int ROWS = BACKWARD_ROWS;
   if (some) {
     float w[W][VEC], b[VEC], x[W - 1 + ROWS][VEC], dv[W - 1 + ROWS][VEC];
-    Piece<T, VEC> xn[ROWS] = {}, gn[ROWS] = {};
+    Piece<T, VEC> xn[ROWS] = {}, gn[ROWS] = {}, g[ROWS];
     const int stop = k.end + W - 1;  // rows walked: [begin, stop)
+    const int rows_in = min(stop, k.last);  // rows read: [begin, rows_in)
     auto fetch = [&](int t) {
+      const T *px = (const T *)a.x + (int64_t)t * a.x_st, *pg = (const T *)a.dy + (int64_t)t * a.dy_st;
+      if (t + ROWS <= rows_in) {
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r)
-        if (t + r < min(stop, k.last)) {
-          xn[r] = load_piece<T, VEC>((const T *)a.x + (int64_t)(t + r) * a.x_st, ch, a.D);
-          gn[r] = load_piece<T, VEC>((const T *)a.dy + (int64_t)(t + r) * a.dy_st, ch, a.D);
+        for (int r = 0; r < ROWS; ++r) {
+          xn[r] = load_piece<T, VEC, STREAMED>(px + r * a.x_st, ch, a.D);
+          gn[r] = load_piece<T, VEC, STREAMED>(pg + r * a.dy_st, ch, a.D);
         }
+      } else {
+#pragma unroll
+        for (int r = 0; r < ROWS - 1; ++r)
+          if (t + r < rows_in) {
+            xn[r] = load_piece<T, VEC, STREAMED>(px + r * a.x_st, ch, a.D);
+            gn[r] = load_piece<T, VEC, STREAMED>(pg + r * a.dy_st, ch, a.D);
+          }
+      }
     };
     fetch(k.begin);
     load_taps<T, W, VEC>(w, b, a, ch);
@@ -189,60 +225,82 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_conv_backward_kernel(ConvArgs 
 #pragma unroll
       for (int c = 0; c < VEC; ++c) dv[j][c] = 0.f;
     }
+    // row t + r of a group: its dv, its share of the sums, and the dx of the row W - 1 before
+    auto slope_of = [&](int r) {
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) {
+        float v = b[c], slope;
+#pragma unroll
+        for (int j = 0; j < W; ++j) v = fmaf(w[j][c], x[r + j][c], v);
+        act_of(a.act, v, &slope);
+        dv[W - 1 + r][c] = (float)g[r].v[c] * slope;
+      }
+    };
+    auto sums_of = [&](int r) {
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) {
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[j][c] = fmaf(dv[W - 1 + r][c], x[r + j][c], dw[j][c]);
+        db[c] += dv[W - 1 + r][c];
+      }
+    };
+    auto dx_of = [&](float (&dx)[VEC], int r) {
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) s = fmaf(w[W - 1 - i][c], dv[r + i][c], s);
+        dx[c] = s;
+      }
+    };
     for (int t = k.begin; t < stop; t += ROWS) {
-      float g[ROWS][VEC];
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
         to_floats(x[W - 1 + r], xn[r]);
-        to_floats(g[r], gn[r]);
+        g[r] = gn[r];
       }
       fetch(t + ROWS);
+      const int first = t - (W - 1);  // whose dx is whole with row t
+      if (t + ROWS <= k.end && first >= k.begin && first + ROWS <= k.last - (W - 1)) {
+        // inside the chunk, and no row of the initial or the final state among those finished
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        if (t + r >= stop) continue;
-        if (t + r < k.last) {
+        for (int r = 0; r < ROWS; ++r) slope_of(r);
 #pragma unroll
-          for (int c = 0; c < VEC; ++c) {
-            float v = b[c], slope;
+        for (int r = 0; r < ROWS; ++r) sums_of(r);
 #pragma unroll
-            for (int j = 0; j < W; ++j) v = fmaf(w[j][c], x[r + j][c], v);
-            act_of(a.act, v, &slope);
-            dv[W - 1 + r][c] = g[r][c] * slope;
+        for (int r = 0; r < ROWS; ++r) {
+          float dx[VEC];
+          dx_of(dx, r);
+          store_floats<T, VEC, STREAMED>((T *)a.dx + (int64_t)(first + r) * a.dx_st, ch, a.D, dx);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          if (t + r >= stop) continue;
+          if (t + r < k.last) {
+            slope_of(r);
+            if (t + r < k.end) sums_of(r);
+          } else {
+#pragma unroll
+            for (int c = 0; c < VEC; ++c) dv[W - 1 + r][c] = 0.f;
           }
-          if (t + r < k.end) {
+          const int row = first + r;
+          const bool state = row < k.begin;
+          if (state && (k.index > 0 || !a.ds0)) continue;
+          float dx[VEC];
+          dx_of(dx, r);
+          const int left = row - (k.last - (W - 1));  // the row's place in the final state
+          if (a.dfinal && left >= 0) {
+            const Piece<float, VEC> f =
+                load_piece<float, VEC>(a.dfinal + ((int64_t)k.seq * (W - 1) + left) * a.D, ch, a.D);
 #pragma unroll
-            for (int c = 0; c < VEC; ++c) {
-#pragma unroll
-              for (int j = 0; j < W; ++j) dw[j][c] = fmaf(dv[W - 1 + r][c], x[r + j][c], dw[j][c]);
-              db[c] += dv[W - 1 + r][c];
-            }
+            for (int c = 0; c < VEC; ++c) dx[c] += f.v[c];
           }
-        } else {
-#pragma unroll
-          for (int c = 0; c < VEC; ++c) dv[W - 1 + r][c] = 0.f;
+          if (state)
+            store_floats<float, VEC>(a.ds0 + ((int64_t)k.seq * (W - 1) + (row - k.first + W - 1)) * a.D, ch, a.D, dx);
+          else
+            store_floats<T, VEC, STREAMED>((T *)a.dx + (int64_t)row * a.dx_st, ch, a.D, dx);
         }
-        const int row = t + r - (W - 1);  // whose dx is whole now
-        const bool state = row < k.begin;
-        if (state && (k.index > 0 || !a.ds0)) continue;
-        float dx[VEC];
-#pragma unroll
-        for (int c = 0; c < VEC; ++c) {
-          float s = 0.f;
-#pragma unroll
-          for (int i = 0; i < W; ++i) s = fmaf(w[W - 1 - i][c], dv[r + i][c], s);
-          dx[c] = s;
-        }
-        const int left = row - (k.last - (W - 1));  // the row's place in the final state
-        if (a.dfinal && left >= 0) {
-          const Piece<float, VEC> f =
-              load_piece<float, VEC>(a.dfinal + ((int64_t)k.seq * (W - 1) + left) * a.D, ch, a.D);
-#pragma unroll
-          for (int c = 0; c < VEC; ++c) dx[c] += f.v[c];
-        }
-        if (state)
-          store_floats<float, VEC>(a.ds0 + ((int64_t)k.seq * (W - 1) + (row - k.first + W - 1)) * a.D, ch, a.D, dx);
-        else
-          store_floats<T, VEC>((T *)a.dx + (int64_t)row * a.dx_st, ch, a.D, dx);
       }
 #pragma unroll
       for (int j = 0; j < W - 1; ++j)
@@ -259,13 +317,14 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_conv_backward_kernel(ConvArgs 
   if (a.db) store_floats<float, VEC>(sums + (int64_t)W * a.D, ch, a.D, db);
 }
 
-// Rows per chunk: the longest of 64, 32 and 16 that gives `want` waves.
-int shift_of(int64_t T, int64_t blocks, int64_t want) {
+// log2 of the rows per chunk
+constexpr int FORWARD_SHIFT = 4;
+// ... of the gradients: 64, or fewer down to 16 for at least 2048 waves
+int backward_shift(int64_t T, int64_t blocks) {
   int shift = 6;
-  while (shift > 4 && (T >> shift) * blocks < want) --shift;
+  while (shift > 4 && (T >> shift) * blocks < 2048) --shift;
   return shift;
 }
-constexpr int64_t WANT = 2048;
 
 template <typename F> hipError_t by_type(int xt, F f) {
   if (xt == EL_F32) return f((float)0);
@@ -285,7 +344,7 @@ template <typename F> hipError_t by_taps(int W, F f) {
 }
 
 int64_t blocks_of(int64_t D, int vec) { return (D + 64 * vec - 1) / (64 * vec); }
-constexpr int FORWARD_VEC = 16, BACKWARD_VEC = 4;  // bytes per lane; channels per lane
+constexpr int FORWARD_VEC = 8, BACKWARD_VEC = 2;  // bytes per lane; channels per lane
 
 }  // namespace
 
@@ -298,7 +357,7 @@ bool conv_served(int64_t T, int64_t N, int64_t D) {
 }
 
 size_t conv_backward_bytes(int64_t T, int64_t N, int64_t D, int64_t W) {
-  return (size_t)chunk_numbers(T, N, shift_of(T, blocks_of(D, BACKWARD_VEC), WANT)) * (W + 2) * D * 4;
+  return (size_t)chunk_numbers(T, N, backward_shift(T, blocks_of(D, BACKWARD_VEC))) * (W + 2) * D * 4;
 }
 
 hipError_t launch_conv(const ConvArgs &a, int xt, hipStream_t stream) {
@@ -306,15 +365,14 @@ hipError_t launch_conv(const ConvArgs &a, int xt, hipStream_t stream) {
     using T = decltype(x);
     constexpr int VEC = FORWARD_VEC / sizeof(T);
     const int64_t blocks = blocks_of(a.D, VEC);
-    const int shift = shift_of(a.T, blocks, WANT);
-    const int64_t jobs = chunk_numbers(a.T, a.N, shift) * blocks;
+    const int64_t jobs = chunk_numbers(a.T, a.N, FORWARD_SHIFT) * blocks;
     if (jobs == 0 || a.N == 0) return hipSuccess;
     const bool streamed = (int64_t)a.T * a.D * 2 * (int64_t)sizeof(T) > STREAM_BYTES;
     return by_taps(a.W, [&](auto w) {
       auto *kernel = streamed ? gdp_conv_kernel<T, decltype(w)::value, VEC, true>
                               : gdp_conv_kernel<T, decltype(w)::value, VEC, false>;
-      hipLaunchKernelGGL(kernel, dim3((unsigned)((jobs + WAVES - 1) / WAVES)), dim3(64 * WAVES), 0, stream, a, shift,
-                         (int)blocks, (int)jobs);
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((jobs + WAVES - 1) / WAVES)), dim3(64 * WAVES), 0, stream, a,
+                         FORWARD_SHIFT, (int)blocks, (int)jobs);
       return hipGetLastError();
     });
   });
@@ -335,13 +393,15 @@ hipError_t launch_conv_decode(const ConvArgs &a, int xt, hipStream_t stream) {
 
 hipError_t launch_conv_backward(const ConvArgs &a, int xt, hipStream_t stream) {
   const int64_t blocks = blocks_of(a.D, BACKWARD_VEC);
-  const int shift = shift_of(a.T, blocks, WANT);
+  const int shift = backward_shift(a.T, blocks);
   const int64_t numbers = chunk_numbers(a.T, a.N, shift), jobs = (numbers + (a.T >> shift) + 1) * blocks;
   const hipError_t e = by_type(xt, [&](auto x) {
     using T = decltype(x);
+    const bool streamed = (int64_t)a.T * a.D * 3 * (int64_t)sizeof(T) > STREAM_BYTES;
     return by_taps(a.W, [&](auto w) {
-      hipLaunchKernelGGL((gdp_conv_backward_kernel<T, decltype(w)::value, BACKWARD_VEC>),
-                         dim3((unsigned)((jobs + WAVES - 1) / WAVES)), dim3(64 * WAVES), 0, stream, a, shift,
+      auto *kernel = streamed ? gdp_conv_backward_kernel<T, decltype(w)::value, BACKWARD_VEC, true>
+                              : gdp_conv_backward_kernel<T, decltype(w)::value, BACKWARD_VEC, false>;
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((jobs + WAVES - 1) / WAVES)), dim3(64 * WAVES), 0, stream, a, shift,
                          (int)blocks, (int)numbers, (int)jobs);
       return hipGetLastError();
     });

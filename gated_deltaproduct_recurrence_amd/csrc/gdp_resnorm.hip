@@ -290,7 +290,7 @@ Plan plan_of(int64_t D, int vec) {
   return p;
 }
 
-constexpr int64_t FORWARD_GRID = 2048, BACKWARD_GRID = 1024;
+constexpr int64_t FORWARD_GRID = 1024, BACKWARD_GRID = 512;
 int64_t grid_of(const Plan &p, int64_t T, int64_t most) {
   const int64_t want = (T + p.teams - 1) / p.teams;
   return want < most ? want : most;
