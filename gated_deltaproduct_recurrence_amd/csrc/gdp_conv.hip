@@ -23,7 +23,7 @@
 namespace gdp {
 namespace {
 
-constexpr int WAVES = 4, FORWARD_ROWS = 2, BACKWARD_ROWS = 2;  // rows: of a group, loaded a group ahead
+constexpr int WAVES = 4, FORWARD_ROWS = 2, BACKWARD_ROWS = 4;  // rows: of a group, loaded a group ahead
 template <bool B> struct Flag { static constexpr bool value = B; };
 
 // Row t >= first - (W - 1) of a chunk's sequence: those before its first lie in the initial state.
@@ -319,10 +319,10 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_conv_backward_kernel(ConvArgs 
 
 // log2 of the rows per chunk
 constexpr int FORWARD_SHIFT = 4;
-// ... of the gradients: 64, or fewer down to 16 for at least 2048 waves
+// ... of the gradients: 128, or fewer down to 16 for at least 4096 waves
 int backward_shift(int64_t T, int64_t blocks) {
-  int shift = 6;
-  while (shift > 4 && (T >> shift) * blocks < 2048) --shift;
+  int shift = 7;
+  while (shift > 4 && (T >> shift) * blocks < 4096) --shift;
   return shift;
 }
 
@@ -344,7 +344,7 @@ template <typename F> hipError_t by_taps(int W, F f) {
 }
 
 int64_t blocks_of(int64_t D, int vec) { return (D + 64 * vec - 1) / (64 * vec); }
-constexpr int FORWARD_VEC = 8, BACKWARD_VEC = 2;  // bytes per lane; channels per lane
+constexpr int FORWARD_VEC = 8, BACKWARD_VEC = 1;  // bytes per lane; channels per lane
 
 }  // namespace
 

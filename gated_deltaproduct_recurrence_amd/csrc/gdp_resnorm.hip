@@ -52,15 +52,27 @@ __device__ __forceinline__ void store_row(T *row, const float (&x)[E][VEC], int 
   }
 }
 
-template <typename T, int VEC, int E>
-__device__ __forceinline__ void load_weights(float (&w)[E][VEC], const void *p, int type, int lane, int lpg, int D) {
+template <typename P, int VEC, int E>
+__device__ __forceinline__ void load_pieces(float (&w)[E][VEC], const P *p, int lane, int lpg, int D) {
+  Row<P, VEC, E> row;
+  row.template load<false>(p, lane, lpg, D);
 #pragma unroll
   for (int e = 0; e < E; ++e)
 #pragma unroll
-    for (int c = 0; c < VEC; ++c) {
-      const int ch = (e * lpg + lane) * VEC + c;
-      w[e][c] = p && ch < D ? param_at<T>(p, type, ch) : 1.f;
-    }
+    for (int c = 0; c < VEC; ++c) w[e][c] = row.at(e, c);
+}
+template <typename T, int VEC, int E>
+__device__ __forceinline__ void load_weights(float (&w)[E][VEC], const void *p, int type, int lane, int lpg, int D) {
+  if (!p) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int c = 0; c < VEC; ++c) w[e][c] = 1.f;
+  } else if (type == EL_F32) {
+    load_pieces<float, VEC, E>(w, (const float *)p, lane, lpg, D);
+  } else {
+    load_pieces<T, VEC, E>(w, (const T *)p, lane, lpg, D);
+  }
 }
 
 template <int VEC, int E, int WIDE>

@@ -61,8 +61,6 @@ BackwardSpace backward_space(void *ws, int64_t T, int64_t N, int64_t D, int64_t 
 }
 static_assert(SELECT_ROWS == 16, "checkpoint numbers are chunk numbers of 2^4 rows");
 
-SelectGrid backward_grid(int64_t T, int64_t N, int64_t D, int64_t G) { return select_grid(T, N, D, G, 2048, 6, 11); }
-
 template <typename UT, typename DT, int M> struct Back {
   UT d_o[M], z[M];
   DT dt[M];

@@ -126,11 +126,15 @@ template <typename F> hipError_t by_states(int64_t S, F f) {
 // many as fill the chip by themselves, as long as twice their mean length, so that most
 // are one chunk and take part in neither of the first two kernels.
 inline SelectGrid forward_grid(int64_t T, int64_t N, int64_t D, int64_t G) {
-  SelectGrid g = select_grid(T, N, D, G, 4096, 5, 11);
+  SelectGrid g = select_grid(T, N, D, G, 4096, 4, 11);
   if (N * g.blocks >= 2048)
     while (g.shift < 11 && ((int64_t)1 << g.shift) * N < 2 * T) ++g.shift;
   g.numbers = chunk_numbers(T, N, g.shift);
   return g;
+}
+// ... and those of the gradients: enough for 2048 workgroups
+inline SelectGrid backward_grid(int64_t T, int64_t N, int64_t D, int64_t G) {
+  return select_grid(T, N, D, G, 2048, 6, 11);
 }
 // B and C into the workspace, and the chunks' order
 hipError_t launch_select_stage(const SelectArgs &a, int u_type, const SelectGrid &g, const SelectSpace &s,
