@@ -479,16 +479,31 @@ gdp_select_backward_kernel(SelectArgs a, SelectGrid g, BackwardSpace b) {
 template <typename UT, typename DT>
 __global__ void __launch_bounds__(256) gdp_select_rows_kernel(SelectArgs a, SelectGrid g, BackwardSpace b, int P) {
   const int64_t c0 = bound_at(a.cu, a.cu_is64, 0, a.T), cN = a.N > 0 ? bound_at(a.cu, a.cu_is64, a.N, a.T) : 0;
+  // four states per lane, eight blocks' loads ahead
   const int64_t all = (int64_t)a.T * a.G * 2 * P, block = (int64_t)a.T * 2 * P;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < all; i += (int64_t)gridDim.x * 1024) {
     const int n = (int)(i & (P - 1)), which = (int)(i / P & 1);
     const int64_t group = i / block, t = i / (2 * P) % a.T;
-    float s = 0.f;
-    if (t >= c0 && t < cN && n < a.S) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (t >= c0 && t < cN) {
       const float *p = b.shares + group * g.per_group * block + i % block;
-      for (int j = 0; j < g.per_group; ++j) s += p[j * block];
+      int j = 0;
+      for (; j + 8 <= g.per_group; j += 8) {
+        float4 x[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = *(const float4 *)(p + (j + q) * block);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) s[0] += x[q].x, s[1] += x[q].y, s[2] += x[q].z, s[3] += x[q].w;
+      }
+      for (; j < g.per_group; ++j) {
+        const float4 x = *(const float4 *)(p + j * block);
+        s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w;
+      }
     }
-    if (n < a.S) ((UT *)(which ? a.dC : a.dB))[(t * a.G + group) * a.S + n] = (UT)s;
+    UT *out = (UT *)(which ? a.dC : a.dB) + (t * a.G + group) * a.S + n;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (n + c < a.S) out[c] = (UT)s[c];
   }
   for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     if (t >= c0 && t < cN) continue;
@@ -541,7 +556,7 @@ hipError_t launch_select_backward(const SelectArgs &given, int ut, int dt, hipSt
         if (hipError_t e = hipGetLastError()) return e;
       }
       if (a.T > 0) {
-        const int64_t want = ((int64_t)a.T * a.G * 2 * P + 255) / 256;
+        const int64_t want = ((int64_t)a.T * a.G * 2 * P + 1023) / 1024;
         hipLaunchKernelGGL((gdp_select_rows_kernel<UT, DT>), dim3((unsigned)(want < 4096 ? want : 4096)), dim3(256), 0,
                            stream, a, g, b, P);
         if (hipError_t e = hipGetLastError()) return e;
