@@ -66,23 +66,20 @@ def _run(cmd, verbose):
 def build_library(out=LIB, verbose=False, sanitize=False):
     """Compile and link libgdp.so; raises CalledProcessError on failure.
     sanitize=True builds the host-sanitized check library instead (to `out`),
-    in one hipcc call without the per-source flags (it never runs a kernel)."""
-    tmp = out + ".tmp"
-    if sanitize:
-        _run([HIPCC, *DEVICE_FLAGS, *HOST_SANITIZE_FLAGS, "-std=c++17", "-fPIC", "-shared", "-Wall",
-              f"-I{INCLUDE}", f"-I{CSRC}", *SOURCES, "-o", tmp], verbose)
-        os.replace(tmp, out)
-        return out
+    without the per-source flags (it never runs a kernel)."""
     from concurrent.futures import ThreadPoolExecutor
-    os.makedirs(OBJ_DIR, exist_ok=True)
-    objs = [os.path.join(OBJ_DIR, os.path.basename(src) + ".o") for src in SOURCES]
-    cmds = [[HIPCC, *DEVICE_FLAGS, "-O3", "-std=c++17", "-fPIC", "-Wall", f"-I{INCLUDE}", f"-I{CSRC}",
-             *SOURCE_FLAGS.get(os.path.basename(src), []), "-c", src, "-o", obj]
+    tmp = out + ".tmp"
+    obj_dir = os.path.join(os.path.dirname(SANITIZED_LIB), "obj") if sanitize else OBJ_DIR
+    os.makedirs(obj_dir, exist_ok=True)
+    flags = HOST_SANITIZE_FLAGS if sanitize else ["-O3"]
+    objs = [os.path.join(obj_dir, os.path.basename(src) + ".o") for src in SOURCES]
+    cmds = [[HIPCC, *DEVICE_FLAGS, *flags, "-std=c++17", "-fPIC", "-Wall", f"-I{INCLUDE}", f"-I{CSRC}",
+             *([] if sanitize else SOURCE_FLAGS.get(os.path.basename(src), [])), "-c", src, "-o", obj]
             for src, obj in zip(SOURCES, objs)]
     with ThreadPoolExecutor(max_workers=max(1, min(len(cmds), os.cpu_count() or 1, 8))) as pool:
         for f in [pool.submit(_run, c, verbose) for c in cmds]:
             f.result()
-    _run([HIPCC, *DEVICE_FLAGS, "-fPIC", "-shared", *objs, "-o", tmp], verbose)
+    _run([HIPCC, *DEVICE_FLAGS, *(HOST_SANITIZE_FLAGS if sanitize else []), "-fPIC", "-shared", *objs, "-o", tmp], verbose)
     os.replace(tmp, out)
     return out
 
