@@ -50,11 +50,11 @@ BackwardSpace backward_space(void *ws, int64_t T, int64_t N, int64_t D, int64_t 
   // (the states' part also serves the forward pass of a call without checkpoints)
   b.s = select_space(ws, T, D, G, S, g.numbers > forward || with_points ? g.numbers : forward);
   size_t at = b.s.bytes;
-  b.points = (float *)((char *)ws + at);
+  b.points = (float *)((uintptr_t)ws + at);
   if (!with_points) at += round256((size_t)chunk_numbers(T, N, 4) * S * D * 4);
-  b.shares = (float *)((char *)ws + at);
+  b.shares = (float *)((uintptr_t)ws + at);
   at += round256((size_t)g.blocks * T * 2 * P * 4);
-  b.sums = (float *)((char *)ws + at);
+  b.sums = (float *)((uintptr_t)ws + at);
   at += round256((size_t)g.numbers * (P + 2) * D * 4);
   b.bytes = at;
   return b;

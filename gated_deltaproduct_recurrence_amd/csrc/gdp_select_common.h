@@ -33,8 +33,9 @@ inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 // waves take them.  Few waves of uneven chunks leave compute units idle at the end otherwise.
 constexpr int64_t MOST_ORDERED = 1024;
 
-// The workspace's first part: B and C as float32, [T, G, 2, padded S]; then the chunks' states [numbers, padded S, D] and sums of steps
-// [numbers, D].
+// The workspace's first part: B and C as float32, [T, G, 2, padded S]; then the chunks'
+// states [numbers, padded S, D], sums of steps [numbers, D] and order.  (As numbers, not
+// pointers: the sizes are asked for without a workspace.)
 struct SelectSpace {
   float *bc, *states, *sums;
   int *order;  // [numbers], or null
@@ -43,7 +44,7 @@ struct SelectSpace {
 inline SelectSpace select_space(void *ws, int64_t T, int64_t D, int64_t G, int64_t S, int64_t numbers) {
   const int64_t P = padded_states(S);
   SelectSpace s;
-  char *p = (char *)ws;
+  const uintptr_t p = (uintptr_t)ws;
   size_t at = 0;
   s.bc = (float *)p;
   at += round256((size_t)T * G * 2 * P * 4);
@@ -76,9 +77,12 @@ template <int M, int N> struct Shared {
   }
   __device__ __forceinline__ void lay(float *lds) const {
     const int lane = threadIdx.x & 63;
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < EACH; ++i)
       if (M * N % 64 == 0 || lane + i * 64 < M * N) lds[lane + i * 64] = v[i];
+    // (a wave's LDS accesses are done in their order; this keeps the compiler to it)
+    __builtin_amdgcn_wave_barrier();
   }
 };
 
