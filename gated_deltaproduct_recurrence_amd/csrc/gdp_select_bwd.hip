@@ -20,6 +20,12 @@
 //
 // The time axis is cut into chunks as in the forward pass; the gradients that enter them
 // from behind come from two kernels before.
+//
+// Measured on MI355X, 8192 x 2048 in 4 sequences, 16 states, bfloat16 with a gate: 250 us, the
+// vector units busy 78% of the time (the kernels before it 70 and 7 us, the sums 20), at
+// 249 registers and two waves per SIMD.  With B and C as scalars, a barrier more and no loads
+// ahead it took 380 us.  1024 and 4096 workgroups wanted in place of 2048
+// cost the training step 9% and 3%, before B and C came out of LDS.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -329,7 +335,6 @@ gdp_select_backward_kernel(SelectArgs a, SelectGrid g, BackwardSpace b) {
       for (int n = 0; n < OWN; ++n) last[n] = live ? point[n] : 0.f;
       __syncthreads();
       if (AHEAD && t0 > k.begin) fetch(t0 - R);
-      // (B and C out of LDS: as scalars the training step of 4 x 2048 x 2048 took 692 us, not 584)
       auto four = [&](float (&x)[OWN], int r, int which) {
         const float4 v = *(const float4 *)(my_bc + (r * 2 + which) * P);
         x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
@@ -546,7 +551,7 @@ hipError_t launch_select_backward(const SelectArgs &given, int ut, int dt, hipSt
         hipLaunchKernelGGL((gdp_select_starts_kernel<UT, DT, P>), dim3((unsigned)((jobs + WAVES - 1) / WAVES)),
                            dim3(64 * WAVES), 0, stream, a, g, b.s, jobs);
         if (hipError_t e = hipGetLastError()) return e;
-        const dim3 lanes((unsigned)(((int64_t)P * a.D + 255) / 256), (unsigned)(a.N < 256 ? a.N : 256));
+        const dim3 lanes((unsigned)(((int64_t)P * a.D + 255) / 256), (unsigned)(a.N < 32 ? a.N : 32));
         hipLaunchKernelGGL(gdp_select_behind_kernel<P>, lanes, dim3(256), 0, stream, a, g, b.s);
         if (hipError_t e = hipGetLastError()) return e;
       }

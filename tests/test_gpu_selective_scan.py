@@ -119,6 +119,19 @@ def test_rows_outside_the_sequences(gdp):
     check(gdp, make([20, 0, 90], 40, 16, BF16, F32, seed=6, start=11, extra=70))
 
 
+def test_rows_without_any_sequence(gdp):
+    check(gdp, make([], 40, 16, BF16, F32, seed=19, extra=300))
+    check(gdp, make([0, 0], 40, 16, BF16, F32, seed=19, start=30, extra=300))
+
+
+@pytest.mark.parametrize("D", [1280, 2600])
+def test_uneven_sequences_in_their_order_of_length(gdp, D):
+    """Enough waves and sequences for the long chunks to be taken first, of many lengths, empty ones among them."""
+    gen = torch.Generator().manual_seed(20)
+    lens = torch.randint(0, 90, (60,), generator=gen).tolist() + [0, 700, 1, 0]
+    check(gdp, make(lens, D, 2, F32, seed=20))
+
+
 def test_one_long_sequence(gdp):
     """More chunks than the walks over them read ahead."""
     check(gdp, make([1500], 20, 4, F32, seed=7))

@@ -111,6 +111,11 @@ def test_rows_outside_the_sequences(gdp):
     check(gdp, make([20, 0, 30], 40, 4, BF16, seed=8, start=11, extra=200), "silu")
 
 
+def test_rows_without_any_sequence(gdp):
+    check(gdp, make([], 40, 4, BF16, seed=18, extra=300), "silu")
+    check(gdp, make([0, 0], 40, 4, BF16, seed=18, start=30, extra=300), "silu")
+
+
 def test_long_chunks(gdp):
     """Enough rows and channels for the longest chunks."""
     d = make([700, 1, 0, 12000, 3586], 2056, 4, BF16, seed=9)
