@@ -328,8 +328,9 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_conv_backward_kernel(ConvArgs 
   if (a.db) store_floats<float, VEC>(sums + (int64_t)W * a.D, ch, a.D, db);
 }
 
-// log2 of the rows per chunk
-constexpr int FORWARD_SHIFT = 4;
+// log2 of the rows per chunk: 16, or 8 (at least the W - 1 rows before it) where that
+// leaves fewer than 2048 waves
+int forward_shift(int64_t T, int64_t blocks) { return (T >> 4) * blocks < 2048 ? 3 : 4; }
 // ... of the gradients: 128, or fewer down to 16 for at least 4096 waves
 int backward_shift(int64_t T, int64_t blocks) {
   int shift = 7;
@@ -376,14 +377,15 @@ hipError_t launch_conv(const ConvArgs &a, int xt, hipStream_t stream) {
     using T = decltype(x);
     constexpr int VEC = FORWARD_VEC / sizeof(T);
     const int64_t blocks = blocks_of(a.D, VEC);
-    const int64_t jobs = chunk_numbers(a.T, a.N, FORWARD_SHIFT) * blocks;
+    const int shift = forward_shift(a.T, blocks);
+    const int64_t jobs = chunk_numbers(a.T, a.N, shift) * blocks;
     if (jobs == 0 || a.N == 0) return hipSuccess;
     const bool streamed = (int64_t)a.T * a.D * 2 * (int64_t)sizeof(T) > STREAM_BYTES;
     return by_taps(a.W, [&](auto w) {
       auto *kernel = streamed ? gdp_conv_kernel<T, decltype(w)::value, VEC, true>
                               : gdp_conv_kernel<T, decltype(w)::value, VEC, false>;
-      hipLaunchKernelGGL(kernel, dim3((unsigned)((jobs + WAVES - 1) / WAVES)), dim3(64 * WAVES), 0, stream, a,
-                         FORWARD_SHIFT, (int)blocks, (int)jobs);
+      hipLaunchKernelGGL(kernel, dim3((unsigned)((jobs + WAVES - 1) / WAVES)), dim3(64 * WAVES), 0, stream, a, shift,
+                         (int)blocks, (int)jobs);
       return hipGetLastError();
     });
   });

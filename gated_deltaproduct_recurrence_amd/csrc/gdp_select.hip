@@ -143,9 +143,7 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_ends_kernel(SelectArgs 
   const int ch = p.ch;
   float A2[P], h[P];
   load_rates<P>(A2, a, ch);
-#pragma unroll
-  for (int n = 0; n < P; ++n)
-    h[n] = a.s0 && p.k.index == 0 && n < a.S ? a.s0[((int64_t)p.k.seq * a.D + ch) * a.S + n] : 0.f;
+  load_states<P>(h, a.s0 && p.k.index == 0 ? a.s0 + ((int64_t)p.k.seq * a.D + ch) * a.S : nullptr, a.S);
   const float bias = a.bias ? a.bias[ch] : 0.f;
   float *mine = lds[threadIdx.x >> 6];
   const float *bc = s.bc + ((int64_t)p.k.begin * a.G + p.group) * 2 * P;
@@ -205,24 +203,21 @@ __global__ void __launch_bounds__(256) gdp_select_enter_kernel(SelectArgs a, Sel
     const float *sum = s.sums + number * a.D + ch;
     float h = *state;
     constexpr int AHEAD = 8;
-    int64_t c = 1;
-    for (; c + AHEAD < chunks; c += AHEAD) {
+    for (int64_t c = 1; c < chunks; c += AHEAD) {
       float end[AHEAD], d[AHEAD];
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
-        end[j] = state[(c + j) * step];
-        d[j] = sum[(c + j) * a.D];
+        end[j] = d[j] = 0.f;
+        if (c + j + 1 < chunks) {  // (behind the last chunk's entry nothing is needed)
+          end[j] = state[(c + j) * step];
+          d[j] = sum[(c + j) * a.D];
+        }
       }
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
-        state[(c + j) * step] = h;
+        if (c + j < chunks) state[(c + j) * step] = h;
         h = fmaf(__builtin_amdgcn_exp2f(A2 * d[j]), h, end[j]);
       }
-    }
-    for (; c < chunks; ++c) {
-      const float end = c + 1 < chunks ? state[c * step] : 0.f, d = c + 1 < chunks ? sum[c * a.D] : 0.f;
-      state[c * step] = h;
-      h = fmaf(__builtin_amdgcn_exp2f(A2 * d), h, end);
     }
   }
 }
@@ -242,8 +237,7 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
 #pragma unroll
     for (int n = 0; n < P; ++n) h[n] = enter[(int64_t)n * a.D];
   } else {
-#pragma unroll
-    for (int n = 0; n < P; ++n) h[n] = a.s0 && n < a.S ? a.s0[((int64_t)k.seq * a.D + ch) * a.S + n] : 0.f;
+    load_states<P>(h, a.s0 ? a.s0 + ((int64_t)k.seq * a.D + ch) * a.S : nullptr, a.S);
   }
   if (k.begin < k.end) {
     const float bias = a.bias ? a.bias[ch] : 0.f, skip = a.skip ? a.skip[ch] : 0.f;
@@ -321,18 +315,10 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
     }
   }
   if (k.end != k.last || !p.live) return;
-  if (a.final_state) {
-#pragma unroll
-    for (int n = 0; n < P; ++n)
-      if (n < a.S) a.final_state[((int64_t)k.seq * a.D + ch) * a.S + n] = h[n];
-  }
+  if (a.final_state) store_states<P>(a.final_state + ((int64_t)k.seq * a.D + ch) * a.S, h, a.S);
   if (a.cache) {
     const int64_t slot = index_at(a.slots, a.slots_is64, k.seq);
-    if (slot >= 0 && slot < a.num_slots) {
-#pragma unroll
-      for (int n = 0; n < P; ++n)
-        if (n < a.S) a.cache[(slot * a.D + ch) * a.S + n] = h[n];
-    }
+    if (slot >= 0 && slot < a.num_slots) store_states<P>(a.cache + (slot * a.D + ch) * a.S, h, a.S);
   }
 }
 

@@ -88,9 +88,7 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_starts_kernel(SelectArg
   if (!find_chunk(&k, a.cu, a.cu_is64, a.T, a.N, g.shift, number) || k.index == 0) return;
   float A2[P], e[P];
   load_rates<P>(A2, a, ch);
-#pragma unroll
-  for (int n = 0; n < P; ++n)
-    e[n] = k.end == k.last && a.dfinal && n < a.S ? a.dfinal[((int64_t)k.seq * a.D + ch) * a.S + n] : 0.f;
+  load_states<P>(e, k.end == k.last && a.dfinal ? a.dfinal + ((int64_t)k.seq * a.D + ch) * a.S : nullptr, a.S);
   const float bias = a.bias ? a.bias[ch] : 0.f;
   const bool gate = a.z != nullptr;
   // rows t, t - 1, ..
@@ -186,24 +184,21 @@ __global__ void __launch_bounds__(256) gdp_select_behind_kernel(SelectArgs a, Se
     const float *sum = s.sums + number * a.D + ch;
     float e = state[(chunks - 1) * step];
     constexpr int AHEAD = 8;
-    int64_t c = chunks - 2;
-    for (; c - AHEAD >= 0; c -= AHEAD) {  // chunk 0 is left to the loop behind
+    for (int64_t c = chunks - 2; c >= 0; c -= AHEAD) {
       float own[AHEAD], d[AHEAD];
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
-        own[j] = state[(c - j) * step];
-        d[j] = sum[(c - j) * a.D];
+        own[j] = d[j] = 0.f;
+        if (c - j > 0) {  // (before chunk 0 nothing is needed)
+          own[j] = state[(c - j) * step];
+          d[j] = sum[(c - j) * a.D];
+        }
       }
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
-        state[(c - j) * step] = e;
+        if (c - j >= 0) state[(c - j) * step] = e;
         e = fmaf(__builtin_amdgcn_exp2f(A2 * d[j]), e, own[j]);
       }
-    }
-    for (; c >= 0; --c) {
-      const float own = c > 0 ? state[c * step] : 0.f, d = c > 0 ? sum[c * a.D] : 0.f;
-      state[c * step] = e;
-      e = fmaf(__builtin_amdgcn_exp2f(A2 * d), e, own);
     }
   }
 }

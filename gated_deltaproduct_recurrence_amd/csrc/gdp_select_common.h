@@ -105,10 +105,35 @@ __device__ __forceinline__ float softplus_of(float v) {
   return __builtin_amdgcn_fmed3f(v, 0.f, __builtin_inff()) + log1p_of(__builtin_amdgcn_exp2f(-fabsf(v) * LOG2E_L));
 }
 
+// a channel's S states in a row of memory, or (null) zeros; zeros behind the last one
+template <int P> __device__ __forceinline__ void load_states(float (&x)[P], const float *p, int S) {
+  if (p && S == P) {
+#pragma unroll
+    for (int n = 0; n < P; n += 4) {
+      const Piece<float, 4> v = *(const Piece<float, 4> *)(p + n);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[n + c] = v.v[c];
+    }
+  } else {
+#pragma unroll
+    for (int n = 0; n < P; ++n) x[n] = p && n < S ? p[n] : 0.f;
+  }
+}
+template <int P> __device__ __forceinline__ void store_states(float *p, const float (&x)[P], int S) {
+  if (S == P) {
+#pragma unroll
+    for (int n = 0; n < P; n += 4) *(Piece<float, 4> *)(p + n) = Piece<float, 4>{{x[n], x[n + 1], x[n + 2], x[n + 3]}};
+  } else {
+#pragma unroll
+    for (int n = 0; n < P; ++n)
+      if (n < S) p[n] = x[n];
+  }
+}
 // A[ch] as base-2 exponents; zeros behind the last state
 template <int P> __device__ __forceinline__ void load_rates(float (&A2)[P], const SelectArgs &a, int ch) {
+  load_states<P>(A2, a.A + (int64_t)ch * a.S, a.S);
 #pragma unroll
-  for (int n = 0; n < P; ++n) A2[n] = n < a.S ? a.A[(int64_t)ch * a.S + n] * LOG2E_L : 0.f;
+  for (int n = 0; n < P; ++n) A2[n] *= LOG2E_L;
 }
 
 template <typename F> hipError_t select_types(int ut, int dt, F f) {
