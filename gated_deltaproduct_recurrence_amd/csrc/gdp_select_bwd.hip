@@ -52,10 +52,13 @@ struct BackwardSpace {
 BackwardSpace backward_space(void *ws, int64_t T, int64_t N, int64_t D, int64_t G, int64_t S, const SelectGrid &g,
                              bool with_points) {
   BackwardSpace b;
-  const int64_t P = padded_states(S), forward = forward_grid(T, N, D, G).numbers;
-  // (the states' part also serves the forward pass of a call without checkpoints)
-  b.s = select_space(ws, T, D, G, S, g.numbers > forward || with_points ? g.numbers : forward);
+  const int64_t P = padded_states(S);
+  b.s = select_space(ws, T, D, G, S, g.numbers);
   size_t at = b.s.bytes;
+  if (!with_points) {  // the forward pass's space comes first, in the same place
+    const size_t forward = select_space(ws, T, D, G, S, forward_grid(T, N, D, G).numbers).bytes;
+    at = forward > at ? forward : at;
+  }
   b.points = (float *)((uintptr_t)ws + at);
   if (!with_points) at += round256((size_t)chunk_numbers(T, N, 4) * S * D * 4);
   b.shares = (float *)((uintptr_t)ws + at);
