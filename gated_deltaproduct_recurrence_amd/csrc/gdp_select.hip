@@ -8,8 +8,7 @@
 // What bounds it is the vector units: per element and state one exponential and four
 // float32 operations, against 6 to 10 bytes per element.  So a lane holds a channel
 // with all its states in registers, and B_t and C_t, the same for a whole wave, come to it
-// from the wave's own LDS, four states per read.  A first kernel lays them out for
-// that (float32, zeros behind the last state, whatever their type and alignment).
+// from the wave's own LDS, four states per read.
 //
 // The time axis: a wave walks one chunk of a sequence (gdp_block_common.h).  Where a call has few
 // channels and long sequences, chunks are short enough to fill the chip, and the
@@ -21,9 +20,10 @@
 // Measured on MI355X, 16 states, bfloat16 with a gate.  An exponential takes two issue slots
 // and everything else one (counters), so a row of 64 channels has 138 slots in the main kernel
 // and 104 in the one before it; the vector units are busy 93% of the time in both on 32768 x 2048
-// in one sequence (278 + 207 us, the call 456 us).  33824 x 4096 in 68 sequences of 1 to 1024
-// rows: 563 us; 812 x 512 in 4: 33 us, latency of four launches.
-//   B and C as scalar operands missed the scalar cache row by row: 575 us on the first shape.
+// in one sequence (277 + 207 us, the call 444 us).  33824 x 4096 in 68 sequences of 1 to 1024
+// rows: 547 us; 812 x 512 in 4: 25 us, latency of three launches.
+//   B and C as scalar operands missed the scalar cache row by row: 575 us on the first shape,
+// and a kernel before that laid them out as floats cost every call 3 to 7 us.
 //   Without the order by length, and with chunks for 4096 waves, the second took 1036 us.
 //   delta u B added by a matrix instruction (one for four states) saves 12 slots per row
 // and was no faster: 466 us and 587.
@@ -42,55 +42,45 @@ namespace {
 
 constexpr int WAVES = 4, ROWS = 4;  // waves per workgroup (or one), rows in flight
 
-// B and C rows as float32 behind each other, zeros behind the last state; the last
-// workgroup sorts the chunk numbers by their chunks' lengths, in 64 classes, longest first
-// (those that name no chunk last).  Within a class they stand as their counters
-// give them, which changes no result.
-template <typename T>
-__global__ void __launch_bounds__(256) gdp_select_stage_kernel(SelectArgs a, float *bc, int P, int shift, int numbers,
-                                                               int *order) {
-  if (order && blockIdx.x == gridDim.x - 1) {
-    __shared__ int count[64], start[64];
-    constexpr int EACH = (int)(MOST_ORDERED / 256);
-    int cls[EACH];
-    if (threadIdx.x < 64) count[threadIdx.x] = 0;
-    __syncthreads();
-    for (int j = 0; j < EACH; ++j) {
-      const int number = j * 256 + threadIdx.x;
-      cls[j] = -1;
-      if (number >= numbers) continue;
-      int lo = 0, hi = a.N;  // the last sequence whose numbers begin at or before it
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (((int)bound_at(a.cu, a.cu_is64, mid, a.T) >> shift) + mid <= number) lo = mid;
-        else hi = mid;
-      }
-      const int first = (int)bound_at(a.cu, a.cu_is64, lo, a.T), last = (int)bound_at(a.cu, a.cu_is64, lo + 1, a.T);
-      const int64_t at = (int64_t)(number - (first >> shift) - lo) << shift, left = at < 0 ? 0 : last - first - at;
-      const int64_t rows = left < 0 ? 0 : (left < (int64_t)1 << shift ? left : (int64_t)1 << shift);
-      cls[j] = 63 - (int)(rows * 63 >> shift);
-      atomicAdd(&count[cls[j]], 1);
+// Sorts the chunk numbers by their chunks' lengths, in 64 classes, longest first (those that
+// name no chunk last).  Within a class they stand as their counters give them,
+// which changes no result.
+__global__ void __launch_bounds__(256) gdp_select_order_kernel(SelectArgs a, int shift, int numbers, int *order) {
+  __shared__ int count[64], start[64];
+  constexpr int EACH = (int)(MOST_ORDERED / 256);
+  int cls[EACH];
+  if (threadIdx.x < 64) count[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < EACH; ++j) {
+    const int number = j * 256 + threadIdx.x;
+    cls[j] = -1;
+    if (number >= numbers) continue;
+    int lo = 0, hi = a.N;  // the last sequence whose numbers begin at or before it
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (((int)bound_at(a.cu, a.cu_is64, mid, a.T) >> shift) + mid <= number) lo = mid;
+      else hi = mid;
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int sum = 0;
-      for (int c = 0; c < 64; ++c) {
-        start[c] = sum;
-        sum += count[c];
-      }
+    const int first = (int)bound_at(a.cu, a.cu_is64, lo, a.T), last = (int)bound_at(a.cu, a.cu_is64, lo + 1, a.T);
+    const int64_t at = (int64_t)(number - (first >> shift) - lo) * ((int64_t)1 << shift);
+    const int64_t left = at < 0 ? 0 : last - first - at;
+    const int64_t rows = left < 0 ? 0 : (left < (int64_t)1 << shift ? left : (int64_t)1 << shift);
+    cls[j] = 63 - (int)(rows * 63 >> shift);
+    atomicAdd(&count[cls[j]], 1);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int sum = 0;
+    for (int c = 0; c < 64; ++c) {
+      start[c] = sum;
+      sum += count[c];
     }
-    __syncthreads();
-    for (int j = 0; j < EACH; ++j)
-      if (cls[j] >= 0) order[atomicAdd(&start[cls[j]], 1)] = j * 256 + threadIdx.x;
-    return;
   }
-  const int64_t all = (int64_t)a.T * a.G * 2 * P, step = (int64_t)(gridDim.x - (order ? 1 : 0)) * 256;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
-    const int n = (int)(i & (P - 1)), which = (int)(i / P & 1);
-    const int64_t row = i / (2 * P), t = row / a.G, g = row % a.G;
-    const T *p = which ? (const T *)a.C + t * a.C_st + g * a.C_sg : (const T *)a.B + t * a.B_st + g * a.B_sg;
-    bc[i] = n < a.S ? (float)p[n] : 0.f;
-  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < EACH; ++j)
+    if (cls[j] >= 0) order[atomicAdd(&start[cls[j]], 1)] = j * 256 + threadIdx.x;
 }
 
 // A wave's chunk and channels
@@ -146,21 +136,18 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_ends_kernel(SelectArgs 
   load_states<P>(h, a.s0 && p.k.index == 0 ? a.s0 + ((int64_t)p.k.seq * a.D + ch) * a.S : nullptr, a.S);
   const float bias = a.bias ? a.bias[ch] : 0.f;
   float *mine = lds[threadIdx.x >> 6];
-  const float *bc = s.bc + ((int64_t)p.k.begin * a.G + p.group) * 2 * P;
-  const int64_t bc_st = (int64_t)a.G * 2 * P;
   Rows<UT, DT, ROWS> next = {};
-  Shared<ROWS, P> next_b;
+  Shared<UT, ROWS, P, 0> next_b;
   next.load(a, p.k.begin, ch, false);
-  next_b.load(bc, bc_st);
+  next_b.load(a, p.group, p.k.begin, 1);
   float sum = 0.f;
   // (a chunk that another follows is full: a multiple of ROWS rows)
   for (int t = p.k.begin; t < p.k.end; t += ROWS) {
     const Rows<UT, DT, ROWS> now = next;
     next_b.lay(mine);
-    bc += ROWS * bc_st;
     if (t + ROWS < p.k.end) {
       next.load(a, t + ROWS, ch, false);
-      next_b.load(bc, bc_st);
+      next_b.load(a, p.group, t + ROWS, 1);
     }
     float delta[ROWS], part = 0.f;
     now.steps(delta, bias, a.softplus);
@@ -243,8 +230,6 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
     const float bias = a.bias ? a.bias[ch] : 0.f, skip = a.skip ? a.skip[ch] : 0.f;
     const bool gate = a.z != nullptr;
     float *mine = lds[threadIdx.x >> 6];
-    const float *bc = s.bc + ((int64_t)k.begin * a.G + p.group) * 2 * P;
-    const int64_t bc_st = (int64_t)a.G * 2 * P;
     UT *o = (UT *)a.o + k.begin * a.o_st + ch;
     // M rows of the recurrence
     auto run = [&](const auto &x) {
@@ -278,11 +263,11 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
       o += M * a.o_st;
     };
     Rows<UT, DT, ROWS> next = {};
-    Shared<ROWS, 2 * P> next_bc;
+    Shared<UT, ROWS, P, 2> next_bc;
     const int whole = k.begin + ((k.end - k.begin) & ~(ROWS - 1));
     if (k.begin < whole) {
       next.load(a, k.begin, ch, gate);
-      next_bc.load(bc, bc_st);
+      next_bc.load(a, p.group, k.begin, 1);
     }
     auto point = [&](int t) {  // before row t, the first of 16
       const int64_t at = (k.first / SELECT_ROWS) + k.seq + (t - k.first) / SELECT_ROWS;
@@ -296,21 +281,19 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
       if (a.points && ((t - k.begin) & (SELECT_ROWS - 1)) == 0) point(t);
       const Rows<UT, DT, ROWS> now = next;
       next_bc.lay(mine);
-      bc += ROWS * bc_st;
       if (t + ROWS < whole) {
         next.load(a, t + ROWS, ch, gate);
-        next_bc.load(bc, bc_st);
+        next_bc.load(a, p.group, t + ROWS, 1);
       }
       run(now);
     }
     if (a.points && t < k.end && ((t - k.begin) & (SELECT_ROWS - 1)) == 0) point(t);
     for (; t < k.end; ++t) {
       Rows<UT, DT, 1> one = {};
-      Shared<1, 2 * P> one_bc;
+      Shared<UT, 1, P, 2> one_bc;
       one.load(a, t, ch, gate);
-      one_bc.load(bc, bc_st);
+      one_bc.load(a, p.group, t, 1);
       one_bc.lay(mine);
-      bc += bc_st;
       run(one);
     }
   }
@@ -375,32 +358,23 @@ bool select_served(int64_t T, int64_t N, int64_t D, int64_t G, int64_t S) {
 }
 
 size_t select_bytes(int64_t T, int64_t N, int64_t D, int64_t G, int64_t S) {
-  return select_space(nullptr, T, D, G, S, forward_grid(T, N, D, G).numbers).bytes;
-}
-
-hipError_t launch_select_stage(const SelectArgs &a, int ut, const SelectGrid &g, const SelectSpace &s,
-                               hipStream_t stream) {
-  const int P = padded_states(a.S);
-  int64_t want = ((int64_t)a.T * a.G * 2 * P + 255) / 256;
-  want = (want < 4096 ? want : 4096) + (s.order ? 1 : 0);
-  if (want == 0) return hipSuccess;
-  auto *kernel = ut == EL_F32 ? gdp_select_stage_kernel<float>
-                              : (ut == EL_BF16 ? gdp_select_stage_kernel<bf16> : gdp_select_stage_kernel<_Float16>);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)want), dim3(256), 0, stream, a, s.bc, P, g.shift, (int)g.numbers, s.order);
-  return hipGetLastError();
+  return select_space(nullptr, D, S, forward_grid(T, N, D, G).numbers).bytes;
 }
 
 hipError_t launch_select(const SelectArgs &a, int ut, int dt, hipStream_t stream) {
   const SelectGrid g = forward_grid(a.T, a.N, a.D, a.G);
   const int64_t jobs = g.numbers * g.blocks;
   if (jobs == 0 || a.N == 0) return hipSuccess;
-  SelectSpace s = select_space(a.ws, a.T, a.D, a.G, a.S, g.numbers);
+  SelectSpace s = select_space(a.ws, a.D, a.S, g.numbers);
   // one wave per workgroup while that leaves compute units without one: 812 rows of 512
   // channels take 40 us so and 44 with four, 32768 of 2048 take 495 and 462
   const int waves = jobs <= 1024 ? 1 : WAVES;
   // (the chunks of one sequence stand in order, and few waves all run at once)
   if (a.N == 1 || waves == 1) s.order = nullptr;
-  if (hipError_t e = launch_select_stage(a, ut, g, s, stream)) return e;
+  if (s.order) {
+    hipLaunchKernelGGL(gdp_select_order_kernel, dim3(1), dim3(256), 0, stream, a, g.shift, (int)g.numbers, s.order);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
   return select_types(ut, dt, [&](auto u, auto d) {
     using UT = decltype(u);
     using DT = decltype(d);

@@ -23,7 +23,7 @@
 //
 // Measured on MI355X, 8192 x 2048 in 4 sequences, 16 states, bfloat16 with a gate: 250 us, the
 // vector units busy 78% of the time (the kernels before it 70 and 7 us, the sums 20), at
-// 249 registers and two waves per SIMD.  With B and C as scalars, a barrier more and no loads
+// 250 registers and two waves per SIMD.  With B and C as scalars, a barrier more and no loads
 // ahead it took 380 us.  1024 and 4096 workgroups wanted in place of 2048
 // cost the training step 9% and 3%, before B and C came out of LDS.
 
@@ -53,10 +53,10 @@ BackwardSpace backward_space(void *ws, int64_t T, int64_t N, int64_t D, int64_t 
                              bool with_points) {
   BackwardSpace b;
   const int64_t P = padded_states(S);
-  b.s = select_space(ws, T, D, G, S, g.numbers);
+  b.s = select_space(ws, D, S, g.numbers);
   size_t at = b.s.bytes;
   if (!with_points) {  // the forward pass's space comes first, in the same place
-    const size_t forward = select_space(ws, T, D, G, S, forward_grid(T, N, D, G).numbers).bytes;
+    const size_t forward = select_space(ws, D, S, forward_grid(T, N, D, G).numbers).bytes;
     at = forward > at ? forward : at;
   }
   b.points = (float *)((uintptr_t)ws + at);
@@ -104,8 +104,6 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_starts_kernel(SelectArg
       if (gate) x.z[r] = ((const UT *)a.z)[(t - r) * a.z_st + ch];
     }
   };
-  const float *bc = s.bc + ((int64_t)(k.end - 1) * a.G + group) * 2 * P + P;  // C of the row
-  const int64_t bc_st = (int64_t)a.G * 2 * P;
   float sum = 0.f;
   auto run = [&](const auto &x) {
     constexpr int M = sizeof(x.d_o) / sizeof(UT);
@@ -139,28 +137,26 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_starts_kernel(SelectArg
   };
   int t = k.end - 1;
   Back<UT, DT, ROWS> next = {};
-  Shared<ROWS, P> next_c;
+  Shared<UT, ROWS, P, 1> next_c;
   if (t - ROWS + 1 >= k.begin) {
     load(next, t);
-    next_c.load(bc, -bc_st);
+    next_c.load(a, group, t, -1);
   }
   for (; t - ROWS + 1 >= k.begin; t -= ROWS) {
     const Back<UT, DT, ROWS> now = next;
     next_c.lay(mine);
-    bc -= ROWS * bc_st;
     if (t - 2 * ROWS + 1 >= k.begin) {
       load(next, t - ROWS);
-      next_c.load(bc, -bc_st);
+      next_c.load(a, group, t - ROWS, -1);
     }
     run(now);
   }
   for (; t >= k.begin; --t) {
     Back<UT, DT, 1> one = {};
-    Shared<1, P> one_c;
+    Shared<UT, 1, P, 1> one_c;
     load(one, t);
-    one_c.load(bc, -bc_st);
+    one_c.load(a, group, t, -1);
     one_c.lay(mine);
-    bc -= bc_st;
     run(one);
   }
   if (at >= per) return;
@@ -275,12 +271,15 @@ gdp_select_backward_kernel(SelectArgs a, SelectGrid g, BackwardSpace b) {
     constexpr bool AHEAD = MINE <= 4;
     UT u_[MINE] = {}, z_[MINE] = {}, do_[MINE] = {};
     DT dt_[MINE] = {};
-    float point[OWN] = {}, bc_[2] = {};
+    float point[OWN] = {};
+    UT bc_[2] = {};  // 2 P values per row: two of a block's per lane of the workgroup, HALF rows apart
+    const Shares<UT> mine_bc = shares_of<UT>(a, threadIdx.x / P & 1, group);
+    const int bc_n = threadIdx.x % P, bc_r = threadIdx.x / (2 * P);
     auto fetch = [&](int t0) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {  // 2 P floats per row: two per lane of the workgroup
-        const int q = threadIdx.x + i * 64 * W, r = q / (2 * P);
-        if (t0 + r < k.end) bc_[i] = b.s.bc[((int64_t)(t0 + r) * a.G + group) * 2 * P + q % (2 * P)];
+      for (int i = 0; i < 2; ++i) {
+        const int64_t t = t0 + bc_r + i * HALF;
+        if (t < k.end && bc_n < a.S) bc_[i] = mine_bc.p[t * mine_bc.st + bc_n];
       }
 #pragma unroll
       for (int i = 0; i < MINE; ++i) {
@@ -327,7 +326,7 @@ gdp_select_backward_kernel(SelectArgs a, SelectGrid g, BackwardSpace b) {
         tile.ds[r][lane] = ds;
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) (&tile.bc[0][0][0])[threadIdx.x + i * 64 * W] = bc_[i];
+      for (int i = 0; i < 2; ++i) (&tile.bc[0][0][0])[threadIdx.x + i * 64 * W] = (float)bc_[i];
       float h[R][OWN], d[R][OWN], last[OWN];  // states before the rows, decays; the state behind the block
 #pragma unroll
       for (int n = 0; n < OWN; ++n) last[n] = live ? point[n] : 0.f;
@@ -528,17 +527,10 @@ hipError_t launch_select_backward(const SelectArgs &given, int ut, int dt, hipSt
   SelectArgs a = given;
   const SelectGrid g = backward_grid(a.T, a.N, a.D, a.G);
   const BackwardSpace b = backward_space(a.ws, a.T, a.N, a.D, a.G, a.S, g, a.points != nullptr);
-  hipError_t e;
-  if (a.points) {
-    SelectSpace stage = b.s;
-    stage.order = nullptr;
-    e = launch_select_stage(a, ut, g, stage, stream);
-  } else {  // the checkpoints again, into the workspace (which begins as the forward pass's)
+  if (!a.points) {  // the checkpoints again, into the workspace (which begins as the forward pass's)
     a.points = b.points;
-    e = launch_select(a, ut, dt, stream);
-    // (with no sequence it does nothing, and no chunk reads B and C)
+    if (hipError_t e = launch_select(a, ut, dt, stream)) return e;
   }
-  if (e != hipSuccess) return e;
   const int64_t jobs = g.numbers * g.blocks;
   return select_types(ut, dt, [&](auto u, auto d) {
     using UT = decltype(u);

@@ -33,23 +33,20 @@ inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 // waves take them.  Few waves of uneven chunks leave compute units idle at the end otherwise.
 constexpr int64_t MOST_ORDERED = 1024;
 
-// The workspace's first part: B and C as float32, [T, G, 2, padded S]; then the chunks'
-// states [numbers, padded S, D], sums of steps [numbers, D] and order.  (As numbers, not
-// pointers: the sizes are asked for without a workspace.)
+// The workspace's first part: the chunks' states [numbers, padded S, D], sums of steps
+// [numbers, D] and order.  (As numbers, not pointers: the sizes are asked for without a
+// workspace.)
 struct SelectSpace {
-  float *bc, *states, *sums;
+  float *states, *sums;
   int *order;  // [numbers], or null
   size_t bytes;
 };
-inline SelectSpace select_space(void *ws, int64_t T, int64_t D, int64_t G, int64_t S, int64_t numbers) {
-  const int64_t P = padded_states(S);
+inline SelectSpace select_space(void *ws, int64_t D, int64_t S, int64_t numbers) {
   SelectSpace s;
   const uintptr_t p = (uintptr_t)ws;
   size_t at = 0;
-  s.bc = (float *)p;
-  at += round256((size_t)T * G * 2 * P * 4);
-  s.states = (float *)(p + at);
-  at += round256((size_t)numbers * P * D * 4);
+  s.states = (float *)p;
+  at += round256((size_t)numbers * padded_states(S) * D * 4);
   s.sums = (float *)(p + at);
   at += round256((size_t)numbers * D * 4);
   s.order = nullptr;
@@ -61,26 +58,35 @@ inline SelectSpace select_space(void *ws, int64_t T, int64_t D, int64_t G, int64
   return s;
 }
 
-// N floats of each of M rows (`stride` apart), held by a wave until it lays them into its
-// own LDS, [M, N], where every lane reads all of them.  (As scalar loads they miss the
-// scalar cache row by row, 600 cycles each, and every wait is one for all of them.)
-template <int M, int N> struct Shared {
-  static constexpr int EACH = (M * N + 63) / 64;
-  float v[EACH];
-  __device__ __forceinline__ void load(const float *p, int64_t stride) {
-    const int lane = threadIdx.x & 63;
+// Row t of a group's B or C, element n
+template <typename T> struct Shares {
+  const T *p; int64_t st;
+};
+template <typename T> __device__ __forceinline__ Shares<T> shares_of(const SelectArgs &a, int which, int group) {
+  return which ? Shares<T>{(const T *)a.C + group * a.C_sg, a.C_st} : Shares<T>{(const T *)a.B + group * a.B_sg, a.B_st};
+}
+
+// M rows of B (WHICH 0), C (1) or both (2), held by a wave until it lays them as floats,
+// with zeros behind the last state, into its own LDS, [M, P] or [M, 2, P], where every lane
+// reads all of them.  (As scalar loads they miss the scalar cache row by row, 600 cycles
+// each, and every wait is one for all of them.)
+template <typename T, int M, int P, int WHICH> struct Shared {
+  static constexpr int N = WHICH == 2 ? 2 * P : P, EACH = (M * N + 63) / 64, STEP = 64 / N;  // STEP: rows between a lane's
+  T v[EACH];
+  // rows t, t + dir, ..
+  __device__ __forceinline__ void load(const SelectArgs &a, int group, int64_t t, int dir) {
+    const int lane = threadIdx.x & 63, n = lane % P;
+    const Shares<T> s = shares_of<T>(a, WHICH == 2 ? lane / P & 1 : WHICH, group);
+    const bool on = n < a.S && (M * N >= 64 || lane < M * N);
 #pragma unroll
-    for (int i = 0; i < EACH; ++i) {
-      const int at = min(lane + i * 64, M * N - 1);
-      v[i] = p[at / N * stride + at % N];
-    }
+    for (int i = 0; i < EACH; ++i) v[i] = on ? s.p[(t + dir * (lane / N + i * STEP)) * s.st + n] : (T)0.f;
   }
   __device__ __forceinline__ void lay(float *lds) const {
     const int lane = threadIdx.x & 63;
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
     for (int i = 0; i < EACH; ++i)
-      if (M * N % 64 == 0 || lane + i * 64 < M * N) lds[lane + i * 64] = v[i];
+      if (M * N >= 64 || lane < M * N) lds[lane + i * 64] = (float)v[i];
     // (a wave's LDS accesses are done in their order; this keeps the compiler to it)
     __builtin_amdgcn_wave_barrier();
   }
@@ -165,8 +171,4 @@ inline SelectGrid forward_grid(int64_t T, int64_t N, int64_t D, int64_t G) {
 inline SelectGrid backward_grid(int64_t T, int64_t N, int64_t D, int64_t G) {
   return select_grid(T, N, D, G, 2048, 6, 11);
 }
-// B and C into the workspace, and the chunks' order
-hipError_t launch_select_stage(const SelectArgs &a, int u_type, const SelectGrid &g, const SelectSpace &s,
-                               hipStream_t stream);
-
 }  // namespace gdp

@@ -544,8 +544,8 @@ int gdp_short_conv_backward(const gdp_tensor *x, const gdp_tensor *weight, const
 /* Rows of a sequence per checkpoint of the selective scan. */
 #define GDP_SELECT_CHECKPOINT_ROWS 16
 
-/* Host-only.  Workspace bytes gdp_selective_scan needs: B and C as float32, and the states
- * at the ends of pieces of long sequences.  0 for invalid sizes. */
+/* Host-only.  Workspace bytes gdp_selective_scan needs: the states at the ends of pieces of
+ * long sequences.  0 for invalid sizes. */
 size_t gdp_selective_scan_workspace_bytes(int64_t T, int64_t N, int64_t D, int64_t G, int64_t S);
 
 /* Device.  Selective state space scan over packed sequences, S states h per channel d:
@@ -578,7 +578,7 @@ size_t gdp_selective_scan_workspace_bytes(int64_t T, int64_t N, int64_t D, int64
  * States are float32, o is rounded once.  A non-finite input stays within its sequence,
  * and but for B and C within its channel.  No output may overlap an input or another output
  * (GDP_EALIAS).  Calls that share a workspace must be ordered.  Two runs on the same inputs
- * give the same bits.  Two to four launches on `stream`, no allocation: capturable. */
+ * give the same bits.  One to four launches on `stream`, no allocation: capturable. */
 int gdp_selective_scan(const gdp_tensor *u, const gdp_tensor *dt, const gdp_tensor *A, const gdp_tensor *B,
                        const gdp_tensor *C, const gdp_tensor *skip, const gdp_tensor *gate, const gdp_tensor *dt_bias,
                        int32_t dt_softplus, const gdp_tensor *cu_seqlens, const gdp_tensor *initial_state,
