@@ -22,16 +22,14 @@ template <typename T, int N> struct __attribute__((packed, aligned(sizeof(T)))) 
 template <typename T, int N, bool STREAMED = false>
 __device__ __forceinline__ Piece<T, N> load_piece(const T *row, int ch, int D) {
   if (ch + N <= D) {
-    if constexpr (STREAMED) {
-      typedef T vec __attribute__((ext_vector_type(N), aligned(sizeof(T))));
-      const vec v = __builtin_nontemporal_load((const vec *)(row + ch));
-      Piece<T, N> p;
+    // (as a vector: copies of the struct itself take the compiler more registers)
+    typedef T vec __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+    const vec *at = (const vec *)(row + ch);
+    const vec v = STREAMED ? __builtin_nontemporal_load(at) : *at;
+    Piece<T, N> p;
 #pragma unroll
-      for (int c = 0; c < N; ++c) p.v[c] = v[c];
-      return p;
-    } else {
-      return *(const Piece<T, N> *)(row + ch);
-    }
+    for (int c = 0; c < N; ++c) p.v[c] = v[c];
+    return p;
   }
   Piece<T, N> p;
 #pragma unroll
@@ -41,15 +39,12 @@ __device__ __forceinline__ Piece<T, N> load_piece(const T *row, int ch, int D) {
 template <typename T, int N, bool STREAMED = false>
 __device__ __forceinline__ void store_piece(T *row, int ch, int D, const Piece<T, N> &p) {
   if (ch + N <= D) {
-    if constexpr (STREAMED) {
-      typedef T vec __attribute__((ext_vector_type(N), aligned(sizeof(T))));
-      vec v;
+    typedef T vec __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+    vec v;
 #pragma unroll
-      for (int c = 0; c < N; ++c) v[c] = p.v[c];
-      __builtin_nontemporal_store(v, (vec *)(row + ch));
-    } else {
-      *(Piece<T, N> *)(row + ch) = p;
-    }
+    for (int c = 0; c < N; ++c) v[c] = p.v[c];
+    if (STREAMED) __builtin_nontemporal_store(v, (vec *)(row + ch));
+    else *(vec *)(row + ch) = v;
     return;
   }
 #pragma unroll

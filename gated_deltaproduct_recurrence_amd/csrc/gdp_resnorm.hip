@@ -114,14 +114,16 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_resnorm_kern
       if (a.z) zn.template load<STREAMED>((const T *)a.z + t * a.z_st, team.lane, lpg, a.D);
     }
   };
+  constexpr bool AHEAD = WIDE < 2;  // lanes of the widest teams have half the registers
   int64_t t = (int64_t)blockIdx.x * teams + tid / lpg;
-  fetch(t);
+  if (AHEAD) fetch(t);
   // (the loop's bound is the block's: its waves meet at the sums' barriers)
   for (int64_t tb = (int64_t)blockIdx.x * teams; tb < a.T; tb += step, t += step) {
+    if (!AHEAD) fetch(t);
     yv = yn;
     zv = zn;
     xv = xn;
-    fetch(t + step);
+    if (AHEAD) fetch(t + step);
     float v[E][VEC];
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -164,26 +166,34 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_resnorm_back
   load_weights<T, VEC, E>(wb, a.w_pre, a.w_type, team.lane, lpg, a.D);
   Row<T, VEC, E> yv{}, zv{}, nv{}, yn{}, zn{}, nn{};
   Row<X, VEC, E> xv{}, rv{}, xn{}, rn{};
+  // A token is loaded ahead, but the widest teams' lanes have half the registers; and in
+  // float32 the output gradients are loaded with the token's first sums (70 registers
+  // spill otherwise; in 16 bits, where none do, loading them late costs 2%).
+  constexpr bool AHEAD = WIDE < 2, LATE = sizeof(T) == 4;
+  auto fetch_outputs = [&](int64_t t) {
+    if (a.pre) nn.template load<STREAMED>((const T *)a.dn + t * a.dn_st, team.lane, lpg, a.D);
+    if (a.dr) rn.template load<STREAMED>((const X *)a.dr + t * a.dr_st, team.lane, lpg, a.D);
+  };
   auto fetch = [&](int64_t t) {
     if (t < a.T) {
       yn.template load<STREAMED>((const T *)a.y + t * a.y_st, team.lane, lpg, a.D);
-      if (a.pre) {  // r is needed for its norm alone
-        xn.template load<STREAMED>((const X *)a.x + t * a.x_st, team.lane, lpg, a.D);
-        nn.template load<STREAMED>((const T *)a.dn + t * a.dn_st, team.lane, lpg, a.D);
-      }
+      // r is needed for its norm alone
+      if (a.pre) xn.template load<STREAMED>((const X *)a.x + t * a.x_st, team.lane, lpg, a.D);
       if (a.z) zn.template load<STREAMED>((const T *)a.z + t * a.z_st, team.lane, lpg, a.D);
-      if (a.dr) rn.template load<STREAMED>((const X *)a.dr + t * a.dr_st, team.lane, lpg, a.D);
+      if (!LATE) fetch_outputs(t);
     }
   };
   int64_t t = (int64_t)blockIdx.x * teams + tid / lpg;
-  fetch(t);
+  if (AHEAD) fetch(t);
   for (int64_t tb = (int64_t)blockIdx.x * teams; tb < a.T; tb += step, t += step) {
+    if (!AHEAD) fetch(t);
+    if (LATE && t < a.T) fetch_outputs(t);
     yv = yn;
     zv = zn;
-    nv = nn;
     xv = xn;
+    nv = nn;
     rv = rn;
-    fetch(t + step);
+    if (AHEAD) fetch(t + step);
     float yhat[E][VEC], e_[E][VEC];  // e_: r, then e
 #pragma unroll
     for (int e = 0; e < E; ++e)
