@@ -14,14 +14,14 @@
 // time, out of the caches.  Groups that lie inside the chunk take no branch per row.
 //
 // What bounds it, measured on MI355X (a 1 GiB copy reaches 5.1 TB/s): the memory.
-// 131104 x 4096 bfloat16 in 68 sequences, 4 taps, SiLU: 399 us, 5.4 TB/s; 32768 x 2048:
-// 68 us, 3.9 TB/s, and its gradients 114 us, 3.5 TB/s (their sums another 8 us).
+// 131104 x 4096 bfloat16 in 68 sequences, 4 taps, SiLU: 392 us, 5.5 TB/s; 32768 x 2048:
+// 51 us, 5.3 TB/s, and its gradients 114 us, 3.5 TB/s (their sums another 8 us).
 //   Forward: 8 bytes of a row per lane, chunks of 16 rows, groups of 2.  On the first
-// shape 16 bytes per lane took 447 us (138 registers), chunks of 32 and 64 rows 410 and
-// 442, groups of 1 and 4 rows 508 and 506.  Loads and stores past the caches: 549 us where
+// shape 16 bytes per lane take 408 us and groups of 4 rows 545; with an earlier form of the
+// loads, where this took 399, chunks of 32 and 64 rows 410 and 442, groups of 1 row 508.  Loads and stores past the caches: 549 us where
 // those left to them took 663 (with an earlier form of the loop).
 //   Gradients: one channel per lane, chunks of up to 128 rows, groups of 4.  2 and 4 channels
-// per lane took 155 and 212 us (73 and 169 registers), chunks of 32, 64 and 128 rows 145,
+// per lane take 145 and 213 us, chunks of 32, 64 and 128 rows 145,
 // 124 and 114.
 
 #include <hip/hip_runtime.h>
