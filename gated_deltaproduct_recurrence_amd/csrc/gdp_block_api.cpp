@@ -43,6 +43,14 @@ int check_output(const gdp_tensor *t, const char *name, int64_t R, int64_t C, in
   return check_row_overlap(t, name);
 }
 
+// (before a channel count is held in 32 bits)
+int check_channels(int64_t D) {
+  if (D > BLOCK_MAX_CHANNELS)
+    return fail(GDP_EUNSUPPORTED, "more than %lld channels are not served (D=%lld)", (long long)BLOCK_MAX_CHANNELS,
+                (long long)D);
+  return GDP_OK;
+}
+
 int check_indices(const gdp_tensor *slots, int64_t N) {
   const int64_t s[1] = {N};
   if (!is_index(slots->dtype)) return fail(GDP_EINVAL, "state_indices must be int32 or int64");
@@ -74,13 +82,14 @@ int conv_args(const gdp_tensor *x, const gdp_tensor *weight, const gdp_tensor *b
   if (weight->ndim != 2) return fail(GDP_EINVAL, "weight must be [D, W]");
   const int64_t T = x->shape[0], D = x->shape[1], W = weight->shape[1];
   if (D < 1) return fail(GDP_EINVAL, "x needs at least one channel");
+  int rc;
+  if ((rc = check_channels(D))) return rc;
   if (!is_float(x->dtype)) return fail(GDP_EUNSUPPORTED, "x must be float32, bfloat16 or float16");
   if (W < 2 || W > CONV_MAX_TAPS)
     return fail(GDP_EUNSUPPORTED, "2 to %d taps are served, got %lld", CONV_MAX_TAPS, (long long)W);
   if (activation != GDP_ACT_NONE && activation != GDP_ACT_SILU && activation != GDP_ACT_SIGMOID)
     return fail(GDP_EINVAL, "unknown activation %d", activation);
   const int64_t ws[2] = {D, W}, bs[1] = {D};
-  int rc;
   if ((rc = check_rows(x, "x", T, D)) || (rc = check_param(weight, "weight", 2, ws, x->dtype))) return rc;
   if (present(bias)) {
     if ((rc = check_param(bias, "bias", 1, bs, x->dtype))) return rc;
@@ -245,6 +254,8 @@ int select_args(const gdp_tensor *u, const gdp_tensor *dt, const gdp_tensor *A, 
   if (B->ndim != 3) return fail(GDP_EINVAL, "B must be [T, G, S]");
   const int64_t T = u->shape[0], D = u->shape[1], S = A->shape[1], G = B->shape[1];
   if (D < 1) return fail(GDP_EINVAL, "u needs at least one channel");
+  int rc;
+  if ((rc = check_channels(D))) return rc;
   if (!is_float(u->dtype)) return fail(GDP_EUNSUPPORTED, "u must be float32, bfloat16 or float16");
   if (dt->dtype != GDP_F32 && dt->dtype != u->dtype) return fail(GDP_EUNSUPPORTED, "dt must be float32 or u's dtype");
   if (B->dtype != u->dtype || C->dtype != u->dtype) return fail(GDP_EUNSUPPORTED, "B and C must have u's dtype");
@@ -253,7 +264,6 @@ int select_args(const gdp_tensor *u, const gdp_tensor *dt, const gdp_tensor *A, 
   if (G < 1 || D % G != 0)
     return fail(GDP_EINVAL, "the %lld channels must be a multiple of the %lld groups of B and C", (long long)D, (long long)G);
   const int64_t as[2] = {D, S}, bs[3] = {T, G, S}, ds[1] = {D};
-  int rc;
   if ((rc = check_rows(u, "u", T, D)) || (rc = check_rows(dt, "dt", T, D)) ||
       (rc = check_packed(A, "A", 2, as, GDP_F32)) || (rc = check_shape(B, "B", 3, bs)) ||
       (rc = check_shape(C, "C", 3, bs)))

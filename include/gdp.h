@@ -483,7 +483,8 @@ int gdp_group_norm_backward(const gdp_tensor *x, const gdp_tensor *weight, const
 /* Device.  Short causal convolution over packed sequences, channel by channel:
  *     v_t = bias + sum_{j < W} weight[d, j] x_{t-W+1+j},   y_t = act(v_t),
  * the W - 1 rows before a sequence's first being its initial state (or zeros).
- *   x            [T, D]    f32, bf16 or f16; rows may be strided
+ *   x            [T, D]    f32, bf16 or f16; rows may be strided; D <= 2^24
+ *                          (GDP_EUNSUPPORTED otherwise)
  *   weight       [D, W]    f32 or x's dtype, contiguous; 2 <= W <= 8 (GDP_EUNSUPPORTED
  *                          otherwise)
  *   bias         [D]       weight's dtype, contiguous, or data == NULL for zeros
@@ -553,7 +554,8 @@ size_t gdp_selective_scan_workspace_bytes(int64_t T, int64_t N, int64_t D, int64
  *     h_t = exp(delta_t A) h_{t-1} + delta_t u_t B_t,
  *     o_t = (C_t . h_t + skip u_t) silu(gate_t),
  * from h = initial_state (or 0) in every sequence; without a gate the last factor is 1.
- *   u            [T, D]    f32, bf16 or f16; rows may be strided
+ *   u            [T, D]    f32, bf16 or f16; rows may be strided; D <= 2^24
+ *                          (GDP_EUNSUPPORTED otherwise)
  *   dt           [T, D]    f32 or u's dtype; rows may be strided
  *   A            [D, S]    f32, contiguous, negative (delta_t A > 0 is served while the
  *                          products of decays over 2048 rows stay finite in float32; what
