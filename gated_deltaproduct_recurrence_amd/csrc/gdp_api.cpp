@@ -405,7 +405,7 @@ static int prefill_impl(const gdp_tensor *q, const gdp_tensor *k, const gdp_tens
       return fail(GDP_EINVAL, "chunk_states has %lld rows; %lld needed", (long long)chunk_states->shape[0],
                   (long long)nt_cap);
   }
-  if (!gdp::prefill_supported(dt == GDP_BF16 ? gdp::IN_BF16 : gdp::IN_F32, (int)K, (int)V))
+  if (!gdp::prefill_supported(dt == GDP_BF16 ? gdp::IN_BF16 : gdp::IN_F32, K, V))
     return fail(GDP_EUNSUPPORTED, "head dims K=%lld V=%lld with %s inputs are not served", (long long)K,
                 (long long)V, dt == GDP_BF16 ? "bf16" : "f32");
 
@@ -715,8 +715,9 @@ int gdp_chunk_prefill_backward(const gdp_tensor *q, const gdp_tensor *k, const g
   const int64_t Hk = k->shape[1], Hv = v->shape[1], V = v->shape[2];
   const int64_t N = cu_seqlens->shape[0] - 1;
   if (N < 0 || Hqk < 1 || Hv < 1 || Hk < 1) return fail(GDP_EINVAL, "bad sizes");
+  if (N > INT32_MAX || Hv > INT32_MAX) return fail(GDP_EINVAL, "too many sequences or heads");
   if (Hv % Hqk != 0 || (Hk != Hqk && Hk != Hv)) return fail(GDP_EINVAL, "head counts: Hv a multiple of Hqk, Hk = Hqk or Hv");
-  if (!gdp::backward_supported((int)K, (int)V, n))
+  if (!gdp::backward_supported(K, V, n))
     return fail(GDP_EUNSUPPORTED, "backward needs K, V in {64, 128} and num_householder <= 5");
   const int32_t dt = q->dtype;
   if (dt != GDP_F32 && dt != GDP_BF16) return fail(GDP_EUNSUPPORTED, "q must be float32 or bfloat16");
@@ -920,7 +921,7 @@ int gdp_recurrent_decode(const gdp_tensor *q, const gdp_tensor *k, const gdp_ten
   for (const gdp_tensor *t : {q, k, v, g_log, beta, o})
     if (!nonneg_strides(t)) return fail(GDP_EINVAL, "negative strides are not supported");
   if (!contiguous(state_cache)) return fail(GDP_EINVAL, "state_cache must be contiguous");
-  if (!gdp::decode_supported((int)K, (int)V))
+  if (!gdp::decode_supported(K, V))
     return fail(GDP_EUNSUPPORTED, "head dims K=%lld V=%lld are not served", (long long)K, (long long)V);
   // the state cache is read and written; o is written: neither may overlap an input or the other
   Range ins[] = {range_of(q, "q"), range_of(k, "k"), range_of(v, "v"), range_of(g_log, "g_log"),

@@ -556,7 +556,7 @@ template <typename T, int K, int V> hipError_t launch_bwd(const BwdArgs &a, hipS
 
 }  // namespace
 
-bool backward_supported(int K, int V, int n) {
+bool backward_supported(int64_t K, int64_t V, int n) {
   return (K == 64 || K == 128) && (V == 64 || V == 128) && n >= 1 && n <= NMAX;
 }
 

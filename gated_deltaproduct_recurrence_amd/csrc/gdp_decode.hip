@@ -118,7 +118,7 @@ template <typename T, int K, int V> hipError_t launch(const DecodeArgs &a, hipSt
 
 }  // namespace
 
-bool decode_supported(int K, int V) { return (K == 64 || K == 128) && (V == 64 || V == 128); }
+bool decode_supported(int64_t K, int64_t V) { return (K == 64 || K == 128) && (V == 64 || V == 128); }
 
 hipError_t launch_decode(const DecodeArgs &a, int dtype, int K, int V, hipStream_t stream) {
   if (dtype == IN_BF16) {

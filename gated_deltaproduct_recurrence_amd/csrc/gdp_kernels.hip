@@ -2307,7 +2307,7 @@ bool fused_chosen(int dtype, int64_t N, int64_t Hv, int path) {
   return dtype == IN_BF16 && (path == PATH_FUSED || (path == PATH_AUTO && N * Hv >= 256));
 }
 
-bool prefill_supported(int dtype, int K, int V) {
+bool prefill_supported(int dtype, int64_t K, int64_t V) {
   const bool kv = (K == 64 || K == 128) && (V == 64 || V == 128);
   if (dtype == IN_BF16) return kv;
   if (dtype == IN_F32) return kv && K == 64;

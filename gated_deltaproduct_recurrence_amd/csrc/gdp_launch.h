@@ -99,7 +99,7 @@ struct DecodeArgs {
 // else the WY kernel + scan kernel pair.
 enum Path { PATH_AUTO = 0, PATH_FUSED = 1, PATH_SPLIT = 2, PATH_SEGMENTED = 3 };
 
-bool prefill_supported(int dtype, int K, int V);
+bool prefill_supported(int dtype, int64_t K, int64_t V);
 // Bytes of the WY-matrix buffer for `rows` expanded chunks and Hv heads.
 size_t wy_buffer_bytes(int dtype, int64_t rows, int64_t Hv);
 hipError_t launch_prefill(const PrefillArgs &a, int dtype, int K, int V, int path, hipStream_t stream);
@@ -171,7 +171,7 @@ struct BwdArgs {
   float *dbeta; int64_t db_st, db_sh;
   float *ds0;                               // [N, Hv, K, V] or null
 };
-bool backward_supported(int K, int V, int n);
+bool backward_supported(int64_t K, int64_t V, int n);
 
 // Chunked gradients on the matrix cores (gdp_bwd_chunk.hip): prep, reverse
 // state-gradient scan and per-chunk gradient kernels.  bf16 inputs; q, k, v and
@@ -282,7 +282,7 @@ hipError_t launch_combine(const CombineArgs &a, int K, int V, hipStream_t stream
 // launches the fused kernel regardless of the chain count (bf16 only)
 hipError_t launch_fused_prefill(const PrefillArgs &a, int K, int V, hipStream_t stream);
 
-bool decode_supported(int K, int V);
+bool decode_supported(int64_t K, int64_t V);
 hipError_t launch_decode(const DecodeArgs &a, int dtype, int K, int V, hipStream_t stream);
 
 }  // namespace gdp
