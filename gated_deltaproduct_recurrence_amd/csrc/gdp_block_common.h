@@ -10,6 +10,8 @@
 
 namespace gdp {
 
+template <bool B> struct Flag { static constexpr bool value = B; };
+
 __device__ __forceinline__ int uniform_of(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
 // N neighbouring elements at any element's alignment: the memory instructions take

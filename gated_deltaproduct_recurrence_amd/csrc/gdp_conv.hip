@@ -35,7 +35,6 @@ namespace gdp {
 namespace {
 
 constexpr int WAVES = 4, FORWARD_ROWS = 2, BACKWARD_ROWS = 4;  // rows: of a group, loaded a group ahead
-template <bool B> struct Flag { static constexpr bool value = B; };
 
 // Row t >= first - (W - 1) of a chunk's sequence: those before its first lie in the initial state.
 template <typename T, int W, int VEC>

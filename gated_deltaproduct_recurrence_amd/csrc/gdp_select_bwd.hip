@@ -444,9 +444,9 @@ gdp_select_backward_kernel(SelectArgs a, SelectGrid g, BackwardSpace b) {
         dskip = fmaf(gy, u, dskip);
         dbias += ddt;
         if (!live) continue;
-        ((UT *)a.du)[t * a.du_st + ch] = (UT)fmaf(tile.delta[r][lane], s1, skip * gy);
+        ((UT *)a.du)[t * a.du_st + ch] = (UT)fmaf(tile.delta[r][lane], s1, a.skip ? skip * gy : 0.f);
         ((DT *)a.ddt)[t * a.ddt_st + ch] = (DT)ddt;
-        if (gate) ((UT *)a.dz)[t * a.dz_st + ch] = (UT)(tile.zs[r][lane] * fmaf(skip, u, s3));
+        if (gate) ((UT *)a.dz)[t * a.dz_st + ch] = (UT)(tile.zs[r][lane] * (a.skip ? fmaf(skip, u, s3) : s3));
       }
     }
     if (k.index == 0 && a.ds0 && live) {

@@ -563,7 +563,7 @@ size_t gdp_selective_scan_workspace_bytes(int64_t T, int64_t N, int64_t D, int64
  *                          for 0); 1 <= S <= 32 (GDP_EUNSUPPORTED otherwise)
  *   B, C         [T, G, S] u's dtype, tokens and groups may be strided; channel d reads
  *                          group d / (D / G)
- *   skip, dt_bias [D]      f32, contiguous, or data == NULL for zeros
+ *   skip, dt_bias [D]      f32, contiguous, or data == NULL for none
  *   gate         [T, D]    u's dtype, rows may be strided, or data == NULL
  *   cu_seqlens   [N+1]     int32 or int64, contiguous
  *   initial_state [N, D, S]  f32 contiguous, or data == NULL for zeros
@@ -578,7 +578,8 @@ size_t gdp_selective_scan_workspace_bytes(int64_t T, int64_t N, int64_t D, int64
  *                          unspecified; what gdp_selective_scan_backward reads
  *   workspace    at least gdp_selective_scan_workspace_bytes(...), 256-byte aligned
  * States are float32, o is rounded once.  A non-finite input stays within its sequence,
- * and but for B and C within its channel.  No output may overlap an input or another output
+ * and but for B and C within its channel; an infinite state times a product of decays below
+ * 2^-126 may be NaN.  No output may overlap an input or another output
  * (GDP_EALIAS).  Calls that share a workspace must be ordered.  Two runs on the same inputs
  * give the same bits.  One to four launches on `stream`, no allocation: capturable. */
 int gdp_selective_scan(const gdp_tensor *u, const gdp_tensor *dt, const gdp_tensor *A, const gdp_tensor *B,
