@@ -238,48 +238,50 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
     // M rows of the recurrence
     auto run = [&](const auto &x) {
       constexpr int M = sizeof(x.u) / sizeof(UT);
-      float delta[M], w[M], y[M], s[M][2];
+      float delta[M], y[M];
       x.steps(delta, bias, a.softplus);
-      auto begin = [&](int r) {
-        const float u = (float)x.u[r];
-        w[r] = delta[r] * u;
-        s[r][0] = !ZEROS || a.skip ? skip * u : 0.f;
-        s[r][1] = 0.f;
-      };
-      // states n .. n + 3 of a row, all of them or (at least one) up to the last one
-      auto four = [&](auto all, int n, int r) {
+      // states n .. n + 3 of row r, all of them or (at least one) up to the last one
+      auto four = [&](auto all, int r, int n, float w, float (&s)[2]) {
         const float4 Bv = *(const float4 *)(mine + r * 2 * P + n), Cv = *(const float4 *)(mine + (r * 2 + 1) * P + n);
         const float B[4] = {Bv.x, Bv.y, Bv.z, Bv.w}, C[4] = {Cv.x, Cv.y, Cv.z, Cv.w};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float after = fmaf(__builtin_amdgcn_exp2f(delta[r] * A2[n + c]), h[n + c], w[r] * B[c]);
+          const float after = fmaf(__builtin_amdgcn_exp2f(delta[r] * A2[n + c]), h[n + c], w * B[c]);
           h[n + c] = decltype(all)::value || c == 0 || n + c < a.S ? after : 0.f;
-          s[r][c & 1] = fmaf(h[n + c], C[c], s[r][c & 1]);
+          s[c & 1] = fmaf(h[n + c], C[c], s[c & 1]);
         }
       };
-      if constexpr (ZEROS) {
+      if constexpr (!ZEROS) {
 #pragma unroll
-        for (int r = 0; r < M; ++r) begin(r);
+        for (int r = 0; r < M; ++r) {
+          const float u = (float)x.u[r], w = delta[r] * u;
+          float s[2] = {skip * u, 0.f};
+#pragma unroll
+          for (int n = 0; n < P; n += 4) four(Flag<true>(), r, n, w, s);
+          y[r] = s[0] + s[1];
+        }
+      } else {
+        float w[M], s[M][2];
+#pragma unroll
+        for (int r = 0; r < M; ++r) {
+          const float u = (float)x.u[r];
+          w[r] = delta[r] * u;
+          s[r][0] = a.skip ? skip * u : 0.f;
+          s[r][1] = 0.f;
+        }
 #pragma unroll
         for (int n = 0; n < P; n += 4) {
           if (n + 4 <= a.S) {
 #pragma unroll
-            for (int r = 0; r < M; ++r) four(Flag<true>(), n, r);
+            for (int r = 0; r < M; ++r) four(Flag<true>(), r, n, w[r], s[r]);
           } else if (n < a.S) {
 #pragma unroll
-            for (int r = 0; r < M; ++r) four(Flag<false>(), n, r);
+            for (int r = 0; r < M; ++r) four(Flag<false>(), r, n, w[r], s[r]);
           }
         }
-      } else {
 #pragma unroll
-        for (int r = 0; r < M; ++r) {
-          begin(r);
-#pragma unroll
-          for (int n = 0; n < P; n += 4) four(Flag<true>(), n, r);
-        }
+        for (int r = 0; r < M; ++r) y[r] = s[r][0] + s[r][1];
       }
-#pragma unroll
-      for (int r = 0; r < M; ++r) y[r] = s[r][0] + s[r][1];
       if (gate) {
 #pragma unroll
         for (int r = 0; r < M; ++r) y[r] *= act_of(GDP_ACT_SILU, (float)x.z[r]);
