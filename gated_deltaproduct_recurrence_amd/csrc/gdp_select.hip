@@ -167,14 +167,15 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_ends_kernel(SelectArgs 
     sum += part;
   }
   if (!p.live) return;
-  float *out = s.states + (int64_t)p.number * P * a.D + ch;
+  const int64_t slot = p.k.begin >> g.shift;
+  float *out = s.states + slot * P * a.D + ch;
 #pragma unroll
   for (int n = 0; n < P; ++n) out[(int64_t)n * a.D] = h[n];
-  s.sums[(int64_t)p.number * a.D + ch] = sum;
+  s.sums[slot * a.D + ch] = sum;
 }
 
-// The states entering the chunks, in place of those at their ends: a lane walks the chunks
-// of a sequence for one state of one channel.
+// The states behind the chunks that another follows, in place of those from 0: a lane walks
+// these chunks of a sequence for one state of one channel.
 template <int P>
 __global__ void __launch_bounds__(256) gdp_select_enter_kernel(SelectArgs a, SelectGrid g, SelectSpace s) {
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;  // n D + ch
@@ -183,27 +184,27 @@ __global__ void __launch_bounds__(256) gdp_select_enter_kernel(SelectArgs a, Sel
   const float A2 = n < a.S ? a.A[(int64_t)ch * a.S + n] * LOG2E_L : 0.f;
   for (int i = blockIdx.y; i < a.N; i += gridDim.y) {
     const int64_t first = bound_at(a.cu, a.cu_is64, i, a.T), len = bound_at(a.cu, a.cu_is64, i + 1, a.T) - first;
-    const int64_t chunks = (len + ((int64_t)1 << g.shift) - 1) >> g.shift;
-    if (chunks < 2) continue;
-    const int64_t step = (int64_t)P * a.D, number = (first >> g.shift) + i;
-    float *state = s.states + number * step + at;
-    const float *sum = s.sums + number * a.D + ch;
+    const int64_t full = ((len + ((int64_t)1 << g.shift) - 1) >> g.shift) - 1;  // chunks that another follows
+    if (full < 2) continue;
+    const int64_t step = (int64_t)P * a.D, slot = first >> g.shift;
+    float *state = s.states + slot * step + at;
+    const float *sum = s.sums + slot * a.D + ch;
     float h = *state;
     constexpr int AHEAD = 8;
-    for (int64_t c = 1; c < chunks; c += AHEAD) {
+    for (int64_t c = 1; c < full; c += AHEAD) {
       float end[AHEAD], d[AHEAD];
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
         end[j] = d[j] = 0.f;
-        if (c + j + 1 < chunks) {  // (behind the last chunk's entry nothing is needed)
+        if (c + j < full) {
           end[j] = state[(c + j) * step];
           d[j] = sum[(c + j) * a.D];
         }
       }
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
-        if (c + j < chunks) state[(c + j) * step] = h;
         h = fmaf(__builtin_amdgcn_exp2f(A2 * d[j]), h, end[j]);
+        if (c + j < full) state[(c + j) * step] = h;
       }
     }
   }
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
   float A2[P], h[P];
   load_rates<P>(A2, a, ch);
   if (k.index > 0) {
-    const float *enter = s.states + (int64_t)p.number * P * a.D + ch;
+    const float *enter = s.states + (int64_t)((k.begin >> g.shift) - 1) * P * a.D + ch;
 #pragma unroll
     for (int n = 0; n < P; ++n) h[n] = enter[(int64_t)n * a.D];
   } else {
@@ -388,14 +389,14 @@ bool select_served(int64_t T, int64_t N, int64_t D, int64_t G, int64_t S) {
 }
 
 size_t select_bytes(int64_t T, int64_t N, int64_t D, int64_t G, int64_t S) {
-  return select_space(nullptr, D, S, forward_grid(T, N, D, G).numbers).bytes;
+  return select_space(nullptr, D, S, forward_grid(T, N, D, G)).bytes;
 }
 
 hipError_t launch_select(const SelectArgs &a, int ut, int dt, hipStream_t stream) {
   const SelectGrid g = forward_grid(a.T, a.N, a.D, a.G);
   const int64_t jobs = g.numbers * g.blocks;
   if (jobs == 0 || a.N == 0) return hipSuccess;
-  SelectSpace s = select_space(a.ws, a.D, a.S, g.numbers);
+  SelectSpace s = select_space(a.ws, a.D, a.S, g);
   // one wave per workgroup while that leaves compute units without one: 812 rows of 512
   // channels take 40 us so and 44 with four, 32768 of 2048 take 495 and 462
   const int waves = jobs <= 1024 ? 1 : WAVES;

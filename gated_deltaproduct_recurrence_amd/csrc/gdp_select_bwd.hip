@@ -43,7 +43,7 @@ constexpr int R = SELECT_ROWS, HALF = R / 2;
 constexpr int OWN = 4;                       // states per wave
 
 struct BackwardSpace {
-  SelectSpace s;     // states: the gradients entering the chunks from behind
+  SelectSpace s;     // states: the gradients behind the chunks that another follows
   float *points;     // checkpoints of a call without them
   float *shares;     // [blocks, T, 2, padded S]: dB and dC over 64 channels
   float *sums;       // [numbers, waves OWN + 2, D]: dA, dskip, dbias over chunks
@@ -53,10 +53,10 @@ BackwardSpace backward_space(void *ws, int64_t T, int64_t N, int64_t D, int64_t 
                              bool with_points) {
   BackwardSpace b;
   const int64_t P = padded_states(S);
-  b.s = select_space(ws, D, S, g.numbers);
+  b.s = select_space(ws, D, S, g);
   size_t at = b.s.bytes;
   if (!with_points) {  // the forward pass's space comes first, in the same place
-    const size_t forward = select_space(ws, D, S, forward_grid(T, N, D, G).numbers).bytes;
+    const size_t forward = select_space(ws, D, S, forward_grid(T, N, D, G)).bytes;
     at = forward > at ? forward : at;
   }
   b.points = (float *)((uintptr_t)ws + at);
@@ -160,14 +160,16 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_starts_kernel(SelectArg
     run(one);
   }
   if (at >= per) return;
-  float *out = s.states + (int64_t)number * P * a.D + ch;
+  const int64_t slot = (k.begin >> g.shift) - 1;  // of the chunk before
+  float *out = s.states + slot * P * a.D + ch;
 #pragma unroll
   for (int n = 0; n < P; ++n) out[(int64_t)n * a.D] = e[n];
-  s.sums[(int64_t)number * a.D + ch] = sum;
+  s.sums[slot * a.D + ch] = sum;
 }
 
-// The gradients entering the chunks from behind, in place of those: a lane walks the
-// chunks of a sequence, last to first, for one state of one channel.
+// The gradients behind the chunks that another follows, in place of what the chunk behind
+// contributes: a lane walks these chunks of a sequence, last to first, for one state of one
+// channel.
 template <int P>
 __global__ void __launch_bounds__(256) gdp_select_behind_kernel(SelectArgs a, SelectGrid g, SelectSpace s) {
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;  // n D + ch
@@ -176,27 +178,27 @@ __global__ void __launch_bounds__(256) gdp_select_behind_kernel(SelectArgs a, Se
   const float A2 = n < a.S ? a.A[(int64_t)ch * a.S + n] * LOG2E_L : 0.f;
   for (int i = blockIdx.y; i < a.N; i += gridDim.y) {
     const int64_t first = bound_at(a.cu, a.cu_is64, i, a.T), len = bound_at(a.cu, a.cu_is64, i + 1, a.T) - first;
-    const int64_t chunks = (len + ((int64_t)1 << g.shift) - 1) >> g.shift;
-    if (chunks < 2) continue;
-    const int64_t step = (int64_t)P * a.D, number = (first >> g.shift) + i;
-    float *state = s.states + number * step + at;
-    const float *sum = s.sums + number * a.D + ch;
-    float e = state[(chunks - 1) * step];
+    const int64_t full = ((len + ((int64_t)1 << g.shift) - 1) >> g.shift) - 1;  // chunks that another follows
+    if (full < 2) continue;
+    const int64_t step = (int64_t)P * a.D, slot = first >> g.shift;
+    float *state = s.states + slot * step + at;
+    const float *sum = s.sums + slot * a.D + ch;
+    float e = state[(full - 1) * step];
     constexpr int AHEAD = 8;
-    for (int64_t c = chunks - 2; c >= 0; c -= AHEAD) {
+    for (int64_t c = full - 2; c >= 0; c -= AHEAD) {
       float own[AHEAD], d[AHEAD];
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
         own[j] = d[j] = 0.f;
-        if (c - j > 0) {  // (before chunk 0 nothing is needed)
+        if (c - j >= 0) {
           own[j] = state[(c - j) * step];
           d[j] = sum[(c - j) * a.D];
         }
       }
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
-        if (c - j >= 0) state[(c - j) * step] = e;
         e = fmaf(__builtin_amdgcn_exp2f(A2 * d[j]), e, own[j]);
+        if (c - j >= 0) state[(c - j) * step] = e;
       }
     }
   }
@@ -259,7 +261,7 @@ gdp_select_backward_kernel(SelectArgs a, SelectGrid g, BackwardSpace b) {
     const float bias = a.bias ? a.bias[ch] : 0.f;
     const bool gate = a.z != nullptr;
     if (k.end < k.last) {
-      const float *behind = b.s.states + ((int64_t)number * P + w * OWN) * a.D + ch;
+      const float *behind = b.s.states + ((int64_t)(k.begin >> g.shift) * P + w * OWN) * a.D + ch;
 #pragma unroll
       for (int n = 0; n < OWN; ++n) e[n] = live ? behind[(int64_t)n * a.D] : 0.f;
     } else if (a.dfinal) {

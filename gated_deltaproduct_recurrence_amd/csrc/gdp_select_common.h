@@ -16,7 +16,12 @@ inline int padded_states(int64_t S) { return S <= 4 ? 4 : (S <= 8 ? 8 : (S <= 16
 struct SelectGrid {
   int blocks, per_group, shift;  // channel blocks, those of one group, log2 of a chunk's rows
   int64_t numbers;               // of chunks
+  int64_t slots;                 // for what one chunk hands to another
 };
+// What chunks hand on stands in the place first row >> shift of the chunk before the boundary: such
+// a chunk is full and at least a row behind it lies in [0, T), so its place is its own and
+// below (T - 1) >> shift, however many sequences there are.
+__host__ __device__ inline int64_t hand_over_slots(int64_t T, int shift) { return T > 0 ? (T - 1) >> shift : 0; }
 inline SelectGrid select_grid(int64_t T, int64_t N, int64_t D, int64_t G, int64_t want, int least, int most) {
   SelectGrid g;
   g.per_group = (int)((D / G + 63) / 64);
@@ -24,6 +29,7 @@ inline SelectGrid select_grid(int64_t T, int64_t N, int64_t D, int64_t G, int64_
   g.shift = most;
   while (g.shift > least && (T >> g.shift) * g.blocks < want) --g.shift;
   g.numbers = chunk_numbers(T, N, g.shift);
+  g.slots = hand_over_slots(T, g.shift);
   return g;
 }
 
@@ -33,26 +39,26 @@ inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 // waves take them.  Few waves of uneven chunks leave compute units idle at the end otherwise.
 constexpr int64_t MOST_ORDERED = 1024;
 
-// The workspace's first part: the chunks' states [numbers, padded S, D], sums of steps
-// [numbers, D] and order.  (As numbers, not pointers: the sizes are asked for without a
+// The workspace's first part: the states [slots, padded S, D] and sums of steps [slots, D]
+// that chunks hand on, and the chunks' order.  (As numbers, not pointers: the sizes are asked for without a
 // workspace.)
 struct SelectSpace {
   float *states, *sums;
   int *order;  // [numbers], or null
   size_t bytes;
 };
-inline SelectSpace select_space(void *ws, int64_t D, int64_t S, int64_t numbers) {
+inline SelectSpace select_space(void *ws, int64_t D, int64_t S, const SelectGrid &g) {
   SelectSpace s;
   const uintptr_t p = (uintptr_t)ws;
   size_t at = 0;
   s.states = (float *)p;
-  at += round256((size_t)numbers * padded_states(S) * D * 4);
+  at += round256((size_t)g.slots * padded_states(S) * D * 4);
   s.sums = (float *)(p + at);
-  at += round256((size_t)numbers * D * 4);
+  at += round256((size_t)g.slots * D * 4);
   s.order = nullptr;
-  if (numbers <= MOST_ORDERED) {
+  if (g.numbers <= MOST_ORDERED) {
     s.order = (int *)(p + at);
-    at += round256((size_t)numbers * 4);
+    at += round256((size_t)g.numbers * 4);
   }
   s.bytes = at;
   return s;
@@ -165,6 +171,7 @@ inline SelectGrid forward_grid(int64_t T, int64_t N, int64_t D, int64_t G) {
   if (N * g.blocks >= 2048)
     while (g.shift < 11 && ((int64_t)1 << g.shift) * N < 2 * T) ++g.shift;
   g.numbers = chunk_numbers(T, N, g.shift);
+  g.slots = hand_over_slots(T, g.shift);
   return g;
 }
 // ... and those of the gradients: enough for 2048 workgroups

@@ -546,7 +546,8 @@ int gdp_short_conv_backward(const gdp_tensor *x, const gdp_tensor *weight, const
 #define GDP_SELECT_CHECKPOINT_ROWS 16
 
 /* Host-only.  Workspace bytes gdp_selective_scan needs: the states at the ends of pieces of
- * long sequences.  0 for invalid sizes. */
+ * long sequences, as many as the rows have, whatever N is.  0 for invalid sizes, and where
+ * nothing is needed. */
 size_t gdp_selective_scan_workspace_bytes(int64_t T, int64_t N, int64_t D, int64_t G, int64_t S);
 
 /* Device.  Selective state space scan over packed sequences, S states h per channel d:
