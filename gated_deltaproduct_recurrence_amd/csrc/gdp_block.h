@@ -44,7 +44,7 @@ hipError_t launch_conv_decode(const ConvArgs &a, int x_type, hipStream_t stream)
 hipError_t launch_conv_backward(const ConvArgs &a, int x_type, hipStream_t stream);
 
 // states per channel at most, and rows of a sequence per checkpoint
-constexpr int SELECT_MAX_STATES = 32, SELECT_ROWS = 16;
+constexpr int SELECT_MAX_STATES = 32, SELECT_SHIFT = 4, SELECT_ROWS = 1 << SELECT_SHIFT;
 
 struct SelectArgs {
   const void *u; int64_t u_st;          // [T, D] (decode: [N, D])

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "gdp.h"
+#include "gdp_chunks.h"
 #include "gdp_launch.h"
 #include "gdp_layer_common.h"
 
@@ -92,42 +93,17 @@ __device__ __forceinline__ float act_of(int act, float v, float *slope) {
   return s;
 }
 
-// A piece of one sequence: rows [begin, end) of sequence `seq`, whose rows are
-// [first, last).  Sequences are cut into chunks of 2^shift rows from their first
-// row on, so no chunk holds rows of two sequences.  Chunk c of sequence i has number
-//     (cu[i] >> shift) + i + c:
-// sequence i + 1 starts at least that many numbers later as sequence i has chunks, so
-// numbers are unique, rise with the rows, and lie below (T >> shift) + N; some name
-// no chunk.  An empty sequence has one chunk, without rows.
-struct Chunk {
-  int begin, end, first, last, seq, index;
-};
-// The chunk of a number, found by a whole wave (all 64 lanes) in steps of 64: false where
-// it names none.  Boundaries that do not rise give chunks that overlap or leave out rows, all
-// within [0, T) and [0, N).
+// The chunk of a number (gdp_chunks.h), found by a whole wave (all 64 lanes): false where it
+// names none.
 __device__ __forceinline__ bool find_chunk(Chunk *k, const void *cu, int is64, int T, int N, int shift, int number) {
   const int lane = threadIdx.x & 63;
-  int lo = 0, hi = N, step;
-  do {
-    step = (hi - lo + 63) >> 6;
+  const int seq = uniform_of(sequence_of(N, [&](int lo, int hi, int step) {
     const int i = lo + lane * step;
-    const bool at = i < hi && ((int)bound_at(cu, is64, i, T) >> shift) + i <= number;
-    const int c = __popcll(__ballot(at));
-    if (c == 0) return false;
-    lo = uniform_of(lo + (c - 1) * step);
-    hi = min(hi, lo + step);
-  } while (step > 1);
-  k->seq = lo;
-  k->first = uniform_of((int)bound_at(cu, is64, lo, T));
-  k->last = max(k->first, uniform_of((int)bound_at(cu, is64, lo + 1, T)));
-  k->index = number - ((k->first >> shift) + lo);
-  const int64_t begin = k->first + ((int64_t)k->index << shift);
-  if (k->index < 0 || (k->index > 0 && begin >= k->last)) return false;
-  k->begin = (int)begin;
-  k->end = min((int64_t)k->last, begin + ((int64_t)1 << shift));
-  return true;
+    return __popcll(__ballot(i < hi && chunk_number((int)bound_at(cu, is64, i, T), i, shift) <= number));
+  }));
+  if (seq < 0) return false;
+  const int first = uniform_of((int)bound_at(cu, is64, seq, T)), last = uniform_of((int)bound_at(cu, is64, seq + 1, T));
+  return chunk_of(k, number, shift, seq, first, last);
 }
-// numbers of chunks of 2^shift rows
-__host__ __device__ inline int64_t chunk_numbers(int64_t T, int64_t N, int shift) { return (T >> shift) + N; }
 
 }  // namespace gdp

@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "gdp_chunks.h"
+
 namespace gdp {
 
 typedef __bf16 bf16;
@@ -13,8 +15,7 @@ __device__ __forceinline__ int64_t index_at(const void *p, int is64, int64_t i) 
 
 // cu_seqlens[i] clamped to [0, T]
 __device__ __forceinline__ int64_t bound_at(const void *cu, int is64, int64_t i, int64_t T) {
-  const int64_t v = index_at(cu, is64, i);
-  return v < 0 ? 0 : (v > T ? T : v);
+  return clamp_bound(index_at(cu, is64, i), T);
 }
 
 // N neighbouring elements

@@ -59,11 +59,11 @@ __global__ void __launch_bounds__(256) gdp_select_order_kernel(SelectArgs a, int
     int lo = 0, hi = a.N;  // the last sequence whose numbers begin at or before it
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (((int)bound_at(a.cu, a.cu_is64, mid, a.T) >> shift) + mid <= number) lo = mid;
+      if (chunk_number((int)bound_at(a.cu, a.cu_is64, mid, a.T), mid, shift) <= number) lo = mid;
       else hi = mid;
     }
     const int first = (int)bound_at(a.cu, a.cu_is64, lo, a.T), last = (int)bound_at(a.cu, a.cu_is64, lo + 1, a.T);
-    const int64_t at = (int64_t)(number - (first >> shift) - lo) * ((int64_t)1 << shift);
+    const int64_t at = (int64_t)(number - chunk_number(first, lo, shift)) * ((int64_t)1 << shift);
     const int64_t left = at < 0 ? 0 : last - first - at;
     const int64_t rows = left < 0 ? 0 : (left < (int64_t)1 << shift ? left : (int64_t)1 << shift);
     cls[j] = 63 - (int)(rows * 63 >> shift);
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_ends_kernel(SelectArgs 
     sum += part;
   }
   if (!p.live) return;
-  const int64_t slot = p.k.begin >> g.shift;
+  const int64_t slot = slot_behind(p.k, g.shift);
   float *out = s.states + slot * P * a.D + ch;
 #pragma unroll
   for (int n = 0; n < P; ++n) out[(int64_t)n * a.D] = h[n];
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(256) gdp_select_enter_kernel(SelectArgs a, Sel
   const float A2 = n < a.S ? a.A[(int64_t)ch * a.S + n] * LOG2E_L : 0.f;
   for (int i = blockIdx.y; i < a.N; i += gridDim.y) {
     const int64_t first = bound_at(a.cu, a.cu_is64, i, a.T), len = bound_at(a.cu, a.cu_is64, i + 1, a.T) - first;
-    const int64_t full = ((len + ((int64_t)1 << g.shift) - 1) >> g.shift) - 1;  // chunks that another follows
+    const int64_t full = followed_chunks(len, g.shift);
     if (full < 2) continue;
     const int64_t step = (int64_t)P * a.D, slot = first >> g.shift;
     float *state = s.states + slot * step + at;
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
   float A2[P], h[P];
   load_rates<P>(A2, a, ch);
   if (k.index > 0) {
-    const float *enter = s.states + (int64_t)((k.begin >> g.shift) - 1) * P * a.D + ch;
+    const float *enter = s.states + slot_before(k, g.shift) * P * a.D + ch;
 #pragma unroll
     for (int n = 0; n < P; ++n) h[n] = enter[(int64_t)n * a.D];
   } else {
@@ -301,8 +301,7 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
       next_bc.load(a, p.group, k.begin, 1);
     }
     auto point = [&](int t) {  // before row t, the first of 16
-      const int64_t at = (k.first / SELECT_ROWS) + k.seq + (t - k.first) / SELECT_ROWS;
-      float *out = a.points + at * a.S * a.D + ch;
+      float *out = a.points + checkpoint_row(k.first, k.seq, t, SELECT_SHIFT) * a.S * a.D + ch;
 #pragma unroll
       for (int n = 0; n < P; ++n)
         if (n < a.S && p.live) out[(int64_t)n * a.D] = h[n];

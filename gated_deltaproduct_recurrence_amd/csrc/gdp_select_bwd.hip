@@ -60,7 +60,7 @@ BackwardSpace backward_space(void *ws, int64_t T, int64_t N, int64_t D, int64_t 
     at = forward > at ? forward : at;
   }
   b.points = (float *)((uintptr_t)ws + at);
-  if (!with_points) at += round256((size_t)chunk_numbers(T, N, 4) * S * D * 4);
+  if (!with_points) at += round256((size_t)chunk_numbers(T, N, SELECT_SHIFT) * S * D * 4);
   b.shares = (float *)((uintptr_t)ws + at);
   at += round256((size_t)g.blocks * T * 2 * P * 4);
   b.sums = (float *)((uintptr_t)ws + at);
@@ -68,8 +68,6 @@ BackwardSpace backward_space(void *ws, int64_t T, int64_t N, int64_t D, int64_t 
   b.bytes = at;
   return b;
 }
-static_assert(SELECT_ROWS == 16, "checkpoint numbers are chunk numbers of 2^4 rows");
-
 template <typename UT, typename DT, int M> struct Back {
   UT d_o[M], z[M];
   DT dt[M];
@@ -160,7 +158,7 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_starts_kernel(SelectArg
     run(one);
   }
   if (at >= per) return;
-  const int64_t slot = (k.begin >> g.shift) - 1;  // of the chunk before
+  const int64_t slot = slot_before(k, g.shift);
   float *out = s.states + slot * P * a.D + ch;
 #pragma unroll
   for (int n = 0; n < P; ++n) out[(int64_t)n * a.D] = e[n];
@@ -178,7 +176,7 @@ __global__ void __launch_bounds__(256) gdp_select_behind_kernel(SelectArgs a, Se
   const float A2 = n < a.S ? a.A[(int64_t)ch * a.S + n] * LOG2E_L : 0.f;
   for (int i = blockIdx.y; i < a.N; i += gridDim.y) {
     const int64_t first = bound_at(a.cu, a.cu_is64, i, a.T), len = bound_at(a.cu, a.cu_is64, i + 1, a.T) - first;
-    const int64_t full = ((len + ((int64_t)1 << g.shift) - 1) >> g.shift) - 1;  // chunks that another follows
+    const int64_t full = followed_chunks(len, g.shift);
     if (full < 2) continue;
     const int64_t step = (int64_t)P * a.D, slot = first >> g.shift;
     float *state = s.states + slot * step + at;
@@ -261,7 +259,7 @@ gdp_select_backward_kernel(SelectArgs a, SelectGrid g, BackwardSpace b) {
     const float bias = a.bias ? a.bias[ch] : 0.f;
     const bool gate = a.z != nullptr;
     if (k.end < k.last) {
-      const float *behind = b.s.states + ((int64_t)(k.begin >> g.shift) * P + w * OWN) * a.D + ch;
+      const float *behind = b.s.states + (slot_behind(k, g.shift) * P + w * OWN) * a.D + ch;
 #pragma unroll
       for (int n = 0; n < OWN; ++n) e[n] = live ? behind[(int64_t)n * a.D] : 0.f;
     } else if (a.dfinal) {
@@ -293,7 +291,7 @@ gdp_select_backward_kernel(SelectArgs a, SelectGrid g, BackwardSpace b) {
           if (gate) z_[i] = ((const UT *)a.z)[t * a.z_st + ch];
         }
       }
-      const int64_t row = (k.first / R) + k.seq + (t0 - k.first) / R;
+      const int64_t row = checkpoint_row(k.first, k.seq, t0, SELECT_SHIFT);
       const float *p = a.points + (row * a.S + w * OWN) * a.D + ch;
 #pragma unroll
       for (int n = 0; n < OWN; ++n)

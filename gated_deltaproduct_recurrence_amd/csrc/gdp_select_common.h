@@ -18,10 +18,6 @@ struct SelectGrid {
   int64_t numbers;               // of chunks
   int64_t slots;                 // for what one chunk hands to another
 };
-// What chunks hand on stands in the place first row >> shift of the chunk before the boundary: such
-// a chunk is full and at least a row behind it lies in [0, T), so its place is its own and
-// below (T - 1) >> shift, however many sequences there are.
-__host__ __device__ inline int64_t hand_over_slots(int64_t T, int shift) { return T > 0 ? (T - 1) >> shift : 0; }
 inline SelectGrid select_grid(int64_t T, int64_t N, int64_t D, int64_t G, int64_t want, int least, int most) {
   SelectGrid g;
   g.per_group = (int)((D / G + 63) / 64);
