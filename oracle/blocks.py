@@ -20,7 +20,10 @@ sigmoid and the activations count as in oracle/layers.py.
       four is off by at most (n / 4 + 4) U of itself; `join` is that number, 64 for
       chunks of up to 240 rows.  Its share of a state is counted row by row.
 Sums over tokens run in chunks of up to `chain` rows one after another, then over
-the chunks 64 apart and pairwise.  Everything is doubled for the second order.
+the chunks 64 apart and pairwise: a sum of n rows in that order is off by at most
+chain + (number of chunks) / 64 + 1 + 6 additions' U of the magnitudes' sum.  The rows per
+chunk follow from the sizes as the library's do (conv_chunk_rows, select_chunk_rows; the
+sizes of its workspaces tell them).  Everything is doubled for the second order.
 """
 import torch
 
@@ -35,6 +38,33 @@ def _cpu(t):
 
 def _edges(cu):
     return [int(c) for c in cu]
+
+
+def _chunk_rows(T, blocks, want, least, most):
+    """The longest chunks of 2^least to 2^most rows of which there are `want` in all channel blocks."""
+    shift = most
+    while shift > least and (T >> shift) * blocks < want:
+        shift -= 1
+    return 1 << shift
+
+
+def conv_chunk_rows(T, D):
+    """Rows per chunk of the convolution's gradients."""
+    return _chunk_rows(T, -(-D // 64), 4096, 4, 7)
+
+
+def select_chunk_rows(T, N, D, G):
+    """Rows per chunk of the scan, forward and in the gradients."""
+    blocks = G * -(-(D // G) // 64)
+    rows = _chunk_rows(T, blocks, 4096, 4, 11)
+    if N * blocks >= 2048:
+        while rows < 2048 and rows * N < 2 * T:
+            rows *= 2
+    return rows, _chunk_rows(T, blocks, 2048, 6, 11)
+
+
+# the residual norm's gradients: workgroups at most, each with its own partial sums
+NORM_WORKGROUPS = 512
 
 
 # ------------------------------------------------------------ short convolution
@@ -86,8 +116,8 @@ def conv(x, weight, cu, bias=None, activation=None, s0=None, d_y=None, d_final=N
         erows = 2 * (erows + (W + 2) * U * mrows)
         res["ds0"][i], res["ds0_bound"][i] = drows[:W - 1], erows[:W - 1]
         res["dx"][lo:lo + n], res["dx_bound"][lo:lo + n] = drows[W - 1:], erows[W - 1:]
-    # chunks of at least 16 and at most 64 rows, their sums 64 apart, then pairwise
-    chain = (64 + (T / 16 + N) / 64 + 8) * U
+    chunk = conv_chunk_rows(T, D)
+    chain = (chunk + (T / chunk + N) / 64 + 8) * U
     res["dweight_bound"] = 2 * (res["dweight_bound"] + chain * mag_w)
     res["dbias_bound"] = 2 * (res["dbias_bound"] + chain * mag_b)
     return res
@@ -125,6 +155,8 @@ def select(u, dt, A, B, C, cu, skip=None, gate=None, dt_bias=None, dt_softplus=F
     (T, D), S, G = u.shape, A.shape[1], B.shape[1]
     edges = _edges(cu)
     N = len(edges) - 1
+    rows, rows_back = select_chunk_rows(T, N, D, G)
+    assert max(rows, rows_back) / 4 + 4 <= join and rows_back <= chain, "the bounds are of shorter chunks"
     per = D // G
     wide = lambda t: t.repeat_interleave(per, 1)  # noqa: E731  [rows, G, S] -> [rows, D, S]
     narrow = lambda t: t.unflatten(1, (G, per)).sum(2)  # noqa: E731
@@ -277,8 +309,9 @@ def residual_norm(x, y, post_weight=None, pre_weight=None, gate=None, activation
         res["n"], res["n_bound"] = rhat * wb, 2 * (erh * wb.abs() + 2 * U * (rhat * wb).abs())
     if d_r is None and d_n is None:
         return res
-    # a workgroup's rows one after another, then its teams, the workgroups 64 apart and pairwise
-    rows = (T / 1024 + 1 + 256 + 1024 / 64 + 8) * U
+    # a team's rows one after another, then up to 256 teams of a workgroup, then the workgroups' sums (of wide
+    # rows two teams' each) 64 apart and pairwise
+    rows = (T / NORM_WORKGROUPS + 1 + 256 + 2 * NORM_WORKGROUPS / 64 + 8) * U
     e = torch.zeros_like(x) if d_r is None else d_r
     ee = torch.zeros_like(x)
     if pre_norm:
