@@ -14,15 +14,15 @@
 // time, out of the caches.  Groups that lie inside the chunk take no branch per row.
 //
 // What bounds it, measured on MI355X (a 1 GiB copy reaches 5.1 TB/s): the memory.
-// 131104 x 4096 bfloat16 in 68 sequences, 4 taps, SiLU: 392 us, 5.5 TB/s; 32768 x 2048:
-// 51 us, 5.3 TB/s, and its gradients 114 us, 3.5 TB/s (their sums another 8 us).
-//   Forward: 8 bytes of a row per lane, chunks of 16 rows, groups of 2.  On the first
-// shape 16 bytes per lane take 408 us and groups of 4 rows 545; with an earlier form of the
-// loads, where this took 399, chunks of 32 and 64 rows 410 and 442, groups of 1 row 508.  Loads and stores past the caches: 549 us where
-// those left to them took 663 (with an earlier form of the loop).
-//   Gradients: one channel per lane, chunks of up to 128 rows, groups of 4.  2 and 4 channels
-// per lane take 145 and 213 us, chunks of 32, 64 and 128 rows 145,
-// 124 and 114.
+// 131104 x 4096 bfloat16 in 68 sequences, 4 taps, SiLU: 393 us, 5.5 TB/s; 32768 x 2048:
+// 51 us, 5.3 TB/s.
+//   Forward: 8 bytes of a row per lane, chunks of 16 rows, groups of 2.  On the first shape
+// 16 bytes per lane take 405 us, chunks of 32 and 64 rows 409 and 441, groups of 1 and 4 rows
+// 524 and 544, and loads and stores left to the caches 407.
+//   Gradients of the second shape: 114 us, 3.5 TB/s (their sums another 7 us), the vector units
+// busy 66% of the time, 6900 of 8192 waves resident: neither they nor the memory are full.
+// One channel per lane, chunks of up to 128 rows, groups of 4.  2 and 4 channels per lane
+// take 141 and 211 us, chunks of up to 32 and 64 rows 135 and 120.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -359,8 +359,10 @@ constexpr int FORWARD_VEC = 8, BACKWARD_VEC = 1;  // bytes per lane; channels pe
 
 }  // namespace
 
-// A launch holds less than 2^32 threads: per block of at least 256 channels a wave for
-// 16 rows, for a sequence, and in the gradients for 16 rows that may be uncovered.
+// A launch holds less than 2^32 threads: in the gradients, per block of 64 channels, a wave for
+// 16 rows, another for 16 rows that may be uncovered, and one for a sequence.  The forward pass has
+// one for 8 rows and for a sequence, per wider block; the decode step 256 threads per entry and
+// 1024 channels.
 bool conv_served(int64_t T, int64_t N, int64_t D) {
   if (T > BLOCK_MAX_ROWS || N > BLOCK_MAX_SEQS || D > BLOCK_MAX_CHANNELS) return false;
   return ((T >> 3) + 1 + N) * blocks_of(D, BACKWARD_VEC) < ((int64_t)1 << 32) / 64 - WAVES &&

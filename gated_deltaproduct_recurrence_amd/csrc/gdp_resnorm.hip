@@ -19,14 +19,16 @@
 // next token are loaded before the current one is computed.
 //
 // What bounds it, measured on MI355X (a 1 GiB copy reaches 5.1 TB/s): the memory.
-// 65536 x 4096 bfloat16 without a gate: 375 us, 5.7 TB/s; 8195 x 4096 float16 with a gate
-// and a float32 stream: 88 us, 5.4 TB/s, and its gradients 181 us, 4.1 TB/s, at 241 registers
+// 65536 x 4096 bfloat16 without a gate: 374 us, 5.7 TB/s; 8195 x 4096 float16 with a gate
+// and a float32 stream: 89 us, 5.3 TB/s, and its gradients 174 us, 4.2 TB/s, at 241 registers
 // and two waves per SIMD with four sums over the token between barriers.
-//   Loads and stores past the caches where the operands exceed the memory-side one: 582 us on
-// the first shape without.  Grid: 1024 workgroups forward, 512 in the gradients; 768, 1536, 2048
-// and 4096 forward: 472, 459, 400 and 413 us, half and twice the workgroups in the training
-// step 380 and 314 us instead of 285.  8 values per lane and twice the waves: 457 us, 307.
-// Gradients of more than 8192 channels keep part of a token outside the registers.
+//   Loads and stores past the caches where the operands exceed the memory-side one: 392 us on
+// the first shape without, where this takes 372.  Grid: 1024 workgroups forward, 512 in the
+// gradients; 768, 1536, 2048 and 4096 forward: 421, 440, 378 and 378 us, half and twice the
+// workgroups of the gradients in the training step 369 and 299 us instead of 271.
+//   Gradients of more than 8192 channels keep part of a token outside the registers and are
+// slow: 4096 tokens of 8192, 12288 and 16384 channels, bfloat16 with a gate, take 194, 930 and
+// 1024 us (2.8, 0.9 and 1.0 TB/s).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -18,16 +18,15 @@
 // sequences of one chunk in neither.  Uneven chunks are handed out longest first.
 //
 // Measured on MI355X, 16 states, bfloat16 with a gate.  An exponential takes two issue slots
-// and everything else one (counters), so a row of 64 channels has 138 slots in the main kernel
-// and 104 in the one before it; the vector units are busy 93% of the time in both on 32768 x 2048
-// in one sequence (277 + 207 us, the call 444 us).  33824 x 4096 in 68 sequences of 1 to 1024
-// rows: 547 us; 812 x 512 in 4: 25 us, latency of three launches.
-//   B and C as scalar operands missed the scalar cache row by row: 575 us on the first shape,
-// and a kernel before that laid them out as floats cost every call 3 to 7 us.
-//   Without the order by length, and with chunks for 4096 waves, the second took 1036 us.
-//   delta u B added by a matrix instruction (one for four states) saves 12 slots per row
-// and was no faster: 466 us and 587.
-//   4096 waves wanted; 2048 and 8192: 496 and 458 us on the first shape.
+// and everything else one (counters), so a row of 64 channels has 140 slots in the main kernel
+// and 104 in the one before it; the vector units are busy 94% of the time in both on 32768 x 2048
+// in one sequence (254 + 185 us and 18 for the walk between, the call 452).  33824 x 4096 in 68
+// sequences of 1 to 1024 rows: 549 us; 812 x 512 in 4: 25 us, latency of three launches.
+// (A process's first calls take a quarter longer, until the clocks have risen.)
+//   4096 waves wanted; 2048 and 8192: 482 and 466 us on the first shape instead of 450.
+//   Of forms that are no longer there: B and C as scalar operands missed the scalar cache row by
+// row (571 us on the first shape, 456 out of LDS); delta u B added by a matrix instruction (one
+// for four states) saved 12 slots per row and was slower (466 instead of 456).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -337,8 +336,8 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
 
 // One token: a stream over the states that are named, four states per lane.  The
 // workgroups walk the channels of an entry before the next entry, so a state is read from end
-// to end: 256 entries of 4096 channels of 16 states take 34 us (4.1 TB/s), and 40 with the
-// entries walked first.  Two entries per lane gain 2%, four lose 30%.
+// to end: 256 entries of 4096 channels of 16 states take 32 us (4.3 TB/s).  When this took 34, the
+// entries walked first took 40, two entries per lane 33 and four 44.
 template <typename UT, typename DT, int P>
 __global__ void __launch_bounds__(256) gdp_select_decode_kernel(SelectArgs a, int blocks) {
   constexpr int LANES = P / 4;  // of one channel
@@ -397,7 +396,7 @@ hipError_t launch_select(const SelectArgs &a, int ut, int dt, hipStream_t stream
   if (jobs == 0 || a.N == 0) return hipSuccess;
   SelectSpace s = select_space(a.ws, a.D, a.S, g);
   // one wave per workgroup while that leaves compute units without one: 812 rows of 512
-  // channels take 40 us so and 44 with four, 32768 of 2048 take 495 and 462
+  // channels take 26.2 us so and 26.8 with four, 32768 of 2048 take 483 and 450
   const int waves = jobs <= 1024 ? 1 : WAVES;
   // (the chunks of one sequence stand in order, and few waves all run at once)
   if (a.N == 1 || waves == 1) s.order = nullptr;

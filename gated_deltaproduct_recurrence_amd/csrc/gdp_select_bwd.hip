@@ -21,11 +21,12 @@
 // The time axis is cut into chunks as in the forward pass; the gradients that enter them
 // from behind come from two kernels before.
 //
-// Measured on MI355X, 8192 x 2048 in 4 sequences, 16 states, bfloat16 with a gate: 250 us, the
-// vector units busy 78% of the time (the kernels before it 70 and 7 us, the sums 20), at
-// 250 registers and two waves per SIMD.  With B and C as scalars, a barrier more and no loads
-// ahead it took 380 us.  1024 and 4096 workgroups wanted in place of 2048
-// cost the training step 9% and 3%, before B and C came out of LDS.
+// Measured on MI355X, 8192 x 2048 in 4 sequences, 16 states, bfloat16 with a gate: 230 us, the
+// vector units busy 77% of the time (the kernels before it 62 and 7 us, the sums 20), at
+// 250 registers and two waves per SIMD.  1024 and 4096 workgroups wanted in place of 2048:
+// the training step takes 518 and 463 us instead of 457.
+//   With 4, 8, 24 and 32 states 168, 268, 443 and 445 us: up to 8 states a wave holds 8 or 16 rows of
+// a block and loads none ahead, up to 4 a workgroup is one wave, from 17 on some registers spill.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
