@@ -51,12 +51,6 @@ int check_channels(int64_t D) {
   return GDP_OK;
 }
 
-int check_indices(const gdp_tensor *slots, int64_t N) {
-  const int64_t s[1] = {N};
-  if (!is_index(slots->dtype)) return fail(GDP_EINVAL, "state_indices must be int32 or int64");
-  return check_shape(slots, "state_indices", 1, s);
-}
-
 // GDP_DEBUG_VALIDATE: the device checks of cu_seqlens and the slots
 int validate(const void *cu, int cu_is64, int64_t N, int64_t T, const void *slots, int slots_is64, int64_t num_slots,
              void *stream) {

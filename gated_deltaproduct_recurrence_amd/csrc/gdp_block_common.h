@@ -66,12 +66,6 @@ template <typename T> __device__ __forceinline__ float param_at(const void *p, i
   return type == EL_F32 ? ((const float *)p)[i] : (float)((const T *)p)[i];
 }
 
-// s = sigmoid(v): the hardware's exponential and reciprocal, each good to one step;
-// the product before them is rounded, which adds |v| 2^-24 relative to exp(-v).  The
-// reciprocal of an infinite sum is 0.
-__device__ __forceinline__ float sigmoid_of(float v) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -LOG2E_L));
-}
 __device__ __forceinline__ float act_of(int act, float v) {
   if (act == GDP_ACT_NONE) return v;
   const float s = sigmoid_of(v);

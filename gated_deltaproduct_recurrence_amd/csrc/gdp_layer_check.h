@@ -46,11 +46,15 @@ inline int check_cu(const gdp_tensor *cu) {
   return GDP_OK;
 }
 
-inline int check_slots(const gdp_tensor *cache, const gdp_tensor *slots, int64_t N, int64_t D) {
-  if (int rc = check_states(cache, "state_cache", -1, D)) return rc;
+inline int check_indices(const gdp_tensor *slots, int64_t N) {
   const int64_t s[1] = {N};
   if (!is_index(slots->dtype)) return fail(GDP_EINVAL, "state_indices must be int32 or int64");
   return check_shape(slots, "state_indices", 1, s);
+}
+
+inline int check_slots(const gdp_tensor *cache, const gdp_tensor *slots, int64_t N, int64_t D) {
+  if (int rc = check_states(cache, "state_cache", -1, D)) return rc;
+  return check_indices(slots, N);
 }
 
 // No output overlaps an input or another output.

@@ -44,6 +44,13 @@ constexpr float LOG2E_L = 1.4426950408889634f;
 // decays below 0.4 otherwise.
 __device__ __forceinline__ float decay(float g) { return __builtin_amdgcn_exp2f(g * LOG2E_L); }
 
+// s = sigmoid(v): the hardware's exponential and reciprocal, each good to one step;
+// the product before them is rounded, which adds |v| 2^-24 relative to exp(-v).  The
+// reciprocal of an infinite sum is 0.
+__device__ __forceinline__ float sigmoid_of(float v) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -LOG2E_L));
+}
+
 // 1 - exp(g): the Taylor polynomial of degree 8 for |g| < 1/2 (its first omitted
 // term is g^9 / 9!, below 2^-26 of the result there), else the difference, whose
 // rounding is 2^-25 of a value above 0.39.  `a` is decay(g).

@@ -40,12 +40,6 @@ namespace {
 
 constexpr int MAX_VALUES = 16;  // values a lane holds of one group
 
-// s = sigmoid(v): the hardware's exponential and reciprocal, each good to one step;
-// the product before them is rounded, which adds |v| 2^-24 relative to exp(-v)
-__device__ __forceinline__ float sigmoid(float v) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(v * -LOG2E_L));
-}
-
 // E pieces of one (token, group)
 template <typename T, int VEC, int E> struct Values {
   Pack<T, VEC> p[E];
@@ -169,14 +163,14 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_norm_kernel(
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
           const float v = (float)zv.p[e].v[c];
-          n[e][c] *= a.act == GDP_ACT_NONE ? v : (a.act == GDP_ACT_SILU ? v * sigmoid(v) : sigmoid(v));
+          n[e][c] *= a.act == GDP_ACT_NONE ? v : (a.act == GDP_ACT_SILU ? v * sigmoid_of(v) : sigmoid_of(v));
         }
     } else if (a.act != GDP_ACT_NONE) {
 #pragma unroll
       for (int e = 0; e < E; ++e)
 #pragma unroll
         for (int c = 0; c < VEC; ++c) {
-          const float s = sigmoid(n[e][c]);
+          const float s = sigmoid_of(n[e][c]);
           n[e][c] = a.act == GDP_ACT_SILU ? n[e][c] * s : s;
         }
     }
@@ -227,7 +221,7 @@ __global__ void __launch_bounds__(WIDE == 0 ? 256 : 512 * WIDE) gdp_norm_backwar
         const float v = a.z ? (float)zv.p[e].v[c] : n;
         float f = v, df = 1.f;
         if (a.act != GDP_ACT_NONE) {
-          const float s = sigmoid(v);
+          const float s = sigmoid_of(v);
           if (a.act == GDP_ACT_SILU) {
             f = v * s;
             df = fmaf(f, 1.f - s, s);  // s (1 + v (1 - s))
