@@ -211,8 +211,8 @@ __global__ void __launch_bounds__(256) gdp_select_enter_kernel(SelectArgs a, Sel
 
 // ZEROS: there is no skip, or there are fewer states than P.  The zeros in their place times an
 // infinite input would be NaN, so they are selected, not multiplied, and groups of four states
-// behind the last one left out.  Otherwise that would cost 2 to 4%: 8192 x 2048 in 4 sequences
-// take 88, 126 and 212 us with 8, 16 and 32 states, and 91, 129 and 221 that way.
+// behind the last one left out.  Otherwise that would cost 1 to 3%: 8192 x 2048 in 4 sequences
+// take 69, 87, 125 and 210 us with 4, 8, 16 and 32 states, and 71, 88, 128 and 214 that way.
 template <typename UT, typename DT, int P, bool ZEROS>
 __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, SelectGrid g, SelectSpace s,
                                                                 int64_t jobs) {
@@ -271,7 +271,8 @@ __global__ void __launch_bounds__(64 * WAVES) gdp_select_kernel(SelectArgs a, Se
         }
 #pragma unroll
         for (int n = 0; n < P; n += 4) {
-          if (n + 4 <= a.S) {
+          // (with half of the P states or fewer, the next smaller P were taken)
+          if ((P > 4 && n < P / 2) || n + 4 <= a.S) {
 #pragma unroll
             for (int r = 0; r < M; ++r) four(Flag<true>(), r, n, w[r], s[r]);
           } else if (n < a.S) {
