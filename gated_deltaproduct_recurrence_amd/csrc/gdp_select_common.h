@@ -38,8 +38,8 @@ inline size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 constexpr int64_t MOST_ORDERED = 1024;
 
 // The workspace's first part: the states [slots, padded S, D] and sums of steps [slots, D]
-// that chunks hand on, and the chunks' order.  (As numbers, not pointers: the sizes are asked for without a
-// workspace.)
+// that chunks hand on, and the chunks' order.  (As numbers, not pointers: the sizes are
+// asked for without a workspace.)
 struct SelectSpace {
   float *states, *sums;
   int *order;  // [numbers], or null
